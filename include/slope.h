@@ -299,6 +299,84 @@ int slope_bwd_dw_masked_noalloc(const uint16_t *dY, const uint16_t *X, const uin
                                 int64_t in, int64_t out, uint16_t *dW_vals, void *stream);
 
 /*
+ * Root-mean-square norm of the tokens entering a linear, with the residual
+ * stream's addition (no counterpart in the pages: it is the step before the
+ * layer's products in a decoder block).  For each token row, D values:
+ *     h = bf16(X + res)  (or X where res is NULL),  rstd = (mean h^2 + eps)^(-1/2),
+ *     Y = bf16(h rstd w),
+ *     Q = round(127 p / max|p|), ties to even, with p = h w (exact in binary32),
+ *     qscale = rstd max|p| / 127,  so that Q qscale stands for h rstd w in int8.
+ * X, res, H, Y [T x D] bf16; w [D] bf16; Q [T x D] int8 in [-127, 127];
+ * qscale, rstd [T] fp32.  H (the residual stream for the next block; only
+ * with res), Y, rstd (for slope_rmsnorm_bwd) and Q with qscale may each be
+ * NULL; one of Y and Q is required.  Q is decided exactly: it depends on h
+ * and w alone, not on the rounding of rstd.
+ * A row of zeros gives Q = 0 with qscale = 0.  A row in which some |h w| is
+ * not finite in binary32 gives Q = 0 with qscale = NaN, so that
+ * slope_fwd_q8's outputs for that token are NaN; its Y follows IEEE
+ * arithmetic.  Squares that overflow binary32 are summed scaled.
+ * D a multiple of 8 up to 32768 (SLOPE_ERR_SHAPE), T >= 1, eps > 0 and
+ * finite (SLOPE_ERR_ARG).  H and Y may be the buffers of X or res (the call
+ * may run in place).  One launch, no workspace; bit-reproducible.
+ */
+int slope_rmsnorm(const uint16_t *X, const uint16_t *res, const uint16_t *w, int64_t T, int64_t D, float eps, uint16_t *H,
+                  uint16_t *Y, int8_t *Q, float *qscale, float *rstd, void *stream);
+
+/*
+ * Gradients of slope_rmsnorm's Y (no counterpart in the pages).  With H the
+ * normalised input (slope_rmsnorm's H, or X without a residual), rstd as it
+ * stored it, n = H rstd and g = dY w:
+ *     dH = bf16(rstd (g - n mean(g n)) + dres),   dw = sum over tokens of dY n.
+ * dY, H, dres, dH [T x D] bf16 (dres, the gradient that reaches h along the
+ * residual stream, may be NULL); w [D] bf16; rstd [T], dw [D] fp32
+ * (overwritten).  dH is the gradient of both X and res.  dH may be the buffer
+ * of dY, H or dres.  ws: scratch of at least slope_rmsnorm_bwd_ws(T, D)
+ * floats on the device, the caller's (so calls with their own ws may
+ * overlap); less is SLOPE_ERR_SHAPE.  Its contents do not matter before and
+ * mean nothing after.  Sizes as slope_rmsnorm.  Two launches; sums in a fixed
+ * order, bit-reproducible.
+ */
+int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, const float *rstd, const uint16_t *dres,
+                      int64_t T, int64_t D, uint16_t *dH, float *dw, float *ws, int64_t ws_floats, void *stream);
+
+/*
+ * Floats of scratch slope_rmsnorm_bwd needs for these sizes (host only, no
+ * device call; no counterpart in the pages).  Sizes as slope_rmsnorm.
+ */
+int slope_rmsnorm_bwd_ws(int64_t T, int64_t D, int64_t *floats);
+
+/*
+ * Int8 quantisation of rows with one scale per row (no counterpart in the
+ * pages): A [rows x K] bf16 -> Q [rows x K] int8 = round(127 a / max|a|),
+ * ties to even, decided exactly, and scale [rows] fp32 = max|a| / 127.
+ * Applied to the kept values of slope_prune24 (vals [out x in/2]) it gives
+ * slope_fwd_q8's weights with one scale per output channel; the codes stay as
+ * they are.  Applied to tokens it gives its tokens where no slope_rmsnorm
+ * made them.  A row of zeros gives Q = 0, scale = 0; a row with a NaN or an
+ * infinity gives Q = 0, scale = NaN.  K a multiple of 8 up to 65536
+ * (SLOPE_ERR_SHAPE), rows >= 1.  One launch, no workspace.
+ */
+int slope_quant_rows(const uint16_t *A, int64_t rows, int64_t K, int8_t *Q, float *scale, void *stream);
+
+/*
+ * Sparse forward in int8 [S2A][S2B][RI] (the pages' inference product, with
+ * both operands quantised; they give no int8 form):
+ *     Y[t][o] = bf16(xscale[t] wscale[o] sum_k Xq[t][k] Wq[o][k] + sum_j XL[t][j] R[j][o])
+ * Xq [T x in] int8 with xscale [T] fp32 (slope_rmsnorm or slope_quant_rows);
+ * Wq 2:4-compressed: vals_q [out x in/2] int8 with wscale [out] fp32
+ * (slope_quant_rows of slope_prune24's vals) and slope_prune24's meta
+ * [out x in/16]; XL [T x r], R [r x out] bf16 as in slope_fwd (r = 0: no
+ * adapter, both may be NULL); Y [T x out] bf16.  The int8 sums are exact in
+ * 32-bit integers (so in is at most 131072, SLOPE_ERR_SHAPE), the adapter's
+ * are fp32, and the two are joined and rounded once.  A NaN or infinite scale
+ * reaches every output of its token or channel.  One launch and no workspace:
+ * calls may overlap on any streams; bit-reproducible.
+ */
+int slope_fwd_q8(const int8_t *Xq, const float *xscale, const int8_t *vals_q, const float *wscale, const uint16_t *meta,
+                 const uint16_t *XL, const uint16_t *R, int64_t T, int64_t in, int64_t out, int64_t r, uint16_t *Y,
+                 void *stream);
+
+/*
  * Wait for `stream`, then read and clear the current device's error word:
  * returns SLOPE_OK, SLOPE_ERR_NONFINITE, SLOPE_ERR_TIMEOUT, SLOPE_ERR_BOUNDS
  * (debug build) or SLOPE_ERR_CUDA.

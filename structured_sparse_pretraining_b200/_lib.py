@@ -32,6 +32,11 @@ SIGNATURES = {
     "slope_bwd_dw_masked": (_int, [_p, _p, _p, _i64, _i64, _i64, _p, _p]),
     "slope_bwd_dw_masked_noalloc": (_int, [_p, _p, _p, _i64, _i64, _i64, _p, _p]),
     "slope_bwd_dw_fused": (_int, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _p, _p, _p, _p]),
+    "slope_rmsnorm": (_int, [_p, _p, _p, _i64, _i64, ctypes.c_float, _p, _p, _p, _p, _p, _p]),
+    "slope_rmsnorm_bwd": (_int, [_p, _p, _p, _p, _p, _i64, _i64, _p, _p, _p, _i64, _p]),
+    "slope_rmsnorm_bwd_ws": (_int, [_i64, _i64, ctypes.POINTER(_i64)]),
+    "slope_quant_rows": (_int, [_p, _i64, _i64, _p, _p, _p]),
+    "slope_fwd_q8": (_int, [_p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _p, _p]),
     "slope_selftest_wait_timeout": (_int, [_p]),
     "slope_sparse_plan": (_int, [_i64, _i64, _i64, _int, ctypes.POINTER(_int), ctypes.POINTER(_int)]),
     "slope_sparse_tile_rows": (_int, [_i64, _i64, _i64, _int, ctypes.POINTER(_int)]),

@@ -1,0 +1,308 @@
+// gemm_q8.cuh -- the int8 2:4 product on tensor cores, 128 x BN tiles.
+//
+//   Y[t][o] = xscale[t] wscale[o] (Xq . Wq^T)[t][o] + (XL . R)[t][o]
+//
+// tcgen05.mma.sp kind::i8: the kept int8 values of 128 output channels
+// (K-major, 128 stored = 256 dense positions a k-tile), BN int8 token rows,
+// exact sums in 32-bit integers in TMEM.  The codes need no rearranging: TMEM
+// wants lane = row with the row's codes in order, so the code tile comes in by
+// TMA in a 32-byte swizzle and tcgen05.cp puts its 128 x 32 bytes into eight
+// columns.  The rank-r adapter runs as dense bf16 MMAs after the int8 ones
+// into an fp32 accumulator of its own, and the epilogue joins the two, which
+// neither scale could do inside one accumulator.
+//
+// Roles (224 threads): warp 0 operand producer, warp 1 TMEM owner and MMA
+// issuer, warps 2..5 epilogue, warp 6 loads the codes where TMA cannot (rows
+// of K/8 bytes that are not a multiple of 16).
+//
+// One tile per CTA, or per cluster of `splits` CTAs that share the sum over K:
+// each leaves its integer partial in its own shared memory (the operand ring,
+// done by then), and after a cluster barrier every CTA adds all partials for
+// its share of the tokens over distributed shared memory.  So no workspace and
+// no atomics, and two launches can overlap; integer sums do not depend on the
+// split.  Row tiles past the end start at M - 128 instead, so that every code
+// the MMA reads is a legal one; K ends inside a k-tile after whole MMAs.
+#pragma once
+#include <cstdint>
+#include <type_traits>
+#include "gemm.cuh"
+#include "ptx.cuh"
+#include "rownorm.cuh"  // pack_bf16x2
+
+namespace slope {
+
+struct Q8Params {
+    int M, T, K, r;        // output channels, tokens, dense K, adapter rank
+    int m_tiles;
+    int splits;            // CTAs per tile (the cluster size)
+    int meta_tma;          // 1: codes by TMA, 0: by warp 6
+    const uint16_t *meta;  // [M x K/16]
+    const float *xscale, *wscale;
+    uint16_t *Y;           // [T x M]
+};
+
+template <int BN>
+struct Q8TileCfg {
+    static constexpr int A_BYTES = 16384;     // 128 rows x 128 stored int8
+    static constexpr int B_PANEL = BN * 128;  // BN rows x 128 dense int8, 128-byte swizzle
+    static constexpr int E_BYTES = 4096;      // 128 rows x 32 bytes of codes, 32-byte swizzle
+    static constexpr int STAGE_BYTES = A_BYTES + 2 * B_PANEL + E_BYTES;
+    // two CTAs to an SM up to BN = 64, one above
+    static constexpr int NS = BN == 16 ? 4 : BN == 32 ? 3 : BN == 64 ? 3 : 4;
+    static constexpr int ADP_COL = BN;        // fp32 adapter accumulator
+    static constexpr int E_COL = 2 * BN;      // 8 columns per stage
+    static constexpr int TMEM_COLS = BN == 128 ? 512 : BN == 64 ? 256 : 128;
+    static constexpr int SMEM_BYTES = NS * STAGE_BYTES + 128 + 1024;
+    static_assert(E_COL + 8 * NS <= TMEM_COLS, "TMEM budget");
+    static_assert(BN * 128 * 4 <= NS * STAGE_BYTES, "partials fit the ring");
+    static_assert(128 >= 8 * (2 * NS + 1) + 8, "barrier area");
+    static_assert(B_PANEL % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzle-atom alignment");
+    static_assert(SMEM_BYTES <= (BN <= 64 ? 115200 : 232448), "shared memory budget");
+};
+
+// W token columns of one warp's 32 channels: v holds this lane's channel.
+// Neighbouring lanes swap so that each stores a bf16 pair of one token.
+template <int W>
+__device__ __forceinline__ void q8_store(const float (&v)[W], const Q8Params &p, int t0, int f0, int lane, bool ok) {
+    const int odd = lane & 1;
+#pragma unroll
+    for (int j = 0; j < W; j += 2) {
+        const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+        const uint32_t pr = odd ? pack_bf16x2(other, v[j + 1]) : pack_bf16x2(v[j], other);
+        const int t = t0 + j + odd;
+        const int64_t at = (int64_t)t * p.M + f0 + (lane & ~1);
+        if (ok && t < p.T && in_bounds(at, 2, (int64_t)p.T * p.M)) *reinterpret_cast<uint32_t *>(p.Y + at) = pr;
+    }
+}
+
+template <int BN>
+__global__ void __launch_bounds__(224)
+    q8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmR,
+                   const __grid_constant__ CUtensorMap tmXL, const __grid_constant__ Q8Params p) {
+    using C = Q8TileCfg<BN>;
+    constexpr int NS = C::NS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + NS * C::STAGE_BYTES);
+    uint64_t *empty = full + NS;
+    uint64_t *acc_full = empty + NS;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(acc_full + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    int *partial = reinterpret_cast<int *>(smem);  // [BN tokens][128 channels], after the ring is done
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = p.splits;
+    const int rank = S > 1 ? (int)cluster_ctarank() : 0;
+    const int tile = blockIdx.x / S;
+    const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
+    const int m0 = min(mt * 128, p.M - 128);  // M >= 128
+    const int n0 = nt * BN;
+    const int kts = (p.K + 255) >> 8;
+    const int k0 = (int)((int64_t)kts * rank / S), k1 = (int)((int64_t)kts * (rank + 1) / S);
+    const int adp_kts = (p.r + 63) >> 6;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&full[s], p.meta_tma ? 1 : 2);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        if (p.meta_tma) tma_prefetch_desc(&tmE);
+        if (p.r > 0) {
+            tma_prefetch_desc(&tmR);
+            tma_prefetch_desc(&tmXL);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    grid_dep_wait();
+    grid_dep_launch();
+
+    bool done = false;  // epilogue warps: the accumulators are complete
+    if (warp == 0) {
+        // ------------------------------------------------------------ operand producer
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            for (int kt = k0; kt < k1 + adp_kts; ++kt) {
+                if (!mbar_wait(&empty[s], ph ^ 1, abort_flag)) break;
+                uint8_t *a = smem + s * C::STAGE_BYTES;
+                uint8_t *b = a + C::A_BYTES;
+                if (kt < k1) {
+                    mbar_arrive_expect_tx(&full[s], C::A_BYTES + 2 * C::B_PANEL + (p.meta_tma ? C::E_BYTES : 0));
+                    tma_load_2d(a, &tmA, &full[s], kt * 128, m0);
+                    if (p.meta_tma) tma_load_2d(b + 2 * C::B_PANEL, &tmE, &full[s], kt * 16, m0);
+                    tma_load_2d(b, &tmB, &full[s], kt * 256, n0);
+                    tma_load_2d(b + C::B_PANEL, &tmB, &full[s], kt * 256 + 128, n0);
+                } else {  // adapter: R^T (MN-major, two panels of 64 channels) and XL, 64 of the rank
+                    const int j0 = (kt - k1) * 64;
+                    mbar_arrive_expect_tx(&full[s], C::A_BYTES + C::B_PANEL);
+                    tma_load_2d(a, &tmR, &full[s], m0, j0);
+                    tma_load_2d(a + 8192, &tmR, &full[s], m0 + 64, j0);
+                    tma_load_2d(b, &tmXL, &full[s], j0, n0);
+                }
+                if (++s == NS) { s = 0; ph ^= 1; }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t IDESC_SP = instr_desc_sp_i8(128, BN);
+            constexpr uint32_t IDESC_AD = instr_desc(128, BN, 1, 0, 0);
+            const uint32_t base = smem_addr(smem);
+            const uint64_t a_desc0 = smem_desc(base, 16, 1024, SWZ_128B);
+            const uint64_t b_desc0 = smem_desc(base + C::A_BYTES, 16, 1024, SWZ_128B);
+            const uint64_t e_desc0 = smem_desc(base + C::A_BYTES + 2 * C::B_PANEL, 16, 256, SWZ_32B);
+            const uint64_t a2_desc0 = smem_desc(base, 8192, 1024, SWZ_128B);
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int kt = k0; kt < k1 + adp_kts; ++kt) {
+                if (!mbar_wait(&full[s], ph, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t off = (uint64_t)((s * C::STAGE_BYTES) >> 4);
+                if (kt < k1) {
+                    // the code columns of stage s: their last readers finished before the stage was refilled
+                    const uint32_t ecol = tmem_base + C::E_COL + 8 * s;
+                    tmem_cp_128x256b(ecol, e_desc0 + off);
+                    const int nblk = min(4, (p.K - kt * 256) >> 6);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (c < nblk)
+                            mma_sp_i8(tmem_base, a_desc0 + off + (uint64_t)(2 * c),
+                                      b_desc0 + off + (uint64_t)(((c >> 1) * C::B_PANEL + (c & 1) * 64) >> 4), ecol + 2 * c,
+                                      IDESC_SP, (kt > k0 || c > 0) ? 1u : 0u);
+                } else {
+                    const int j0 = (kt - k1) * 64;
+                    const int nblk = min(4, (p.r - j0 + 15) >> 4);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (c < nblk)
+                            mma_bf16(tmem_base + C::ADP_COL, a2_desc0 + off + (uint64_t)(128 * c),
+                                     b_desc0 + off + (uint64_t)(2 * c), IDESC_AD, (j0 > 0 || c > 0) ? 1u : 0u);
+                }
+                mma_commit(&empty[s]);
+                if (++s == NS) { s = 0; ph ^= 1; }
+            }
+            if (ok) mma_commit(acc_full);
+        }
+    } else if (warp < 6) {
+        // ------------------------------------------------------------ epilogue, first part
+        const int q = warp & 3;
+        done = mbar_wait_warp(acc_full, 0, abort_flag);
+        tc_fence_after();
+        if (done && S > 1) {
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+#pragma unroll 1
+            for (int c = 0; c < BN; c += 8) {
+                uint32_t v[8];
+                tmem_ld_32x32_n(taddr + c, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) partial[(c + j) * 128 + 32 * q + lane] = (int)v[j];
+            }
+        }
+    } else if (!p.meta_tma) {
+        // ------------------------------------------------------------ code loader
+        const int words = p.K >> 4;  // code words of a row; a multiple of 4
+        int s = 0;
+        uint32_t ph = 0;
+        for (int kt = k0; kt < k1 + adp_kts; ++kt) {
+            if (!mbar_wait_warp(&empty[s], ph ^ 1, abort_flag)) break;
+            if (kt < k1) {
+                uint8_t *e = smem + s * C::STAGE_BYTES + C::A_BYTES + 2 * C::B_PANEL;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = lane + 32 * i;
+                    uint2 w[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int w0 = kt * 16 + 4 * c;
+                        const int64_t at = (int64_t)(m0 + row) * words + w0;
+                        w[c] = make_uint2(0x44444444u, 0x44444444u);
+                        if (w0 < words && in_bounds(at, 4, (int64_t)p.M * words))
+                            w[c] = *reinterpret_cast<const uint2 *>(p.meta + at);
+                    }
+                    const int x = (row >> 2) & 1;  // the 32-byte swizzle
+                    *reinterpret_cast<uint4 *>(e + row * 32 + 16 * x) = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+                    *reinterpret_cast<uint4 *>(e + row * 32 + 16 * (1 - x)) = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
+                }
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]);
+            if (++s == NS) { s = 0; ph ^= 1; }
+        }
+    }
+    __syncwarp();
+    if (S > 1) cluster_sync();  // every CTA's partial is in place
+    if (warp >= 2 && warp < 6) {
+        // ------------------------------------------------------------ epilogue, second part: this CTA's share of the tokens
+        const int q = warp & 3;
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+        const int f = m0 + 32 * q + lane;          // this lane's channel
+        const bool row_ok = done && f >= mt * 128;  // rows the previous tile owns are not stored again
+        const float ws = done && in_bounds(f, 1, p.M) ? p.wscale[f] : 0.0f;
+        const int share = BN / S;
+        auto columns = [&](auto width, int c) {
+            constexpr int W = decltype(width)::value;
+            uint32_t ai[W], af[W];
+            if (S == 1) tmem_ld_32x32_n(taddr + c, ai);
+            if (p.r > 0) tmem_ld_32x32_n(taddr + C::ADP_COL + c, af);
+            tmem_ld_wait();
+            if (S > 1) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) ai[j] = 0;
+                for (int u = 0; u < S; ++u) {
+                    const uint32_t src = cluster_addr(partial + c * 128 + 32 * q + lane, u);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) ai[j] += (uint32_t)ld_cluster_s32(src + j * 512);
+                }
+            }
+            float v[W];
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const int t = n0 + c + j;
+                const float x = t < p.T && in_bounds(t, 1, p.T) ? __ldg(p.xscale + t) : 0.0f;
+                v[j] = fmaf((float)(int)ai[j], x * ws, p.r > 0 ? bits_to_f32(af[j]) : 0.0f);
+            }
+            q8_store(v, p, n0 + c, m0 + 32 * q, lane, row_ok);
+        };
+        // tokens past the end have no columns to write (their share may be empty)
+        const int c_end = min((rank + 1) * share, (p.T - n0 + 1) & ~1);
+        if (share % 8 == 0) {
+#pragma unroll 1
+            for (int c = rank * share; c < c_end; c += 8) columns(std::integral_constant<int, 8>{}, c);
+        } else {
+#pragma unroll 1
+            for (int c = rank * share; c < c_end; c += 2) columns(std::integral_constant<int, 2>{}, c);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    if (S > 1) cluster_sync();  // the partials have been read
+    else __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem_base, C::TMEM_COLS);
+    }
+}
+
+}  // namespace slope

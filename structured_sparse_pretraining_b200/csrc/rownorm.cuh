@@ -1,0 +1,407 @@
+// rownorm.cuh -- row-wise kernels around the int8 product: root-mean-square
+// norm (with the residual's addition and an int8 output), its gradients, and
+// the int8 quantiser of rows.
+//
+// Norm.  For a token row x (and the residual stream's row e, when there is
+// one):  h = bf16(x + e),  rstd = (mean h^2 + eps)^(-1/2),
+//        y = bf16(h rstd w),  and in int8  y ~ q s  with
+//        p = h w,  q = round(127 p / max|p|),  s = rstd max|p| / 127.
+// The factor rstd cancels in q: p is the product of two bf16 numbers and so
+// exact in binary32, and q is decided exactly (quant_exact), so that q does
+// not depend on how the sum of squares was ordered or rounded.
+//
+// Quantiser.  q = round(127 a / max|a|), s = max|a| / 127 for rows a of bf16
+// values: the kept weights of an output channel, or tokens no norm produced.
+//
+// Gradients.  With n = h rstd and g = dY w:
+//   dh = rstd (g - n mean(g n)) (+ the gradient arriving along the residual),
+//   dw = sum over tokens of dY n.
+//
+// All of it is bound by HBM: each row is read once, held in registers as
+// bf16 while its statistics are reduced, and written once.  A row is one
+// warp's up to 1024 values and one CTA's above, NV 16-byte chunks to a thread.
+#pragma once
+#include <cuda_bf16.h>
+#include <cstdint>
+#include "ptx.cuh"
+#include "skinny.cuh"  // bf16x2_to_float2
+
+namespace slope {
+
+constexpr int ROW_WARPS = 4;            // rows per CTA where a warp takes a row
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// A row's factors for the quantiser.  `f` brings max|p| into a range where
+// 127 p and 127 / max|p| neither overflow nor lose bits (a power of two, so
+// p f is exact for every p that does not quantise to zero).
+struct QuantRow {
+    float f, pm, inv;
+};
+__device__ __forceinline__ QuantRow quant_row(float pmax) {
+    QuantRow q;
+    q.f = pmax < 0x1p-60f ? 0x1p100f : pmax > 0x1p60f ? 0x1p-100f : 1.0f;
+    q.pm = pmax * q.f;
+    q.inv = pmax > 0.0f ? __fdiv_rn(127.0f, q.pm) : 0.0f;
+    return q;
+}
+
+// round(127 p / max|p|), ties to even, decided exactly for t = p f: k is the
+// rounding of the binary32 quotient, off by at most one beside a border.
+// 127 t has at most 23 significant bits and k pm too (7 + 16), and their
+// difference d, a multiple of t's last place, fits 24, so d is exact:
+// |d| > pm / 2 moves k by one, |d| = pm / 2 is a tie.
+__device__ __noinline__ float quant_exact(float t, float k, float pm) {
+    const float d = fmaf(-k, pm, 127.0f * t), a = fabsf(d), half = 0.5f * pm;
+    const bool odd = (static_cast<int>(k) & 1) != 0;
+    return (a > half || (a == half && odd)) ? k + copysignf(1.0f, d) : k;
+}
+
+// Eight values to eight int8 codes.  Adding 1.5 2^23 rounds to an integer in
+// the float's low bits; a quotient within 2^-13 of a border (2.4 in 10^4 of
+// them) is decided again by quant_exact.
+__device__ __forceinline__ uint2 quant8(const float (&p)[8], const QuantRow &q) {
+    constexpr float MAGIC = 12582912.0f;
+    float m[8], worst = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float t = p[j] * q.f * q.inv;
+        m[j] = t + MAGIC;
+        worst = fmaxf(worst, fabsf(t - (m[j] - MAGIC)));
+    }
+    if (worst > 0.5f - 0x1p-13f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m[j] = quant_exact(p[j] * q.f, m[j] - MAGIC, q.pm) + MAGIC;
+    }
+    uint2 r;
+    r.x = __byte_perm(__byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0040),
+                      __byte_perm(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0040), 0x5410);
+    r.y = __byte_perm(__byte_perm(__float_as_uint(m[4]), __float_as_uint(m[5]), 0x0040),
+                      __byte_perm(__float_as_uint(m[6]), __float_as_uint(m[7]), 0x0040), 0x5410);
+    return r;
+}
+
+struct RowParams {
+    const uint16_t *X;    // [T x D] tokens (or the quantiser's rows)
+    const uint16_t *res;  // [T x D] residual stream, or null
+    const uint16_t *w;    // [D] norm weight
+    uint16_t *H;          // [T x D] bf16(X + res), or null
+    uint16_t *Y;          // [T x D] normalised tokens, or null
+    int8_t *Q;            // [T x D] int8, or null
+    float *qscale;        // [T], with Q
+    float *rstd;          // [T], or null
+    int64_t T;
+    int D;
+    float eps;
+};
+
+// NORM: the norm; otherwise the quantiser.  WARP: a warp per row, otherwise a
+// CTA per row.  H may be the buffer of X or res, and Y that of any of them: a
+// thread reads its chunks of a row before it writes those same chunks.
+template <int NV, bool WARP, bool NORM>
+__global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const __grid_constant__ RowParams p) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int gsize = WARP ? 32 : blockDim.x, gi = WARP ? lane : threadIdx.x;
+    const int64_t row = WARP ? (int64_t)blockIdx.x * ROW_WARPS + warp : (int64_t)blockIdx.x;
+    const int nchunk = p.D >> 3;
+    const int64_t total = p.T * p.D;
+    __shared__ float s_sum[32];
+    __shared__ uint32_t s_max[32];
+    grid_dep_wait();
+    grid_dep_launch();
+    if (WARP && row >= p.T) return;
+
+    uint4 h[NV];
+    const int64_t base = row * p.D;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = gi + i * gsize;
+        h[i] = make_uint4(0, 0, 0, 0);
+        if (c < nchunk && in_bounds(base + 8 * c, 8, total)) h[i] = *reinterpret_cast<const uint4 *>(p.X + base + 8 * c);
+    }
+    if (NORM && p.res) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = gi + i * gsize;
+            if (c < nchunk && in_bounds(base + 8 * c, 8, total)) {
+                const uint4 e = *reinterpret_cast<const uint4 *>(p.res + base + 8 * c);
+                uint32_t *a = reinterpret_cast<uint32_t *>(&h[i]);
+                const uint32_t b[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 u = bf16x2_to_float2(a[k]), v = bf16x2_to_float2(b[k]);
+                    a[k] = pack_bf16x2(u.x + v.x, u.y + v.y);
+                }
+                if (p.H) *reinterpret_cast<uint4 *>(p.H + base + 8 * c) = h[i];
+            }
+        }
+    }
+
+    // the row's sum of squares and its largest |p| (as bits: an infinity or a
+    // NaN, whose bits are larger than any number's, wins)
+    float ss = 0.0f;
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = gi + i * gsize;
+        uint4 wv = make_uint4(0, 0, 0, 0);
+        if (NORM && p.Q && c < nchunk && in_bounds(8 * c, 8, p.D)) wv = __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c));
+        const uint32_t a[4] = {h[i].x, h[i].y, h[i].z, h[i].w}, b[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 u = bf16x2_to_float2(a[k]);
+            if (NORM) {
+                ss = fmaf(u.x, u.x, fmaf(u.y, u.y, ss));
+                if (p.Q) {
+                    const float2 v = bf16x2_to_float2(b[k]);
+                    mx = max(mx, max(__float_as_uint(u.x * v.x) & 0x7FFFFFFFu, __float_as_uint(u.y * v.y) & 0x7FFFFFFFu));
+                }
+            } else {
+                mx = max(mx, max(__float_as_uint(u.x) & 0x7FFFFFFFu, __float_as_uint(u.y) & 0x7FFFFFFFu));
+            }
+        }
+    }
+    if (NORM) ss = warp_sum(ss);
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if (!WARP) {
+        if (lane == 0) {
+            s_sum[warp] = ss;
+            s_max[warp] = mx;
+        }
+        __syncthreads();
+        const int nw = blockDim.x >> 5;
+        ss = warp_sum(lane < nw ? s_sum[lane] : 0.0f);
+        mx = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[lane] : 0u);
+    }
+
+    float rstd = 1.0f;
+    if (NORM) {
+        if (__float_as_uint(ss) == kInfBits) {
+            // the squares overflow binary32: once more on h 2^-80 (an infinity
+            // in the row stays one, and gives rstd = 0 and NaN beside it)
+            float s2 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const uint32_t a[4] = {h[i].x, h[i].y, h[i].z, h[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 u = bf16x2_to_float2(a[k]);
+                    s2 = fmaf(u.x * 0x1p-80f, u.x * 0x1p-80f, fmaf(u.y * 0x1p-80f, u.y * 0x1p-80f, s2));
+                }
+            }
+            s2 = warp_sum(s2);
+            if (!WARP) {
+                __syncthreads();  // every thread has read the first sums
+                if (lane == 0) s_sum[warp] = s2;
+                __syncthreads();
+                s2 = warp_sum(lane < (int)(blockDim.x >> 5) ? s_sum[lane] : 0.0f);
+            }
+            rstd = __frcp_rn(__fsqrt_rn(s2 / (float)p.D)) * 0x1p-80f;
+        } else {
+            rstd = __frcp_rn(__fsqrt_rn(ss / (float)p.D + p.eps));
+        }
+        if (p.rstd && gi == 0 && in_bounds(row, 1, p.T)) p.rstd[row] = rstd;
+    }
+    const bool finite = mx < kInfBits;
+    const float pmax = __uint_as_float(mx);
+    const QuantRow q = quant_row(finite ? pmax : 0.0f);
+    if (p.Q && gi == 0 && in_bounds(row, 1, p.T))
+        p.qscale[row] = finite ? rstd * pmax / 127.0f : __uint_as_float(0x7FC00000u);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = gi + i * gsize;
+        if (c >= nchunk || !in_bounds(base + 8 * c, 8, total)) continue;
+        const uint32_t a[4] = {h[i].x, h[i].y, h[i].z, h[i].w};
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 u = bf16x2_to_float2(a[k]);
+            v[2 * k] = u.x;
+            v[2 * k + 1] = u.y;
+        }
+        if (NORM) {
+            const uint4 wv = __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c));
+            const uint32_t b[4] = {wv.x, wv.y, wv.z, wv.w};
+            if (p.Y) {
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 g = bf16x2_to_float2(b[k]);
+                    o[k] = pack_bf16x2(v[2 * k] * rstd * g.x, v[2 * k + 1] * rstd * g.y);
+                }
+                *reinterpret_cast<uint4 *>(p.Y + base + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 g = bf16x2_to_float2(b[k]);
+                v[2 * k] *= g.x;
+                v[2 * k + 1] *= g.y;
+            }
+        }
+        if (p.Q)
+            *reinterpret_cast<uint2 *>(p.Q + base + 8 * c) = finite ? quant8(v, q) : make_uint2(0, 0);
+    }
+}
+
+struct RowBwdParams {
+    const uint16_t *dY, *H, *w;
+    const float *rstd;
+    const uint16_t *dres;  // or null
+    uint16_t *dH;
+    float *part;           // [parts x D] partial sums of dw
+    int64_t T;
+    int D;
+    int parts;             // CTAs of the launch
+};
+
+// A CTA takes rows blockIdx.x, + gridDim.x, ... (ROW_WARPS at a time where a
+// warp takes a row), keeps its sum of dY n in registers and writes it as one
+// row of `part`; dw_sum_kernel adds those rows in a fixed order.  HOLD: the
+// row stays in registers between the reduction and the gradient; without it
+// (rows too long beside the sums) it is read again, from L2.
+template <int NV, bool WARP, bool HOLD>
+__global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_bwd_kernel(const __grid_constant__ RowBwdParams p) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int gsize = WARP ? 32 : blockDim.x, gi = WARP ? lane : threadIdx.x;
+    const int nchunk = p.D >> 3;
+    const int64_t total = p.T * p.D;
+    extern __shared__ float s_dw[];  // WARP: [ROW_WARPS][D]
+    __shared__ float s_sum[2][32];
+    grid_dep_wait();
+    grid_dep_launch();
+    float acc[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+    const float inv_d = 1.0f / (float)p.D;
+    int turn = 0;
+    for (int64_t row = WARP ? (int64_t)blockIdx.x * ROW_WARPS + warp : (int64_t)blockIdx.x; row < p.T;
+         row += WARP ? (int64_t)gridDim.x * ROW_WARPS : (int64_t)gridDim.x) {
+        const int64_t base = row * p.D;
+        uint4 h[HOLD ? NV : 1], g[HOLD ? NV : 1];
+        const float rstd = in_bounds(row, 1, p.T) ? p.rstd[row] : 0.0f;
+        auto load = [&](int i, uint4 &hv, uint4 &gv) {
+            const int c = gi + i * gsize;
+            hv = gv = make_uint4(0, 0, 0, 0);
+            if (c < nchunk && in_bounds(base + 8 * c, 8, total)) {
+                hv = *reinterpret_cast<const uint4 *>(p.H + base + 8 * c);
+                gv = *reinterpret_cast<const uint4 *>(p.dY + base + 8 * c);
+            }
+        };
+        if (HOLD) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) load(i, h[i], g[i]);
+        }
+        float dot = 0.0f;  // sum of g h
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = gi + i * gsize;
+            if (!HOLD) load(i, h[0], g[0]);
+            uint4 wv = make_uint4(0, 0, 0, 0);
+            if (c < nchunk && in_bounds(8 * c, 8, p.D)) wv = __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c));
+            const uint4 hv = h[HOLD ? i : 0], gv = g[HOLD ? i : 0];
+            const uint32_t a[4] = {hv.x, hv.y, hv.z, hv.w}, b[4] = {gv.x, gv.y, gv.z, gv.w}, d[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 hh = bf16x2_to_float2(a[k]), gg = bf16x2_to_float2(b[k]), ww = bf16x2_to_float2(d[k]);
+                dot = fmaf(gg.x * ww.x, hh.x * rstd, fmaf(gg.y * ww.y, hh.y * rstd, dot));
+                acc[i][2 * k] = fmaf(gg.x, hh.x * rstd, acc[i][2 * k]);
+                acc[i][2 * k + 1] = fmaf(gg.y, hh.y * rstd, acc[i][2 * k + 1]);
+            }
+        }
+        dot = warp_sum(dot);
+        if (!WARP) {
+            if (lane == 0) s_sum[turn][warp] = dot;
+            __syncthreads();
+            dot = warp_sum(lane < (int)(blockDim.x >> 5) ? s_sum[turn][lane] : 0.0f);
+            turn ^= 1;  // the next row's sums go beside this row's, which other warps may still read
+        }
+        const float mean = dot * inv_d;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = gi + i * gsize;
+            if (!HOLD) load(i, h[0], g[0]);
+            if (c >= nchunk || !in_bounds(base + 8 * c, 8, total)) continue;
+            const uint4 wv = __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c));
+            uint4 ev = make_uint4(0, 0, 0, 0);
+            if (p.dres) ev = *reinterpret_cast<const uint4 *>(p.dres + base + 8 * c);
+            const uint4 hv = h[HOLD ? i : 0], gv = g[HOLD ? i : 0];
+            const uint32_t a[4] = {hv.x, hv.y, hv.z, hv.w}, b[4] = {gv.x, gv.y, gv.z, gv.w}, d[4] = {wv.x, wv.y, wv.z, wv.w};
+            const uint32_t e[4] = {ev.x, ev.y, ev.z, ev.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 hh = bf16x2_to_float2(a[k]), gg = bf16x2_to_float2(b[k]), ww = bf16x2_to_float2(d[k]);
+                const float2 ee = bf16x2_to_float2(e[k]);
+                o[k] = pack_bf16x2(fmaf(rstd, fmaf(-hh.x * rstd, mean, gg.x * ww.x), ee.x),
+                                   fmaf(rstd, fmaf(-hh.y * rstd, mean, gg.y * ww.y), ee.y));
+            }
+            *reinterpret_cast<uint4 *>(p.dH + base + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+    // this CTA's partial row
+    const int64_t pbase = (int64_t)blockIdx.x * p.D, ptotal = (int64_t)p.parts * p.D;
+    if (WARP) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = gi + i * gsize;
+            if (c < nchunk) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s_dw[warp * p.D + 8 * c + j] = acc[i][j];
+            }
+        }
+        __syncthreads();
+        for (int d = threadIdx.x; d < p.D; d += blockDim.x) {
+            float s = s_dw[d];
+#pragma unroll
+            for (int k = 1; k < ROW_WARPS; ++k) s += s_dw[k * p.D + d];
+            if (in_bounds(pbase + d, 1, ptotal)) p.part[pbase + d] = s;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = gi + i * gsize;
+            if (c < nchunk && in_bounds(pbase + 8 * c, 8, ptotal)) {
+                float4 *dst = reinterpret_cast<float4 *>(p.part + pbase + 8 * c);
+                dst[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+                dst[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+            }
+        }
+    }
+}
+
+// dw[d] = sum over the `parts` rows of part[.][d], in a fixed order: 32
+// columns per CTA, 8 warps over the rows, their sums added in warp order.
+__global__ void __launch_bounds__(256) dw_sum_kernel(const float *part, int parts, int D, float *dw) {
+    __shared__ float s[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int d = blockIdx.x * 32 + lane;
+    grid_dep_wait();
+    grid_dep_launch();
+    float a = 0.0f;
+    if (d < D) {
+#pragma unroll 8
+        for (int r = warp; r < parts; r += 8)
+            if (in_bounds((int64_t)r * D + d, 1, (int64_t)parts * D)) a += __ldcg(part + (int64_t)r * D + d);
+    }
+    s[warp][lane] = a;
+    __syncthreads();
+    if (warp == 0 && d < D) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k) a += s[k][lane];
+        if (in_bounds(d, 1, D)) dw[d] = a;
+    }
+}
+
+}  // namespace slope

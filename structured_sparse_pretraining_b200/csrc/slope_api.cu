@@ -16,9 +16,12 @@
 #include "../../include/slope.h"
 #include "gemm.cuh"
 #include "gemm_pair.cuh"
+#include "gemm_q8.cuh"
 #include "gemm_wide.cuh"
 #include "prune.cuh"
+#include "rownorm.cuh"
 #include "skinny.cuh"
+#include "skinny_q8.cuh"
 
 namespace {
 
@@ -42,6 +45,12 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 #define CHECK_PTR(p)                                                              \
     do {                                                                          \
         if ((p) == nullptr) return fail(SLOPE_ERR_ARG, "%s is NULL", #p);         \
+        if (!aligned16(p)) return fail(SLOPE_ERR_ALIGN, "%s is not 16-byte aligned", #p); \
+    } while (0)
+
+// An optional pointer: null, or aligned.
+#define CHECK_OPT(p)                                                              \
+    do {                                                                          \
         if (!aligned16(p)) return fail(SLOPE_ERR_ALIGN, "%s is not 16-byte aligned", #p); \
     } while (0)
 
@@ -135,6 +144,23 @@ int make_map(CUtensorMap &m, const void *base, int64_t rows, int64_t cols, int64
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(SLOPE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for [%lld x %lld] box [%d x %d]", (int)r,
+                    (long long)rows, (long long)cols, box_rows, box_cols);
+    return SLOPE_OK;
+}
+
+// The same over an int8 tensor [rows x cols] without padding, 128-byte swizzle.
+int make_map_i8(CUtensorMap &m, const void *base, int64_t rows, int64_t cols, int box_cols, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(SLOPE_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)cols};
+    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(SLOPE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for int8 [%lld x %lld] box [%d x %d]", (int)r,
                     (long long)rows, (long long)cols, box_rows, box_cols);
     return SLOPE_OK;
 }
@@ -1540,6 +1566,304 @@ int slope_adapter_bwd(const uint16_t *X, const uint16_t *dY, const uint16_t *XL,
     if (int rc = token_reduction(dY, XL, T, out, r, dR, true, d, st)) return rc;
     // dL = X^T . G
     return token_reduction(X, G, T, in, r, dL, false, d, st);
+}
+
+}  // extern "C"
+
+namespace {
+// ------------------------------------------------------------------ row kernels (norm, its gradients, quantiser)
+constexpr int64_t NORM_MAX_D = 32768, QUANT_MAX_K = 65536;
+
+int check_width(int64_t v, int64_t most, const char *name) {
+    if (v <= 0) return fail(SLOPE_ERR_ARG, "%s = %lld must be positive", name, (long long)v);
+    if (v % 8 != 0 || v > most)
+        return fail(SLOPE_ERR_SHAPE, "%s = %lld must be a multiple of 8 up to %lld", name, (long long)v, (long long)most);
+    return SLOPE_OK;
+}
+
+// How a row of D values is laid over threads: one warp's up to 1024 values
+// (NV 16-byte chunks per lane), one CTA's above.
+struct RowPlan {
+    bool warp;
+    int nv, threads;
+};
+RowPlan pick_row_plan(int64_t D) {
+    const int chunks = (int)(D / 8);
+    if (chunks <= 128) return RowPlan{true, chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4, 32 * slope::ROW_WARPS};
+    const int nv = chunks <= 2048 ? 2 : chunks <= 4096 ? 4 : 8;
+    return RowPlan{false, nv, (chunks + 32 * nv - 1) / (32 * nv) * 32};
+}
+
+template <bool NORM>
+int row_launch(const slope::RowParams &p, cudaStream_t st, const char *what) {
+    const RowPlan r = pick_row_plan(p.D);
+    const int64_t blocks = r.warp ? (p.T + slope::ROW_WARPS - 1) / slope::ROW_WARPS : p.T;
+    const dim3 grid((unsigned)blocks), block((unsigned)r.threads);
+    if (r.warp) {
+        if (r.nv == 1) return launch_pdl(slope::row_kernel<1, true, NORM>, grid, block, 0, st, what, p);
+        if (r.nv == 2) return launch_pdl(slope::row_kernel<2, true, NORM>, grid, block, 0, st, what, p);
+        return launch_pdl(slope::row_kernel<4, true, NORM>, grid, block, 0, st, what, p);
+    }
+    if (r.nv == 2) return launch_pdl(slope::row_kernel<2, false, NORM>, grid, block, 0, st, what, p);
+    if constexpr (!NORM)  // the norm's rows end at NV = 4
+        if (r.nv == 8) return launch_pdl(slope::row_kernel<8, false, NORM>, grid, block, 0, st, what, p);
+    return launch_pdl(slope::row_kernel<4, false, NORM>, grid, block, 0, st, what, p);
+}
+
+// CTAs of the gradient kernel, and so rows of its partial sums of dw: enough
+// to fill 148 SMs with about 1536 threads each.
+int64_t norm_bwd_parts(int64_t T, int64_t D) {
+    const RowPlan r = pick_row_plan(D);
+    const int64_t per_sm = 1536 / r.threads < 1 ? 1 : 1536 / r.threads > 4 ? 4 : 1536 / r.threads;
+    const int64_t blocks = r.warp ? (T + slope::ROW_WARPS - 1) / slope::ROW_WARPS : T;
+    return blocks < 148 * per_sm ? blocks : 148 * per_sm;
+}
+}  // namespace
+
+extern "C" {
+
+int slope_rmsnorm(const uint16_t *X, const uint16_t *res, const uint16_t *w, int64_t T, int64_t D, float eps, uint16_t *H,
+                  uint16_t *Y, int8_t *Q, float *qscale, float *rstd, void *stream) {
+    CHECK_PTR(X);
+    CHECK_PTR(w);
+    if (!Y && !Q) return fail(SLOPE_ERR_ARG, "rmsnorm: one of Y and Q is required");
+    if (Q && !qscale) return fail(SLOPE_ERR_ARG, "qscale is NULL");
+    if (H && !res) return fail(SLOPE_ERR_ARG, "rmsnorm: H without res (H would be X)");
+    CHECK_OPT(res);
+    CHECK_OPT(H);
+    CHECK_OPT(Y);
+    CHECK_OPT(Q);
+    CHECK_OPT(qscale);
+    CHECK_OPT(rstd);
+    if (int rc = check_tokens(T)) return rc;
+    if (int rc = check_width(D, NORM_MAX_D, "D")) return rc;
+    if (!(eps > 0.0f) || !std::isfinite(eps)) return fail(SLOPE_ERR_ARG, "rmsnorm: eps must be positive and finite");
+    DevInfo d;
+    if (int rc = device_info(d)) return rc;
+    slope::RowParams p{X, res, w, H, Y, Q, Q ? qscale : nullptr, rstd, T, (int)D, eps};
+    return row_launch<true>(p, static_cast<cudaStream_t>(stream), "rmsnorm launch");
+}
+
+int slope_quant_rows(const uint16_t *A, int64_t rows, int64_t K, int8_t *Q, float *scale, void *stream) {
+    CHECK_PTR(A);
+    CHECK_PTR(Q);
+    CHECK_PTR(scale);
+    if (rows <= 0) return fail(SLOPE_ERR_ARG, "rows = %lld must be positive", (long long)rows);
+    if (rows > (int64_t(1) << 30)) return fail(SLOPE_ERR_SHAPE, "rows = %lld too large", (long long)rows);
+    if (int rc = check_width(K, QUANT_MAX_K, "K")) return rc;
+    DevInfo d;
+    if (int rc = device_info(d)) return rc;
+    slope::RowParams p{A, nullptr, nullptr, nullptr, nullptr, Q, scale, nullptr, rows, (int)K, 0.0f};
+    return row_launch<false>(p, static_cast<cudaStream_t>(stream), "quant_rows launch");
+}
+
+int slope_rmsnorm_bwd_ws(int64_t T, int64_t D, int64_t *floats) {
+    if (!floats) return fail(SLOPE_ERR_ARG, "floats is NULL");
+    if (int rc = check_tokens(T)) return rc;
+    if (int rc = check_width(D, NORM_MAX_D, "D")) return rc;
+    *floats = norm_bwd_parts(T, D) * D;
+    return SLOPE_OK;
+}
+
+int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, const float *rstd, const uint16_t *dres,
+                      int64_t T, int64_t D, uint16_t *dH, float *dw, float *ws, int64_t ws_floats, void *stream) {
+    CHECK_PTR(dY);
+    CHECK_PTR(H);
+    CHECK_PTR(w);
+    CHECK_PTR(rstd);
+    CHECK_PTR(dH);
+    CHECK_PTR(dw);
+    CHECK_PTR(ws);
+    CHECK_OPT(dres);
+    if (int rc = check_tokens(T)) return rc;
+    if (int rc = check_width(D, NORM_MAX_D, "D")) return rc;
+    const int64_t parts = norm_bwd_parts(T, D);
+    if (ws_floats < parts * D)
+        return fail(SLOPE_ERR_SHAPE, "rmsnorm_bwd: ws holds %lld floats, %lld are needed (slope_rmsnorm_bwd_ws)",
+                    (long long)ws_floats, (long long)(parts * D));
+    DevInfo d;
+    if (int rc = device_info(d)) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    slope::RowBwdParams p{dY, H, w, rstd, dres, dH, ws, T, (int)D, (int)parts};
+    const RowPlan r = pick_row_plan(D);
+    const dim3 grid((unsigned)parts), block((unsigned)r.threads);
+    const char *what = "rmsnorm_bwd launch";
+    const int smem = r.warp ? (int)(slope::ROW_WARPS * D * sizeof(float)) : 0;
+    int rc;
+    if (r.warp)
+        rc = r.nv == 1   ? launch_pdl(slope::row_bwd_kernel<1, true, true>, grid, block, smem, st, what, p)
+             : r.nv == 2 ? launch_pdl(slope::row_bwd_kernel<2, true, true>, grid, block, smem, st, what, p)
+                         : launch_pdl(slope::row_bwd_kernel<4, true, true>, grid, block, smem, st, what, p);
+    else
+        rc = r.nv == 2 ? launch_pdl(slope::row_bwd_kernel<2, false, true>, grid, block, smem, st, what, p)
+                       : launch_pdl(slope::row_bwd_kernel<4, false, false>, grid, block, smem, st, what, p);
+    if (rc) return rc;
+    return launch_pdl(slope::dw_sum_kernel, dim3((unsigned)((D + 31) / 32)), dim3(256), 0, st, "rmsnorm_bwd dw launch",
+                      (const float *)ws, (int)parts, (int)D, dw);
+}
+
+}  // extern "C"
+
+namespace {
+// ------------------------------------------------------------------ int8 sparse product
+constexpr int64_t Q8_MAX_K = 131072;  // 128 * 128 * K / 2 stays below 2^31
+
+// Opt in to `bytes` of dynamic shared memory once per device.
+template <typename Kern>
+int allow_smem(Kern kern, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64 && (done.load() & (1ull << dev))) return SLOPE_OK;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(int8 product)");
+    if (dev < 64) done.fetch_or(1ull << dev);
+    return SLOPE_OK;
+}
+
+struct Q8Plan {
+    int bn;      // 0: CUDA cores, else the token width of the tensor-core tile
+    int splits;  // CTAs that share a tile's sum over K (or warps a group of channels, on CUDA cores)
+    int tb;      // CUDA cores: tokens per pass
+};
+
+Q8Plan pick_q8_plan(int64_t M, int64_t T, int64_t K, int sms) {
+    if (T <= 4 || M < 128) {
+        const int64_t row = (K + 1023) / 1024 * 1024;
+        int tb = T >= 3 ? 4 : (int)T;
+        while (tb > 1 && tb * row > 200 * 1024) tb /= 2;
+        // warps share a group of channels while there are fewer groups than warps on the GPU
+        int ks = 1;
+        while (ks < slope::SQ8_WARPS && M / slope::SQ8_ROWS * ks * 2 <= (int64_t)sms * slope::SQ8_WARPS && ks * 1024 < K) ks *= 2;
+        return Q8Plan{0, ks, tb};
+    }
+    const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+    const int64_t kts = (K + 255) / 256, tiles = (M + 127) / 128 * ((T + bn - 1) / bn);
+    const int64_t slots = (int64_t)sms * (bn <= 64 ? 2 : 1);
+    Q8Plan best{bn, 1, 0};
+    double best_cost = 1e300;
+    for (int s = 1; s <= 8 && s <= kts; s *= 2) {
+        const double cost = (double)((tiles * s + slots - 1) / slots) * ((double)((kts + s - 1) / s) + 4.0) + 0.5 * (s > 1 ? s : 0);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best.splits = s;
+        }
+    }
+    return best;
+}
+
+template <int TB>
+int launch_skinny_q8(const slope::SkinnyQ8Params &p, int sms, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    if (int rc = allow_smem(slope::skinny_q8_kernel<TB>, 200 * 1024, done)) return rc;
+    const int smem = TB * (int)((p.K + 1023) / 1024) * 1024;
+    const int gpc = slope::SQ8_WARPS / p.ksplit;
+    const int64_t groups = p.M / slope::SQ8_ROWS;
+    const int64_t need = (groups + gpc - 1) / gpc;
+    const int64_t cap = (int64_t)sms * (smem <= 100 * 1024 ? 2 : 1);
+    const dim3 grid((unsigned)(need < cap ? need : cap), (unsigned)((p.T + TB - 1) / TB));
+    return launch_pdl(slope::skinny_q8_kernel<TB>, grid, dim3(32 * slope::SQ8_WARPS), smem, st, "int8 product launch", p);
+}
+
+template <int BN>
+int launch_q8_tile(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &e, const CUtensorMap &r2,
+                   const CUtensorMap &xl, const slope::Q8Params &p, cudaStream_t st) {
+    using C = slope::Q8TileCfg<BN>;
+    auto kern = slope::q8_tile_kernel<BN>;
+    static std::atomic<uint64_t> done{0};
+    if (int rc = allow_smem(kern, C::SMEM_BYTES, done)) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)((int64_t)p.m_tiles * ((p.T + BN - 1) / BN) * p.splits), 1, 1);
+    cfg.blockDim = dim3(224, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.splits > 1 ? 2 : 1;
+    cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a, b, e, r2, xl, p);
+    if (err != cudaSuccess) return cuda_fail(err, "int8 product launch");
+    ++g_launches;
+    return SLOPE_OK;
+}
+
+int q8_product(const int8_t *X, const float *xscale, const int8_t *W, const float *wscale, const uint16_t *meta,
+               const uint16_t *XL, const uint16_t *R, int64_t T, int64_t K, int64_t M, int64_t r, uint16_t *Y, cudaStream_t st) {
+    DevInfo d;
+    if (int rc = device_info(d)) return rc;
+    const Q8Plan plan = pick_q8_plan(M, T, K, d.sms);
+    if (plan.bn == 0) {
+        // the grid's second dimension counts blocks of tb tokens
+        for (int64_t t0 = 0; t0 < T;) {
+            const int64_t n = T - t0 < 65535 * (int64_t)plan.tb ? T - t0 : 65535 * (int64_t)plan.tb;
+            slope::SkinnyQ8Params p{X + t0 * K, xscale + t0, W, wscale, meta, XL ? XL + t0 * r : nullptr, R, Y + t0 * M,
+                                    (int)n, (int)K, (int)M, (int)r, plan.splits};
+            const int rc = plan.tb == 4   ? launch_skinny_q8<4>(p, d.sms, st)
+                           : plan.tb == 2 ? launch_skinny_q8<2>(p, d.sms, st)
+                                          : launch_skinny_q8<1>(p, d.sms, st);
+            if (rc) return rc;
+            t0 += n;
+        }
+        return SLOPE_OK;
+    }
+    CUtensorMap a, b, e, r2, xl;
+    slope::Q8Params p{};
+    p.M = (int)M;
+    p.T = (int)T;
+    p.K = (int)K;
+    p.r = (int)r;
+    p.m_tiles = (int)((M + 127) / 128);
+    p.splits = plan.splits;
+    p.meta_tma = K % 128 == 0;
+    p.meta = meta;
+    p.xscale = xscale;
+    p.wscale = wscale;
+    p.Y = Y;
+    if (int rc = make_map_i8(a, W, M, K / 2, 128, 128)) return rc;
+    if (int rc = make_map_i8(b, X, T, K, 128, plan.bn)) return rc;
+    e = a;  // unused maps are copies of a valid one
+    r2 = a;
+    xl = a;
+    if (p.meta_tma)
+        if (int rc = make_map(e, meta, M, K / 16, K / 16, 16, 128, 32, false)) return rc;
+    if (r > 0) {
+        if (int rc = make_map(r2, R, r, M, M, 64, 64)) return rc;
+        if (int rc = make_map(xl, XL, T, r, r, 64, plan.bn)) return rc;
+    }
+    switch (plan.bn) {
+        case 16: return launch_q8_tile<16>(a, b, e, r2, xl, p, st);
+        case 32: return launch_q8_tile<32>(a, b, e, r2, xl, p, st);
+        case 64: return launch_q8_tile<64>(a, b, e, r2, xl, p, st);
+        default: return launch_q8_tile<128>(a, b, e, r2, xl, p, st);
+    }
+}
+}  // namespace
+
+extern "C" {
+
+int slope_fwd_q8(const int8_t *Xq, const float *xscale, const int8_t *vals_q, const float *wscale, const uint16_t *meta,
+                 const uint16_t *XL, const uint16_t *R, int64_t T, int64_t in, int64_t out, int64_t r, uint16_t *Y,
+                 void *stream) {
+    CHECK_PTR(Xq);
+    CHECK_PTR(xscale);
+    CHECK_PTR(vals_q);
+    CHECK_PTR(wscale);
+    CHECK_PTR(meta);
+    CHECK_PTR(Y);
+    if (int rc = check_tokens(T)) return rc;
+    if (int rc = check_features(in, "in")) return rc;
+    if (in > Q8_MAX_K) return fail(SLOPE_ERR_SHAPE, "in = %lld: int8 sums are exact up to %lld", (long long)in, (long long)Q8_MAX_K);
+    if (int rc = check_features(out, "out")) return rc;
+    if (int rc = check_rank(r)) return rc;
+    if (r > 0) {
+        CHECK_PTR(XL);
+        CHECK_PTR(R);
+    }
+    return q8_product(Xq, xscale, vals_q, wscale, meta, XL, R, T, in, out, r, Y, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

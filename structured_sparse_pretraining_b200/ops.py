@@ -263,6 +263,113 @@ def bwd_dw_masked_noalloc(dY, X, meta, dW_vals):
     return dW_vals
 
 
+def _call_on(first, name, *args, others=()):
+    """Call an entry point on the device of `first` (current or not) and that
+    device's current stream; every tensor of the call must be there."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one device is needed")
+    with torch.cuda.device(first.device):
+        return _lib.call(name, *args, _stream())
+
+
+def _matrix(t, dtype, name, shape=None):
+    _need(t, dtype, name, shape)
+    if t.dim() != 2:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected two dimensions")
+    return t
+
+
+def _out(t, shape, dtype, name, like):
+    return _empty(shape, dtype, like) if t is None else _need(t, dtype, name, shape)
+
+
+def rmsnorm(X, w, eps, res=None, with_rstd=False, H=None, Y=None, rstd=None):
+    """(Y, H, rstd): h = bf16(X + res), Y = h rstd w with rstd = (mean h^2 + eps)^(-1/2)
+    per token.  X, res [T, D] bf16, w [D] bf16.  H (h, the residual stream) is
+    None without res; rstd [T] fp32 is written with with_rstd (rmsnorm_bwd
+    needs it), else None."""
+    _, _, Y, H, rstd = _rmsnorm(X, w, eps, res, True, False, with_rstd, H, Y, None, None, rstd)
+    return Y, H, rstd
+
+
+def rmsnorm_q8(X, w, eps, res=None, with_y=False, with_rstd=False, H=None, Y=None, Q=None, qscale=None, rstd=None):
+    """(Q, qscale, Y, H, rstd): rmsnorm with its output in int8, Q [T, D] with
+    one scale per token (Q qscale stands for h rstd w), and with with_y in bf16
+    too (the adapter's product reads that)."""
+    return _rmsnorm(X, w, eps, res, with_y or Y is not None, True, with_rstd, H, Y, Q, qscale, rstd)
+
+
+def _rmsnorm(X, w, eps, res, with_y, with_q8, with_rstd, H, Y, Q, qscale, rstd):
+    T, D = _matrix(X, torch.bfloat16, "X").shape
+    _need(w, torch.bfloat16, "w", (D,))
+    if res is not None:
+        _need(res, torch.bfloat16, "res", (T, D))
+        H = _out(H, (T, D), torch.bfloat16, "H", X)
+    elif H is not None:
+        raise ValueError("H without res (H would be X)")
+    Y = _out(Y, (T, D), torch.bfloat16, "Y", X) if with_y else None
+    Q = _out(Q, (T, D), torch.int8, "Q", X) if with_q8 else None
+    qscale = _out(qscale, (T,), torch.float32, "qscale", X) if with_q8 else None
+    rstd = _out(rstd, (T,), torch.float32, "rstd", X) if with_rstd or rstd is not None else None
+    _call_on(X, "slope_rmsnorm", _ptr(X), _ptr(res), _ptr(w), T, D, float(eps), _ptr(H), _ptr(Y), _ptr(Q), _ptr(qscale),
+             _ptr(rstd), others=(res, w, H, Y, Q, qscale, rstd))
+    return Q, qscale, Y, H, rstd
+
+
+def rmsnorm_bwd(dY, H, w, rstd, dres=None, dH=None, dw=None):
+    """(dH, dw): gradients of rmsnorm's Y with respect to h (X and res both
+    take dH; dres, the gradient reaching h along the residual stream, is added)
+    [T, D] bf16 and to w [D] fp32.  H is rmsnorm's (or X without a residual)."""
+    T, D = _matrix(dY, torch.bfloat16, "dY").shape
+    _need(H, torch.bfloat16, "H", (T, D))
+    _need(w, torch.bfloat16, "w", (D,))
+    _need(rstd, torch.float32, "rstd", (T,))
+    if dres is not None:
+        _need(dres, torch.bfloat16, "dres", (T, D))
+    dH = _out(dH, (T, D), torch.bfloat16, "dH", dY)
+    dw = _out(dw, (D,), torch.float32, "dw", dY)
+    floats = ctypes.c_int64(0)
+    _lib.call("slope_rmsnorm_bwd_ws", T, D, ctypes.byref(floats))
+    ws = _empty((floats.value,), torch.float32, dY)
+    _call_on(dY, "slope_rmsnorm_bwd", _ptr(dY), _ptr(H), _ptr(w), _ptr(rstd), _ptr(dres), T, D, _ptr(dH), _ptr(dw), _ptr(ws),
+             floats.value, others=(H, w, rstd, dres, dH, dw))
+    return dH, dw
+
+
+def quant_rows(A, Q=None, scale=None):
+    """(Q, scale): rows of A [rows, K] bf16 in int8 with one fp32 scale per row
+    (the kept weights of prune24: one per output channel)."""
+    rows, K = _matrix(A, torch.bfloat16, "A").shape
+    Q = _out(Q, (rows, K), torch.int8, "Q", A)
+    scale = _out(scale, (rows,), torch.float32, "scale", A)
+    _call_on(A, "slope_quant_rows", _ptr(A), rows, K, _ptr(Q), _ptr(scale), others=(Q, scale))
+    return Q, scale
+
+
+def fwd_q8(Xq, xscale, vals_q, wscale, meta, XL, R, out_features, Y=None):
+    """Y [T, out] bf16 = xscale wscale (Xq . Wq^T) + XL . R: fwd in int8, with
+    Xq [T, in] and xscale [T] from rmsnorm_q8 or quant_rows, and vals_q
+    [out, in/2], wscale [out] the kept weights through quant_rows (XL, R None:
+    no adapter)."""
+    T, in_ = _matrix(Xq, torch.int8, "Xq").shape
+    _need(xscale, torch.float32, "xscale", (T,))
+    _need(vals_q, torch.int8, "vals_q", (out_features, in_ // 2))
+    _need(wscale, torch.float32, "wscale", (out_features,))
+    _need(meta, torch.int16, "meta", (out_features, in_ // 16))
+    r = 0
+    if R is not None:
+        r = _matrix(R, torch.bfloat16, "R").shape[0]
+        _need(R, torch.bfloat16, "R", (r, out_features))
+        _need(XL, torch.bfloat16, "XL", (T, r))
+    elif XL is not None:
+        raise ValueError("XL without R")
+    Y = _out(Y, (T, out_features), torch.bfloat16, "Y", Xq)
+    _call_on(Xq, "slope_fwd_q8", _ptr(Xq), _ptr(xscale), _ptr(vals_q), _ptr(wscale), _ptr(meta), _ptr(XL) if r else None,
+             _ptr(R) if r else None, T, in_, out_features, r, _ptr(Y), others=(xscale, vals_q, wscale, meta, XL, R, Y))
+    return Y
+
+
 def sparse_plan(M, T, K, sms=148):
     """(BN, splits) the sparse products use for an M x K operand and T tokens
     on a device with `sms` SMs (host-only query, no GPU needed)."""

@@ -117,13 +117,14 @@ def test_rmsnorm_q8_is_decided_by_h_and_w_alone():
     h = sig.repeat_interleave(128) / 256
     w = sig.repeat(128) / 128
     for top in (255.0, 201.0, 129.0):
-        X = torch.cat([h, -h, torch.tensor([top]), torch.zeros(7)]).to(torch.bfloat16).view(1, -1).cuda()
-        wt = torch.cat([w, w, torch.ones(8)]).to(torch.bfloat16).cuda()
-        X = torch.cat([X, X * 2.0 ** -7, X * 2.0 ** 60, X * 2.0 ** -90]).contiguous()
-        X[1, -8] = top / 64
-        Q, _, _, _, _ = ops.rmsnorm_q8(X, wt, EPS)
-        q, _ = P.quantise(X.double() * wt.double())
-        assert torch.equal(Q, q)
+        for sign in (1, -1):
+            X = torch.cat([sign * h, torch.tensor([top]), torch.zeros(7)]).to(torch.bfloat16).view(1, -1).cuda()
+            wt = torch.cat([w, torch.ones(8)]).to(torch.bfloat16).cuda()
+            X = torch.cat([X, X * 2.0 ** -7, X * 2.0 ** 60, X * 2.0 ** -90]).contiguous()
+            X[1, -8] = top / 64
+            Q, _, _, _, _ = ops.rmsnorm_q8(X, wt, EPS)
+            q, _ = P.quantise(X.double() * wt.double())
+            assert torch.equal(Q, q)
 
 
 def test_rmsnorm_not_finite_and_huge():

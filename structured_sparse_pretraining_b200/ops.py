@@ -263,25 +263,40 @@ def bwd_dw_masked_noalloc(dY, X, meta, dW_vals):
     return dW_vals
 
 
-def _call_on(first, name, *args, others=()):
-    """Call an entry point on the device of `first` (current or not) and that
-    device's current stream; every tensor of the call must be there."""
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}: one device is needed")
-    with torch.cuda.device(first.device):
-        return _lib.call(name, *args, _stream())
-
-
-def _matrix(t, dtype, name, shape=None):
+# The calls below may be a few microseconds of GPU work each, so their checks
+# take the short way when everything fits: one comparison chain per tensor, and
+# the long way, with its message, only for what does not.
+def _fit(t, dtype, name, shape, dev):
+    """t as a contiguous CUDA tensor of `dtype` and `shape` on device `dev`, or an error."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
     _need(t, dtype, name, shape)
-    if t.dim() != 2:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected two dimensions")
-    return t
+    raise ValueError(f"{name} is on {t.device}: every tensor of a call must be on one device")
 
 
-def _out(t, shape, dtype, name, like):
-    return _empty(shape, dtype, like) if t is None else _need(t, dtype, name, shape)
+def _rows(t, dtype, name):
+    """(rows, columns) of a contiguous two-dimensional CUDA tensor."""
+    if t is not None and t.dtype is dtype and t.is_cuda and t.dim() == 2 and t.is_contiguous():
+        return t.shape
+    _need(t, dtype, name)
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected two dimensions")
+
+
+def _out(t, dtype, name, shape, like, dev):
+    """(output tensor, pointer): the given one, checked, or a new one."""
+    if t is None:  # empty_like of a contiguous tensor is the cheapest allocation torch has
+        t = torch.empty_like(like) if like.dtype is dtype and like.shape == shape else like.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
+    return t, _fit(t, dtype, name, shape, dev)
+
+
+def _call_on(dev, name, *args):
+    """Call an entry point on device `dev` (current or not) and its current stream."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch.cuda.current_device():
+        return _lib.call(name, *args, stream)
+    with torch.cuda.device(dev):
+        return _lib.call(name, *args, stream)
 
 
 def rmsnorm(X, w, eps, res=None, with_rstd=False, H=None, Y=None, rstd=None):
@@ -301,19 +316,23 @@ def rmsnorm_q8(X, w, eps, res=None, with_y=False, with_rstd=False, H=None, Y=Non
 
 
 def _rmsnorm(X, w, eps, res, with_y, with_q8, with_rstd, H, Y, Q, qscale, rstd):
-    T, D = _matrix(X, torch.bfloat16, "X").shape
-    _need(w, torch.bfloat16, "w", (D,))
+    shape = T, D = _rows(X, torch.bfloat16, "X")
+    dev = X.get_device()
+    pw = _fit(w, torch.bfloat16, "w", (D,), dev)
+    pe = ph = py = pq = ps = pr = None
     if res is not None:
-        _need(res, torch.bfloat16, "res", (T, D))
-        H = _out(H, (T, D), torch.bfloat16, "H", X)
+        pe = _fit(res, torch.bfloat16, "res", shape, dev)
+        H, ph = _out(H, torch.bfloat16, "H", shape, X, dev)
     elif H is not None:
         raise ValueError("H without res (H would be X)")
-    Y = _out(Y, (T, D), torch.bfloat16, "Y", X) if with_y else None
-    Q = _out(Q, (T, D), torch.int8, "Q", X) if with_q8 else None
-    qscale = _out(qscale, (T,), torch.float32, "qscale", X) if with_q8 else None
-    rstd = _out(rstd, (T,), torch.float32, "rstd", X) if with_rstd or rstd is not None else None
-    _call_on(X, "slope_rmsnorm", _ptr(X), _ptr(res), _ptr(w), T, D, float(eps), _ptr(H), _ptr(Y), _ptr(Q), _ptr(qscale),
-             _ptr(rstd), others=(res, w, H, Y, Q, qscale, rstd))
+    if with_y:
+        Y, py = _out(Y, torch.bfloat16, "Y", shape, X, dev)
+    if with_q8:
+        Q, pq = _out(Q, torch.int8, "Q", shape, X, dev)
+        qscale, ps = _out(qscale, torch.float32, "qscale", (T,), X, dev)
+    if with_rstd or rstd is not None:
+        rstd, pr = _out(rstd, torch.float32, "rstd", (T,), X, dev)
+    _call_on(dev, "slope_rmsnorm", X.data_ptr(), pe, pw, T, D, eps, ph, py, pq, ps, pr)
     return Q, qscale, Y, H, rstd
 
 
@@ -321,29 +340,29 @@ def rmsnorm_bwd(dY, H, w, rstd, dres=None, dH=None, dw=None):
     """(dH, dw): gradients of rmsnorm's Y with respect to h (X and res both
     take dH; dres, the gradient reaching h along the residual stream, is added)
     [T, D] bf16 and to w [D] fp32.  H is rmsnorm's (or X without a residual)."""
-    T, D = _matrix(dY, torch.bfloat16, "dY").shape
-    _need(H, torch.bfloat16, "H", (T, D))
-    _need(w, torch.bfloat16, "w", (D,))
-    _need(rstd, torch.float32, "rstd", (T,))
-    if dres is not None:
-        _need(dres, torch.bfloat16, "dres", (T, D))
-    dH = _out(dH, (T, D), torch.bfloat16, "dH", dY)
-    dw = _out(dw, (D,), torch.float32, "dw", dY)
+    shape = T, D = _rows(dY, torch.bfloat16, "dY")
+    dev = dY.get_device()
+    ph = _fit(H, torch.bfloat16, "H", shape, dev)
+    pw = _fit(w, torch.bfloat16, "w", (D,), dev)
+    pr = _fit(rstd, torch.float32, "rstd", (T,), dev)
+    pe = None if dres is None else _fit(dres, torch.bfloat16, "dres", shape, dev)
+    dH, pdh = _out(dH, torch.bfloat16, "dH", shape, dY, dev)
+    dw, pdw = _out(dw, torch.float32, "dw", (D,), dY, dev)
     floats = ctypes.c_int64(0)
     _lib.call("slope_rmsnorm_bwd_ws", T, D, ctypes.byref(floats))
-    ws = _empty((floats.value,), torch.float32, dY)
-    _call_on(dY, "slope_rmsnorm_bwd", _ptr(dY), _ptr(H), _ptr(w), _ptr(rstd), _ptr(dres), T, D, _ptr(dH), _ptr(dw), _ptr(ws),
-             floats.value, others=(H, w, rstd, dres, dH, dw))
+    ws = dY.new_empty((floats.value,), dtype=torch.float32)
+    _call_on(dev, "slope_rmsnorm_bwd", dY.data_ptr(), ph, pw, pr, pe, T, D, pdh, pdw, ws.data_ptr(), floats.value)
     return dH, dw
 
 
 def quant_rows(A, Q=None, scale=None):
     """(Q, scale): rows of A [rows, K] bf16 in int8 with one fp32 scale per row
     (the kept weights of prune24: one per output channel)."""
-    rows, K = _matrix(A, torch.bfloat16, "A").shape
-    Q = _out(Q, (rows, K), torch.int8, "Q", A)
-    scale = _out(scale, (rows,), torch.float32, "scale", A)
-    _call_on(A, "slope_quant_rows", _ptr(A), rows, K, _ptr(Q), _ptr(scale), others=(Q, scale))
+    shape = rows, K = _rows(A, torch.bfloat16, "A")
+    dev = A.get_device()
+    Q, pq = _out(Q, torch.int8, "Q", shape, A, dev)
+    scale, ps = _out(scale, torch.float32, "scale", (rows,), A, dev)
+    _call_on(dev, "slope_quant_rows", A.data_ptr(), rows, K, pq, ps)
     return Q, scale
 
 
@@ -352,21 +371,21 @@ def fwd_q8(Xq, xscale, vals_q, wscale, meta, XL, R, out_features, Y=None):
     Xq [T, in] and xscale [T] from rmsnorm_q8 or quant_rows, and vals_q
     [out, in/2], wscale [out] the kept weights through quant_rows (XL, R None:
     no adapter)."""
-    T, in_ = _matrix(Xq, torch.int8, "Xq").shape
-    _need(xscale, torch.float32, "xscale", (T,))
-    _need(vals_q, torch.int8, "vals_q", (out_features, in_ // 2))
-    _need(wscale, torch.float32, "wscale", (out_features,))
-    _need(meta, torch.int16, "meta", (out_features, in_ // 16))
-    r = 0
+    T, in_ = _rows(Xq, torch.int8, "Xq")
+    dev = Xq.get_device()
+    ps = _fit(xscale, torch.float32, "xscale", (T,), dev)
+    pv = _fit(vals_q, torch.int8, "vals_q", (out_features, in_ // 2), dev)
+    pws = _fit(wscale, torch.float32, "wscale", (out_features,), dev)
+    pm = _fit(meta, torch.int16, "meta", (out_features, in_ // 16), dev)
+    r, px, pr = 0, None, None
     if R is not None:
-        r = _matrix(R, torch.bfloat16, "R").shape[0]
-        _need(R, torch.bfloat16, "R", (r, out_features))
-        _need(XL, torch.bfloat16, "XL", (T, r))
+        r = _rows(R, torch.bfloat16, "R")[0]
+        pr = _fit(R, torch.bfloat16, "R", (r, out_features), dev)
+        px = _fit(XL, torch.bfloat16, "XL", (T, r), dev)
     elif XL is not None:
         raise ValueError("XL without R")
-    Y = _out(Y, (T, out_features), torch.bfloat16, "Y", Xq)
-    _call_on(Xq, "slope_fwd_q8", _ptr(Xq), _ptr(xscale), _ptr(vals_q), _ptr(wscale), _ptr(meta), _ptr(XL) if r else None,
-             _ptr(R) if r else None, T, in_, out_features, r, _ptr(Y), others=(xscale, vals_q, wscale, meta, XL, R, Y))
+    Y, py = _out(Y, torch.bfloat16, "Y", (T, out_features), Xq, dev)
+    _call_on(dev, "slope_fwd_q8", Xq.data_ptr(), ps, pv, pws, pm, px, pr, T, in_, out_features, r, py)
     return Y
 
 

@@ -1,0 +1,320 @@
+// gemm_q8_wide.cuh -- the int8 2:4 product at many tokens, on pairs of SMs
+// with two row blocks per CTA (see gemm_q8.cuh for the product and the codes,
+// gemm_wide.cuh for why two blocks share the token operand).
+//
+// Pair tile: 512 output channels x 224 tokens.  A k-tile is 256 dense
+// positions: per CTA two blocks of 128 rows x 128 kept int8 (32 KB), 112 token
+// rows x 256 int8 (28 KB) and the codes (8 KB), for 2 x 4 sparse MMAs of
+// M256 N224 K64.  Codes go from the stage straight into TMEM (tcgen05.cp); the
+// code columns of stage s are written again only after the stage was refilled,
+// that is after the MMAs that read them.
+//
+// TMEM: 2 x 224 columns of integers and 24 to 48 of codes leave no room for
+// the adapter's fp32 accumulator.  So with an adapter the epilogue turns the
+// integers into scaled fp32 in place (float(acc) xscale wscale), the rank-r
+// bf16 MMAs then accumulate onto that, and the result is read and rounded
+// once.
+//
+// Roles (320 threads): warp 0 operand producer, warp 1 TMEM owner and (pair
+// leader) MMA issuer, warps 2..5 epilogue of block 0, warps 6..9 of block 1.
+// An epilogue warp takes its 32 channels x 224 tokens into registers as bf16
+// pairs, releases the accumulator, and only then transposes and stores, beside
+// the next tile's MMAs.  Row blocks past the end start at M - 128 instead and
+// store only their own rows, so that every code read is a legal one.
+#pragma once
+#include <cstdint>
+#include "gemm_q8.cuh"
+
+namespace slope {
+
+struct Q8WideCfg {
+    static constexpr int BN = 224, BNH = 112;
+    static constexpr int NBLK = 2, TILE_M = 512;
+    static constexpr int A_BYTES = 16384;
+    static constexpr int B_PANEL = BNH * 128;
+    static constexpr int E_BYTES = 4096;
+    static constexpr int STAGE_BYTES = NBLK * A_BYTES + 2 * B_PANEL + NBLK * E_BYTES;
+    static constexpr int NS = 3;
+    static constexpr int STAGING_BYTES = 8 * 2048;  // a 32 x 32 bf16 transpose tile per epilogue warp
+    static constexpr int E_COL = NBLK * BN;         // 8 columns per block and stage
+    static constexpr int TMEM_COLS = 512;
+    static constexpr int SMEM_BYTES = NS * STAGE_BYTES + STAGING_BYTES + 256 + 1024;
+    static_assert(E_COL + 8 * NBLK * NS <= TMEM_COLS, "TMEM budget");
+    static_assert(256 >= 8 * (2 * NS + 3 + NBLK) + 8, "barrier area");
+    static_assert(STAGE_BYTES % 1024 == 0 && B_PANEL % 1024 == 0, "swizzle-atom alignment");
+    static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+};
+
+struct Q8WideParams {
+    int M, T, K, r;
+    int m_tiles, n_tiles, raster_g, num_work;
+    const float *xscale, *wscale;
+    uint16_t *Y;
+};
+
+__global__ void __launch_bounds__(320, 1)
+    q8_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmR,
+                   const __grid_constant__ CUtensorMap tmXL, const __grid_constant__ Q8WideParams p) {
+    using C = Q8WideCfg;
+    constexpr int NS = C::NS, BN = C::BN, BNH = C::BNH, NBLK = C::NBLK;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *staging = smem + NS * C::STAGE_BYTES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(staging + C::STAGING_BYTES);  // leader: both CTAs' bytes
+    uint64_t *empty = full + NS;         // each CTA: stage s may be refilled
+    uint64_t *acc_full = empty + NS;     // each CTA: the integer sums are complete
+    uint64_t *conv = acc_full + 1;       // leader: both CTAs' accumulators hold scaled fp32 (16 arrivals)
+    uint64_t *adp_full = conv + 1;       // each CTA: the adapter is added
+    uint64_t *acc_empty = adp_full + 1;  // leader, per block: both CTAs drained it (8 arrivals)
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(acc_empty + NBLK);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+    const int kts = (p.K + 255) >> 8, adp_kts = (p.r + 63) >> 6;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(conv, 16);
+        mbar_init(adp_full, 1);
+        for (int b = 0; b < NBLK; ++b) mbar_init(&acc_empty[b], 8);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmE);
+        if (p.r > 0) {
+            tma_prefetch_desc(&tmR);
+            tma_prefetch_desc(&tmXL);
+        }
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_holder, C::TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the peer's barriers are initialised before any remote arrive
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    grid_dep_wait();
+    grid_dep_launch();
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ operand producer (both CTAs)
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0;
+            for (int w = pair; w < p.num_work; w += num_pairs) {
+                int mt, nt;
+                grouped_tile(w, p.m_tiles, p.n_tiles, p.raster_g, mt, nt);
+                int m0[NBLK];
+#pragma unroll
+                for (int blk = 0; blk < NBLK; ++blk) m0[blk] = min(mt * C::TILE_M + 256 * blk + 128 * (int)rank, p.M - 128);
+                const int n0 = nt * BN + BNH * (int)rank;
+                for (int kt = 0; kt < kts + adp_kts; ++kt) {
+                    if (!mbar_wait(&empty[s], ph ^ 1, abort_flag)) goto done;
+                    uint8_t *a = smem + s * C::STAGE_BYTES;
+                    uint8_t *b = a + NBLK * C::A_BYTES;
+                    uint8_t *e = b + 2 * C::B_PANEL;
+                    const uint32_t lead_full = cluster_addr(&full[s], 0);
+                    if (kt < kts) {
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
+#pragma unroll
+                        for (int blk = 0; blk < NBLK; ++blk) {
+                            tma_load_2d_pair(a + blk * C::A_BYTES, &tmA, lead_full, kt * 128, m0[blk]);
+                            tma_load_2d_pair(e + blk * C::E_BYTES, &tmE, lead_full, kt * 16, m0[blk]);
+                        }
+                        tma_load_2d_pair(b, &tmB, lead_full, kt * 256, n0);
+                        tma_load_2d_pair(b + C::B_PANEL, &tmB, lead_full, kt * 256 + 128, n0);
+                    } else {  // adapter: R^T (MN-major, two panels of 64 channels per block) and XL, 64 of the rank
+                        const int j0 = (kt - kts) * 64;
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (NBLK * C::A_BYTES + C::B_PANEL));
+#pragma unroll
+                        for (int blk = 0; blk < NBLK; ++blk) {
+                            tma_load_2d_pair(a + blk * C::A_BYTES, &tmR, lead_full, m0[blk], j0);
+                            tma_load_2d_pair(a + blk * C::A_BYTES + 8192, &tmR, lead_full, m0[blk] + 64, j0);
+                        }
+                        tma_load_2d_pair(b, &tmXL, lead_full, j0, n0);
+                    }
+                    if (++s == NS) { s = 0; ph ^= 1; }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (leader only)
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t IDESC_SP = instr_desc_sp_i8(256, BN);
+            constexpr uint32_t IDESC_AD = instr_desc(256, BN, 1, 0, 0);
+            const uint32_t base = smem_addr(smem);
+            const uint64_t a_desc0 = smem_desc(base, 16, 1024, SWZ_128B);
+            const uint64_t b_desc0 = smem_desc(base + NBLK * C::A_BYTES, 16, 1024, SWZ_128B);
+            const uint64_t e_desc0 = smem_desc(base + NBLK * C::A_BYTES + 2 * C::B_PANEL, 16, 256, SWZ_32B);
+            const uint64_t a2_desc0 = smem_desc(base, 8192, 1024, SWZ_128B);
+            int s = 0;
+            uint32_t ph = 0;
+            int it = 0;
+            for (int w = pair; w < p.num_work; w += num_pairs, ++it) {
+                for (int kt = 0; kt < kts; ++kt) {
+                    if (!mbar_wait(&full[s], ph, abort_flag)) goto done;
+                    tc_fence_after();
+                    const uint64_t off = (uint64_t)((s * C::STAGE_BYTES) >> 4);
+                    const uint32_t ecol = tmem_base + C::E_COL + 8 * NBLK * s;
+#pragma unroll
+                    for (int blk = 0; blk < NBLK; ++blk)
+                        tmem_cp_128x256b_pair(ecol + 8 * blk, e_desc0 + off + (uint64_t)((blk * C::E_BYTES) >> 4));
+                    const int nk = min(4, (p.K - kt * 256) >> 6);
+#pragma unroll
+                    for (int blk = 0; blk < NBLK; ++blk) {
+                        if (kt == 0) {
+                            if (!mbar_wait(&acc_empty[blk], (it & 1) ^ 1, abort_flag)) goto done;
+                            tc_fence_after();
+                        }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (c < nk)
+                                mma_sp_i8_pair(tmem_base + blk * BN, a_desc0 + off + (uint64_t)(((blk * C::A_BYTES) >> 4) + 2 * c),
+                                               b_desc0 + off + (uint64_t)(((c >> 1) * C::B_PANEL + (c & 1) * 64) >> 4),
+                                               ecol + 8 * blk + 2 * c, IDESC_SP, (kt > 0 || c > 0) ? 1u : 0u);
+                    }
+                    mma_commit_pair_both(&empty[s]);
+                    if (++s == NS) { s = 0; ph ^= 1; }
+                }
+                mma_commit_pair_both(acc_full);
+                if (adp_kts == 0) continue;
+                if (!mbar_wait(conv, it & 1, abort_flag)) goto done;
+                tc_fence_after();
+                for (int kt = 0; kt < adp_kts; ++kt) {
+                    if (!mbar_wait(&full[s], ph, abort_flag)) goto done;
+                    tc_fence_after();
+                    const uint64_t off = (uint64_t)((s * C::STAGE_BYTES) >> 4);
+                    const int nk = min(4, (p.r - kt * 64 + 15) >> 4);
+#pragma unroll
+                    for (int blk = 0; blk < NBLK; ++blk)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (c < nk)
+                                mma_bf16_pair(tmem_base + blk * BN, a2_desc0 + off + (uint64_t)(((blk * C::A_BYTES) >> 4) + 128 * c),
+                                              b_desc0 + off + (uint64_t)(2 * c), IDESC_AD, 1u);
+                    mma_commit_pair_both(&empty[s]);
+                    if (++s == NS) { s = 0; ph ^= 1; }
+                }
+                mma_commit_pair_both(adp_full);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue (both CTAs)
+        const int q = warp & 3, blk = (warp - 2) >> 2;
+        uint8_t *tile = staging + (warp - 2) * 2048;  // [32 tokens][32 channels] bf16
+        const int seg = lane & 3, rsub = lane >> 2, odd = lane & 1;
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + blk * BN;
+        constexpr int NCH = BN / 32;
+        int it = 0;
+        for (int w = pair; w < p.num_work; w += num_pairs, ++it) {
+            int mt, nt;
+            grouped_tile(w, p.m_tiles, p.n_tiles, p.raster_g, mt, nt);
+            const int own = mt * C::TILE_M + 256 * blk + 128 * (int)rank;  // the rows this block stores start here
+            const int m0 = min(own, p.M - 128) + 32 * q;                   // this warp's first channel
+            const int n0 = nt * BN;
+            const float ws = in_bounds(m0 + lane, 1, p.M) ? __ldg(p.wscale + m0 + lane) : 0.0f;
+            // the scales of four tokens (0 past the end)
+            auto xscale4 = [&](int t) {
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (t + 4 <= p.T) {
+                    if (in_bounds(t, 4, p.T)) x = __ldg(reinterpret_cast<const float4 *>(p.xscale + t));
+                } else {
+                    if (t < p.T) x.x = __ldg(p.xscale + t);
+                    if (t + 1 < p.T) x.y = __ldg(p.xscale + t + 1);
+                    if (t + 2 < p.T) x.z = __ldg(p.xscale + t + 2);
+                }
+                return x;
+            };
+            auto scaled = [&](uint32_t (&v)[32], int cc) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 x = xscale4(n0 + 32 * cc + j);
+                    v[j] = __float_as_uint((float)(int)v[j] * (x.x * ws));
+                    v[j + 1] = __float_as_uint((float)(int)v[j + 1] * (x.y * ws));
+                    v[j + 2] = __float_as_uint((float)(int)v[j + 2] * (x.z * ws));
+                    v[j + 3] = __float_as_uint((float)(int)v[j + 3] * (x.w * ws));
+                }
+            };
+            if (!mbar_wait_warp(acc_full, it & 1, abort_flag)) break;
+            tc_fence_after();
+            if (adp_kts > 0) {
+#pragma unroll 1
+                for (int cc = 0; cc < NCH; ++cc) {
+                    uint32_t v[32];
+                    tmem_ld_32x32(taddr + 32 * cc, v);
+                    tmem_ld_wait();
+                    scaled(v, cc);
+                    tmem_st_32x32(taddr + 32 * cc, v);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive(conv);
+                    else mbar_arrive_cluster(cluster_addr(conv, 0));
+                }
+                if (!mbar_wait_warp(adp_full, it & 1, abort_flag)) break;
+                tc_fence_after();
+            }
+            uint32_t out[NCH][16];  // bf16 pairs of neighbouring tokens, this lane's channel
+#pragma unroll
+            for (int cc = 0; cc < NCH; ++cc) {
+                uint32_t v[32];
+                tmem_ld_32x32(taddr + 32 * cc, v);
+                tmem_ld_wait();
+                if (adp_kts == 0) scaled(v, cc);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) out[cc][j] = pack_bf16x2(bits_to_f32(v[2 * j]), bits_to_f32(v[2 * j + 1]));
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (rank == 0) mbar_arrive(&acc_empty[blk]);
+                else mbar_arrive_cluster(cluster_addr(&acc_empty[blk], 0));
+            }
+            const bool m_ok = m0 + 8 * seg >= own && own < p.M;  // rows of the clamped overlap belong to the block before
+#pragma unroll
+            for (int cc = 0; cc < NCH; ++cc) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    // neighbouring lanes swap a token so that each holds two channels of one
+                    const uint32_t other = __shfl_xor_sync(0xffffffffu, out[cc][j], 1);
+                    const uint32_t pr = odd ? __byte_perm(other, out[cc][j], 0x7632) : __byte_perm(out[cc][j], other, 0x5410);
+                    *reinterpret_cast<uint32_t *>(tile + ((2 * j + odd) * 32 + (lane & ~1)) * 2) = pr;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int t = n0 + 32 * cc + 8 * g + rsub;
+                    const uint4 val = *reinterpret_cast<const uint4 *>(tile + ((8 * g + rsub) * 32 + seg * 8) * 2);
+                    const int64_t at = (int64_t)t * p.M + m0 + seg * 8;
+                    if (m_ok && t < p.T && in_bounds(at, 8, (int64_t)p.T * p.M)) *reinterpret_cast<uint4 *>(p.Y + at) = val;
+                }
+                __syncwarp();  // every lane has read the tile before the next chunk overwrites it
+            }
+        }
+    }
+done:
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while its peer may still signal it
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    }
+}
+
+}  // namespace slope

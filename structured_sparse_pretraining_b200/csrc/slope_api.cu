@@ -17,6 +17,7 @@
 #include "gemm.cuh"
 #include "gemm_pair.cuh"
 #include "gemm_q8.cuh"
+#include "gemm_q8_wide.cuh"
 #include "gemm_wide.cuh"
 #include "prune.cuh"
 #include "rownorm.cuh"
@@ -1706,6 +1707,7 @@ int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, 
 
 namespace {
 // ------------------------------------------------------------------ int8 sparse product
+constexpr int Q8_WIDE_SLOT = 42;      // its entry in launch_clusters' table
 constexpr int64_t Q8_MAX_K = 131072;  // 128 * 128 * K / 2 stays below 2^31
 
 // Opt in to `bytes` of dynamic shared memory once per device.
@@ -1724,6 +1726,7 @@ struct Q8Plan {
     int bn;      // 0: CUDA cores, else the token width of the tensor-core tile
     int splits;  // CTAs that share a tile's sum over K (or warps a group of channels, on CUDA cores)
     int tb;      // CUDA cores: tokens per pass
+    bool wide;   // q8_wide_kernel: 512 x 224 pair tiles
 };
 
 Q8Plan pick_q8_plan(int64_t M, int64_t T, int64_t K, int sms) {
@@ -1734,12 +1737,13 @@ Q8Plan pick_q8_plan(int64_t M, int64_t T, int64_t K, int sms) {
         // warps share a group of channels while there are fewer groups than warps on the GPU
         int ks = 1;
         while (ks < slope::SQ8_WARPS && M / slope::SQ8_ROWS * ks * 2 <= (int64_t)sms * slope::SQ8_WARPS && ks * 1024 < K) ks *= 2;
-        return Q8Plan{0, ks, tb};
+        return Q8Plan{0, ks, tb, false};
     }
+    if (T >= 1024 && K % 128 == 0) return Q8Plan{224, 1, 0, true};
     const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
     const int64_t kts = (K + 255) / 256, tiles = (M + 127) / 128 * ((T + bn - 1) / bn);
     const int64_t slots = (int64_t)sms * (bn <= 64 ? 2 : 1);
-    Q8Plan best{bn, 1, 0};
+    Q8Plan best{bn, 1, 0, false};
     double best_cost = 1e300;
     for (int s = 1; s <= 8 && s <= kts; s *= 2) {
         const double cost = (double)((tiles * s + slots - 1) / slots) * ((double)((kts + s - 1) / s) + 4.0) + 0.5 * (s > 1 ? s : 0);
@@ -1823,8 +1827,9 @@ int q8_product(const int8_t *X, const float *xscale, const int8_t *W, const floa
     p.xscale = xscale;
     p.wscale = wscale;
     p.Y = Y;
+    const int box_t = plan.wide ? slope::Q8WideCfg::BNH : plan.bn;  // token rows of a TMA box
     if (int rc = make_map_i8(a, W, M, K / 2, 128, 128)) return rc;
-    if (int rc = make_map_i8(b, X, T, K, 128, plan.bn)) return rc;
+    if (int rc = make_map_i8(b, X, T, K, 128, box_t)) return rc;
     e = a;  // unused maps are copies of a valid one
     r2 = a;
     xl = a;
@@ -1832,7 +1837,19 @@ int q8_product(const int8_t *X, const float *xscale, const int8_t *W, const floa
         if (int rc = make_map(e, meta, M, K / 16, K / 16, 16, 128, 32, false)) return rc;
     if (r > 0) {
         if (int rc = make_map(r2, R, r, M, M, 64, 64)) return rc;
-        if (int rc = make_map(xl, XL, T, r, r, 64, plan.bn)) return rc;
+        if (int rc = make_map(xl, XL, T, r, r, 64, box_t)) return rc;
+    }
+    if (plan.wide) {
+        using C = slope::Q8WideCfg;
+        slope::Q8WideParams wp{p.M, p.T, p.K, p.r};
+        wp.m_tiles = (p.M + C::TILE_M - 1) / C::TILE_M;
+        wp.n_tiles = (p.T + C::BN - 1) / C::BN;
+        wp.raster_g = wide_raster_group(wp.m_tiles, d.sms);
+        wp.num_work = wp.m_tiles * wp.n_tiles;
+        wp.xscale = xscale;
+        wp.wscale = wscale;
+        wp.Y = Y;
+        return launch_pairs(slope::q8_wide_kernel, Q8_WIDE_SLOT, 320, C::SMEM_BYTES, wp.num_work, d.sms, st, a, b, e, r2, xl, wp);
     }
     switch (plan.bn) {
         case 16: return launch_q8_tile<16>(a, b, e, r2, xl, p, st);

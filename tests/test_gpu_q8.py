@@ -237,6 +237,9 @@ PRODUCT = [
     (16, 36864, 256, 96), (8, 131072, 128, 8), (48, 16384, 384, 8), (100, 8192, 128, 64), (12, 2048, 128, 0),
     # many tiles
     (24, 512, 40000, 8), (700, 1024, 5120, 96), (2100, 1536, 2048, 16), (4096, 512, 512, 8),
+    # 512 x 224 pair tiles: ragged in channels (clamped blocks), tokens and the sum; every count of adapter k-tiles
+    (5000, 128, 128, 0), (4100, 256, 192, 8), (2300, 640, 1088, 256), (1792, 1024, 2560, 96), (3001, 1408, 832, 136), (2048, 2048, 4096, 0),
+    (9000, 384, 704, 64),
 ]
 
 

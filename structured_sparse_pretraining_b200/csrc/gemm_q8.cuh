@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(224)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *partial = reinterpret_cast<int *>(smem);  // [BN tokens][128 channels], after the ring is done
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int S = p.splits;
     const int rank = S > 1 ? (int)cluster_ctarank() : 0;
     const int tile = blockIdx.x / S;
@@ -158,50 +158,48 @@ __global__ void __launch_bounds__(224)
             }
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t IDESC_SP = instr_desc_sp_i8(128, BN);
-            constexpr uint32_t IDESC_AD = instr_desc(128, BN, 1, 0, 0);
-            const uint32_t base = smem_addr(smem);
-            const uint64_t a_desc0 = smem_desc(base, 16, 1024, SWZ_128B);
-            const uint64_t b_desc0 = smem_desc(base + C::A_BYTES, 16, 1024, SWZ_128B);
-            const uint64_t e_desc0 = smem_desc(base + C::A_BYTES + 2 * C::B_PANEL, 16, 256, SWZ_32B);
-            const uint64_t a2_desc0 = smem_desc(base, 8192, 1024, SWZ_128B);
-            int s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int kt = k0; kt < k1 + adp_kts; ++kt) {
-                if (!mbar_wait(&full[s], ph, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t off = (uint64_t)((s * C::STAGE_BYTES) >> 4);
-                if (kt < k1) {
-                    // the code columns of stage s: their last readers finished before the stage was refilled
-                    const uint32_t ecol = tmem_base + C::E_COL + 8 * s;
-                    tmem_cp_128x256b(ecol, e_desc0 + off);
-                    const int nblk = min(4, (p.K - kt * 256) >> 6);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (c < nblk)
-                            mma_sp_i8(tmem_base, a_desc0 + off + (uint64_t)(2 * c),
-                                      b_desc0 + off + (uint64_t)(((c >> 1) * C::B_PANEL + (c & 1) * 64) >> 4), ecol + 2 * c,
-                                      IDESC_SP, (kt > k0 || c > 0) ? 1u : 0u);
-                } else {
-                    const int j0 = (kt - k1) * 64;
-                    const int nblk = min(4, (p.r - j0 + 15) >> 4);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (c < nblk)
-                            mma_bf16(tmem_base + C::ADP_COL, a2_desc0 + off + (uint64_t)(128 * c),
-                                     b_desc0 + off + (uint64_t)(2 * c), IDESC_AD, (j0 > 0 || c > 0) ? 1u : 0u);
-                }
-                mma_commit(&empty[s]);
-                if (++s == NS) { s = 0; ph ^= 1; }
+        // ------------------------------------------------------------ MMA issuer (the whole warp, one lane elected)
+        constexpr uint32_t IDESC_SP = instr_desc_sp_i8(128, BN);
+        constexpr uint32_t IDESC_AD = instr_desc(128, BN, 1, 0, 0);
+        const uint32_t base = smem_addr(smem);
+        const uint64_t a_desc0 = smem_desc(base, 16, 1024, SWZ_128B);
+        const uint64_t b_desc0 = smem_desc(base + C::A_BYTES, 16, 1024, SWZ_128B);
+        const uint64_t e_desc0 = smem_desc(base + C::A_BYTES + 2 * C::B_PANEL, 16, 256, SWZ_32B);
+        const uint64_t a2_desc0 = smem_desc(base, 8192, 1024, SWZ_128B);
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int kt = k0; kt < k1 + adp_kts; ++kt) {
+            if (!mbar_wait_warp(&full[s], ph, abort_flag)) {
+                ok = false;
+                break;
             }
-            if (ok) mma_commit(acc_full);
+            tc_fence_after();
+            const uint64_t off = (uint64_t)((s * C::STAGE_BYTES) >> 4);
+            if (kt < k1) {
+                // the code columns of stage s: their last readers finished before the stage was refilled
+                const uint32_t ecol = tmem_base + C::E_COL + 8 * s;
+                elect_cp_128x256b<false>(ecol, e_desc0 + off);
+                const int nblk = min(4, (p.K - kt * 256) >> 6);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c < nblk)
+                        elect_mma_sp_i8<false>(tmem_base, a_desc0 + off + (uint64_t)(2 * c),
+                                               b_desc0 + off + (uint64_t)(((c >> 1) * C::B_PANEL + (c & 1) * 64) >> 4),
+                                               ecol + 2 * c, IDESC_SP, (kt > k0 || c > 0) ? 1u : 0u);
+            } else {
+                const int j0 = (kt - k1) * 64;
+                const int nblk = min(4, (p.r - j0 + 15) >> 4);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c < nblk)
+                        elect_mma_bf16<false>(tmem_base + C::ADP_COL, a2_desc0 + off + (uint64_t)(128 * c),
+                                              b_desc0 + off + (uint64_t)(2 * c), IDESC_AD, (j0 > 0 || c > 0) ? 1u : 0u);
+            }
+            elect_commit<false>(&empty[s]);
+            if (++s == NS) { s = 0; ph ^= 1; }
         }
+        if (ok) elect_commit<false>(acc_full);
     } else if (warp < 6) {
         // ------------------------------------------------------------ epilogue, first part
         const int q = warp & 3;

@@ -40,7 +40,7 @@ struct Q8WideCfg {
     static constexpr int TMEM_COLS = 512;
     static constexpr int SMEM_BYTES = NS * STAGE_BYTES + STAGING_BYTES + 256 + 1024;
     static_assert(E_COL + 8 * NBLK * NS <= TMEM_COLS, "TMEM budget");
-    static_assert(256 >= 8 * (2 * NS + 3 + NBLK) + 8, "barrier area");
+    static_assert(256 >= 8 * (2 * NS + 1 + 3 * NBLK) + 8, "barrier area");
     static_assert(STAGE_BYTES % 1024 == 0 && B_PANEL % 1024 == 0, "swizzle-atom alignment");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -63,14 +63,14 @@ __global__ void __launch_bounds__(320, 1)
     uint8_t *staging = smem + NS * C::STAGE_BYTES;
     uint64_t *full = reinterpret_cast<uint64_t *>(staging + C::STAGING_BYTES);  // leader: both CTAs' bytes
     uint64_t *empty = full + NS;         // each CTA: stage s may be refilled
-    uint64_t *acc_full = empty + NS;     // each CTA: the integer sums are complete
-    uint64_t *conv = acc_full + 1;       // leader: both CTAs' accumulators hold scaled fp32 (16 arrivals)
-    uint64_t *adp_full = conv + 1;       // each CTA: the adapter is added
-    uint64_t *acc_empty = adp_full + 1;  // leader, per block: both CTAs drained it (8 arrivals)
+    uint64_t *acc_full = empty + NS;        // each CTA: the integer sums are complete
+    uint64_t *conv = acc_full + 1;          // per block: leader: both CTAs' sums are scaled fp32 (8 arrivals)
+    uint64_t *adp_full = conv + NBLK;       // per block: each CTA: the adapter is added
+    uint64_t *acc_empty = adp_full + NBLK;  // per block: leader: both CTAs drained it (8 arrivals)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(acc_empty + NBLK);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
     const int kts = (p.K + 255) >> 8, adp_kts = (p.r + 63) >> 6;
@@ -81,9 +81,11 @@ __global__ void __launch_bounds__(320, 1)
             mbar_init(&empty[s], 1);
         }
         mbar_init(acc_full, 1);
-        mbar_init(conv, 16);
-        mbar_init(adp_full, 1);
-        for (int b = 0; b < NBLK; ++b) mbar_init(&acc_empty[b], 8);
+        for (int b = 0; b < NBLK; ++b) {
+            mbar_init(&conv[b], 8);
+            mbar_init(&adp_full[b], 1);
+            mbar_init(&acc_empty[b], 8);
+        }
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -150,8 +152,8 @@ __global__ void __launch_bounds__(320, 1)
             }
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer (leader only)
-        if (rank == 0 && lane == 0) {
+        // ------------------------------------------------------------ MMA issuer (leader's whole warp, one lane elected)
+        if (rank == 0) {
             constexpr uint32_t IDESC_SP = instr_desc_sp_i8(256, BN);
             constexpr uint32_t IDESC_AD = instr_desc(256, BN, 1, 0, 0);
             const uint32_t base = smem_addr(smem);
@@ -162,52 +164,68 @@ __global__ void __launch_bounds__(320, 1)
             int s = 0;
             uint32_t ph = 0;
             int it = 0;
+            auto adapter = [&](int st, int blk, int kt) {
+                const uint64_t off = (uint64_t)((st * C::STAGE_BYTES) >> 4);
+                const int nk = min(4, (p.r - kt * 64 + 15) >> 4);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c < nk)
+                        elect_mma_bf16<true>(tmem_base + blk * BN, a2_desc0 + off + (uint64_t)(((blk * C::A_BYTES) >> 4) + 128 * c),
+                                             b_desc0 + off + (uint64_t)(2 * c), IDESC_AD, 1u);
+            };
             for (int w = pair; w < p.num_work; w += num_pairs, ++it) {
+                // (Running the first or last one to three k-tiles block by block, so that one block's drain overlaps
+                // the other's MMAs, was measured within 1% of this at 9216 -> 36864 and 1024 -> 4096.)
+                for (int blk = 0; blk < NBLK; ++blk)
+                    if (!mbar_wait_warp(&acc_empty[blk], (it & 1) ^ 1, abort_flag)) goto done;
+                tc_fence_after();
                 for (int kt = 0; kt < kts; ++kt) {
-                    if (!mbar_wait(&full[s], ph, abort_flag)) goto done;
+                    if (!mbar_wait_warp(&full[s], ph, abort_flag)) goto done;
                     tc_fence_after();
                     const uint64_t off = (uint64_t)((s * C::STAGE_BYTES) >> 4);
                     const uint32_t ecol = tmem_base + C::E_COL + 8 * NBLK * s;
 #pragma unroll
                     for (int blk = 0; blk < NBLK; ++blk)
-                        tmem_cp_128x256b_pair(ecol + 8 * blk, e_desc0 + off + (uint64_t)((blk * C::E_BYTES) >> 4));
+                        elect_cp_128x256b<true>(ecol + 8 * blk, e_desc0 + off + (uint64_t)((blk * C::E_BYTES) >> 4));
                     const int nk = min(4, (p.K - kt * 256) >> 6);
-#pragma unroll
-                    for (int blk = 0; blk < NBLK; ++blk) {
-                        if (kt == 0) {
-                            if (!mbar_wait(&acc_empty[blk], (it & 1) ^ 1, abort_flag)) goto done;
-                            tc_fence_after();
-                        }
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (c < nk)
-                                mma_sp_i8_pair(tmem_base + blk * BN, a_desc0 + off + (uint64_t)(((blk * C::A_BYTES) >> 4) + 2 * c),
-                                               b_desc0 + off + (uint64_t)(((c >> 1) * C::B_PANEL + (c & 1) * 64) >> 4),
-                                               ecol + 8 * blk + 2 * c, IDESC_SP, (kt > 0 || c > 0) ? 1u : 0u);
-                    }
-                    mma_commit_pair_both(&empty[s]);
-                    if (++s == NS) { s = 0; ph ^= 1; }
-                }
-                mma_commit_pair_both(acc_full);
-                if (adp_kts == 0) continue;
-                if (!mbar_wait(conv, it & 1, abort_flag)) goto done;
-                tc_fence_after();
-                for (int kt = 0; kt < adp_kts; ++kt) {
-                    if (!mbar_wait(&full[s], ph, abort_flag)) goto done;
-                    tc_fence_after();
-                    const uint64_t off = (uint64_t)((s * C::STAGE_BYTES) >> 4);
-                    const int nk = min(4, (p.r - kt * 64 + 15) >> 4);
 #pragma unroll
                     for (int blk = 0; blk < NBLK; ++blk)
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             if (c < nk)
-                                mma_bf16_pair(tmem_base + blk * BN, a2_desc0 + off + (uint64_t)(((blk * C::A_BYTES) >> 4) + 128 * c),
-                                              b_desc0 + off + (uint64_t)(2 * c), IDESC_AD, 1u);
-                    mma_commit_pair_both(&empty[s]);
+                                elect_mma_sp_i8<true>(tmem_base + blk * BN,
+                                                      a_desc0 + off + (uint64_t)(((blk * C::A_BYTES) >> 4) + 2 * c),
+                                                      b_desc0 + off + (uint64_t)(((c >> 1) * C::B_PANEL + (c & 1) * 64) >> 4),
+                                                      ecol + 8 * blk + 2 * c, IDESC_SP, (kt > 0 || c > 0) ? 1u : 0u);
+                    elect_commit<true>(&empty[s]);
                     if (++s == NS) { s = 0; ph ^= 1; }
                 }
-                mma_commit_pair_both(adp_full);
+                elect_commit<true>(acc_full);
+                if (adp_kts == 0) continue;
+                // block by block while the ring holds the whole adapter, else stage by stage
+                const int group = adp_kts <= NS ? adp_kts : 1;
+                for (int kt = 0; kt < adp_kts; kt += group) {
+                    const int s0 = s;
+#pragma unroll
+                    for (int blk = 0; blk < NBLK; ++blk) {
+                        if (kt == 0) {
+                            if (!mbar_wait_warp(&conv[blk], it & 1, abort_flag)) goto done;
+                            tc_fence_after();
+                        }
+                        int st = s0;
+                        for (int i = 0; i < group; ++i) {
+                            if (blk == 0) {
+                                if (!mbar_wait_warp(&full[s], ph, abort_flag)) goto done;
+                                tc_fence_after();
+                                if (++s == NS) { s = 0; ph ^= 1; }
+                            }
+                            adapter(st, blk, kt + i);
+                            if (blk == NBLK - 1) elect_commit<true>(&empty[st]);
+                            if (++st == NS) st = 0;
+                        }
+                        if (kt + group == adp_kts) elect_commit<true>(&adp_full[blk]);
+                    }
+                }
             }
         }
     } else {
@@ -225,22 +243,20 @@ __global__ void __launch_bounds__(320, 1)
             const int m0 = min(own, p.M - 128) + 32 * q;                   // this warp's first channel
             const int n0 = nt * BN;
             const float ws = in_bounds(m0 + lane, 1, p.M) ? __ldg(p.wscale + m0 + lane) : 0.0f;
-            // the scales of four tokens (0 past the end)
-            auto xscale4 = [&](int t) {
-                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (t + 4 <= p.T) {
-                    if (in_bounds(t, 4, p.T)) x = __ldg(reinterpret_cast<const float4 *>(p.xscale + t));
-                } else {
-                    if (t < p.T) x.x = __ldg(p.xscale + t);
-                    if (t + 1 < p.T) x.y = __ldg(p.xscale + t + 1);
-                    if (t + 2 < p.T) x.z = __ldg(p.xscale + t + 2);
-                }
-                return x;
-            };
-            auto scaled = [&](uint32_t (&v)[32], int cc) {
+            // the tile's token scales (0 past the end), through this warp's transpose tile: read from global
+            // memory chunk by chunk they cost most of the drain, beside 1 KB of L1 left by shared memory
+            float *xs = reinterpret_cast<float *>(tile);
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 x = xscale4(n0 + 32 * cc + j);
+            for (int cc = 0; cc < NCH; ++cc) {
+                const int t = n0 + 32 * cc + lane;
+                xs[32 * cc + lane] = t < p.T && in_bounds(t, 1, p.T) ? __ldg(p.xscale + t) : 0.0f;
+            }
+            __syncwarp();
+            // 16 columns of integer sums to scaled fp32
+            auto scaled = [&](uint32_t (&v)[16], int h) {
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(xs + 16 * h + j);
                     v[j] = __float_as_uint((float)(int)v[j] * (x.x * ws));
                     v[j + 1] = __float_as_uint((float)(int)v[j + 1] * (x.y * ws));
                     v[j + 2] = __float_as_uint((float)(int)v[j + 2] * (x.z * ws));
@@ -249,34 +265,36 @@ __global__ void __launch_bounds__(320, 1)
             };
             if (!mbar_wait_warp(acc_full, it & 1, abort_flag)) break;
             tc_fence_after();
+            uint32_t v[2][16];  // the next 16 columns are on their way while these are worked on
             if (adp_kts > 0) {
-#pragma unroll 1
-                for (int cc = 0; cc < NCH; ++cc) {
-                    uint32_t v[32];
-                    tmem_ld_32x32(taddr + 32 * cc, v);
+                tmem_ld_32x32_n(taddr, v[0]);
+#pragma unroll
+                for (int h = 0; h < 2 * NCH; ++h) {
                     tmem_ld_wait();
-                    scaled(v, cc);
-                    tmem_st_32x32(taddr + 32 * cc, v);
+                    if (h + 1 < 2 * NCH) tmem_ld_32x32_n(taddr + 16 * (h + 1), v[(h + 1) & 1]);
+                    scaled(v[h & 1], h);
+                    tmem_st_32x32_n(taddr + 16 * h, v[h & 1]);
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (rank == 0) mbar_arrive(conv);
-                    else mbar_arrive_cluster(cluster_addr(conv, 0));
+                    if (rank == 0) mbar_arrive(&conv[blk]);
+                    else mbar_arrive_cluster(cluster_addr(&conv[blk], 0));
                 }
-                if (!mbar_wait_warp(adp_full, it & 1, abort_flag)) break;
+                if (!mbar_wait_warp(&adp_full[blk], it & 1, abort_flag)) break;
                 tc_fence_after();
             }
             uint32_t out[NCH][16];  // bf16 pairs of neighbouring tokens, this lane's channel
+            tmem_ld_32x32_n(taddr, v[0]);
 #pragma unroll
-            for (int cc = 0; cc < NCH; ++cc) {
-                uint32_t v[32];
-                tmem_ld_32x32(taddr + 32 * cc, v);
+            for (int h = 0; h < 2 * NCH; ++h) {
                 tmem_ld_wait();
-                if (adp_kts == 0) scaled(v, cc);
+                if (h + 1 < 2 * NCH) tmem_ld_32x32_n(taddr + 16 * (h + 1), v[(h + 1) & 1]);
+                if (adp_kts == 0) scaled(v[h & 1], h);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) out[cc][j] = pack_bf16x2(bits_to_f32(v[2 * j]), bits_to_f32(v[2 * j + 1]));
+                for (int j = 0; j < 8; ++j)
+                    out[h >> 1][8 * (h & 1) + j] = pack_bf16x2(bits_to_f32(v[h & 1][2 * j]), bits_to_f32(v[h & 1][2 * j + 1]));
             }
             tc_fence_before();
             __syncwarp();
@@ -284,6 +302,7 @@ __global__ void __launch_bounds__(320, 1)
                 if (rank == 0) mbar_arrive(&acc_empty[blk]);
                 else mbar_arrive_cluster(cluster_addr(&acc_empty[blk], 0));
             }
+            __syncwarp();  // the scales have been read: the tile is free
             const bool m_ok = m0 + 8 * seg >= own && own < p.M;  // rows of the clamped overlap belong to the block before
 #pragma unroll
             for (int cc = 0; cc < NCH; ++cc) {

@@ -234,19 +234,6 @@ __device__ __forceinline__ void mma_sp_bf16(uint32_t d_tmem, uint64_t adesc, uin
         : "memory");
 }
 
-// Sparse int8 (kind::i8, signed, 32-bit integer accumulate, 64 dense K): the
-// codes are two TMEM columns at e_tmem, lane = row of A, the row's sixteen
-// 4-bit codes in ascending order, exactly as the compressed format stores them.
-__device__ __forceinline__ void mma_sp_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t e_tmem,
-                                          uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "tcgen05.mma.sp.cta_group::1.kind::i8 [%0], %1, %2, [%3], %4, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(e_tmem), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 // Arrive once on `bar` when every tcgen05 op issued so far by this thread is done.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -278,7 +265,15 @@ __device__ __forceinline__ void tmem_ld_32x32_x16(uint32_t taddr, uint32_t (&v)[
         : "r"(taddr)
         : "memory");
 }
-// The first 8 or 2 columns.
+// The first 16, 8 or 2 columns.
+__device__ __forceinline__ void tmem_ld_32x32_n(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_ld_32x32_n(uint32_t taddr, uint32_t (&v)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
@@ -296,15 +291,11 @@ __device__ __forceinline__ void tmem_st_32x32_x4(uint32_t taddr, uint32_t a, uin
                  "r"(c), "r"(d)
                  : "memory");
 }
-__device__ __forceinline__ void tmem_st_32x32(uint32_t taddr, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_st_32x32_n(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -315,10 +306,6 @@ __device__ __forceinline__ void tmem_cp_128x128b(uint32_t taddr, uint64_t sdesc)
     asm volatile("tcgen05.cp.cta_group::1.128x128b [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
-// 128 lanes x 256 bits (8 columns).
-__device__ __forceinline__ void tmem_cp_128x256b(uint32_t taddr, uint64_t sdesc) {
-    asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-}
 
 // ------------------------------------------------------------------ CTA pairs (cta_group::2)
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -397,18 +384,6 @@ __device__ __forceinline__ void mma_sp_bf16_pair(uint32_t d_tmem, uint64_t adesc
 __device__ __forceinline__ void tmem_cp_128x128b_pair(uint32_t taddr, uint64_t sdesc) {
     asm volatile("tcgen05.cp.cta_group::2.128x128b [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
-__device__ __forceinline__ void tmem_cp_128x256b_pair(uint32_t taddr, uint64_t sdesc) {
-    asm volatile("tcgen05.cp.cta_group::2.128x256b [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-}
-__device__ __forceinline__ void mma_sp_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t e_tmem,
-                                               uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "tcgen05.mma.sp.cta_group::2.kind::i8 [%0], %1, %2, [%3], %4, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(e_tmem), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
 __device__ __forceinline__ void mma_commit_pair(uint32_t cluster_bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(cluster_bar)
                  : "memory");
@@ -420,6 +395,66 @@ __device__ __forceinline__ void mma_commit_pair_both(const uint64_t *bar) {
                      smem_addr(bar)),
                  "h"(static_cast<uint16_t>(3))
                  : "memory");
+}
+
+// ------------------------------------------------------------------ tcgen05 issued by a converged warp
+// The same instructions for an issuing warp that stays converged, one elected
+// lane issuing each (elect.sync picks the same lane every time, as commit
+// needs).  With uniform control flow the descriptors stay in uniform
+// registers; inside a one-lane branch each instruction first moves them there,
+// and the issue of a sparse MMA of M256 N224 takes 144 cycles against 112 of
+// the tensor pipe (measured on resident operands; N = 32: 144 against 56).
+#define SLOPE_ELECT "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\t"
+// Sparse int8 (kind::i8, signed, 32-bit integer accumulate, 64 dense K): the
+// codes are two TMEM columns at e_tmem, lane = row of A, the row's sixteen
+// 4-bit codes in ascending order, exactly as the compressed format stores them.
+template <bool PAIR>
+__device__ __forceinline__ void elect_mma_sp_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t e_tmem,
+                                                uint32_t idesc, uint32_t accumulate) {
+    if (PAIR)
+        asm volatile(SLOPE_ELECT "setp.ne.b32 p, %5, 0;\n\t"
+                     "@q tcgen05.mma.sp.cta_group::2.kind::i8 [%0], %1, %2, [%3], %4, p;\n\t}" ::"r"(d_tmem),
+                     "l"(adesc), "l"(bdesc), "r"(e_tmem), "r"(idesc), "r"(accumulate)
+                     : "memory");
+    else
+        asm volatile(SLOPE_ELECT "setp.ne.b32 p, %5, 0;\n\t"
+                     "@q tcgen05.mma.sp.cta_group::1.kind::i8 [%0], %1, %2, [%3], %4, p;\n\t}" ::"r"(d_tmem),
+                     "l"(adesc), "l"(bdesc), "r"(e_tmem), "r"(idesc), "r"(accumulate)
+                     : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void elect_mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    if (PAIR)
+        asm volatile(SLOPE_ELECT "setp.ne.b32 p, %4, 0;\n\t"
+                     "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                     "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                     : "memory");
+    else
+        asm volatile(SLOPE_ELECT "setp.ne.b32 p, %4, 0;\n\t"
+                     "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                     "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                     : "memory");
+}
+// Copy 128 lanes x 256 bits (8 columns) from shared memory into TMEM.
+template <bool PAIR>
+__device__ __forceinline__ void elect_cp_128x256b(uint32_t taddr, uint64_t sdesc) {
+    if (PAIR) asm volatile(SLOPE_ELECT "@q tcgen05.cp.cta_group::2.128x256b [%0], %1;\n\t}" ::"r"(taddr), "l"(sdesc) : "memory");
+    else asm volatile(SLOPE_ELECT "@q tcgen05.cp.cta_group::1.128x256b [%0], %1;\n\t}" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+// Commit to `bar`; for a pair to the barrier at that offset in both CTAs.
+template <bool PAIR>
+__device__ __forceinline__ void elect_commit(const uint64_t *bar) {
+    if (PAIR)
+        asm volatile(SLOPE_ELECT
+                     "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+                         smem_addr(bar)),
+                     "h"(static_cast<uint16_t>(3))
+                     : "memory");
+    else
+        asm volatile(SLOPE_ELECT "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+                         smem_addr(bar))
+                     : "memory");
 }
 
 // ------------------------------------------------------------------ descriptors

@@ -1,4 +1,5 @@
-// gemm_q8.cuh -- the int8 2:4 product on tensor cores, 128 x BN tiles.
+// gemm_q8.cuh -- the int8 2:4 product on tensor cores at few tokens, where the
+// streaming of the weights bounds it: 128 x BN tiles.
 //
 //   Y[t][o] = xscale[t] wscale[o] (Xq . Wq^T)[t][o] + (XL . R)[t][o]
 //
@@ -15,13 +16,18 @@
 // issuer, warps 2..5 epilogue, warp 6 loads the codes where TMA cannot (rows
 // of K/8 bytes that are not a multiple of 16).
 //
-// One tile per CTA, or per cluster of `splits` CTAs that share the sum over K:
-// each leaves its integer partial in its own shared memory (the operand ring,
-// done by then), and after a cluster barrier every CTA adds all partials for
-// its share of the tokens over distributed shared memory.  So no workspace and
-// no atomics, and two launches can overlap; integer sums do not depend on the
-// split.  Row tiles past the end start at M - 128 instead, so that every code
-// the MMA reads is a legal one; K ends inside a k-tile after whole MMAs.
+// Persistent clusters of `splits` CTAs; the CTAs of a cluster share each
+// tile's sum over K, so that tiles can be handed out evenly whatever their
+// number (27648 channels are 216 tiles: two rounds for 148 single CTAs, a
+// quarter of the second idle, but three full ones for 74 clusters of two).
+// Each CTA finishes its share of the tile's tokens: the others push their
+// integer partials of that share into its shared memory (distributed shared
+// memory, one buffer per source), then it adds them to its own.  So no
+// workspace and no atomics, and launches can overlap; integer sums do not
+// depend on the split.  The integer accumulator is double-buffered: the next
+// tile's MMAs run beside the epilogue.  Row tiles past the end start at
+// M - 128 instead, so that every code the MMA reads is a legal one; K ends
+// inside a k-tile after whole MMAs.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -33,8 +39,8 @@ namespace slope {
 
 struct Q8Params {
     int M, T, K, r;        // output channels, tokens, dense K, adapter rank
-    int m_tiles;
-    int splits;            // CTAs per tile (the cluster size)
+    int m_tiles, num_work;
+    int splits;            // CTAs per cluster
     int meta_tma;          // 1: codes by TMA, 0: by warp 6
     const uint16_t *meta;  // [M x K/16]
     const float *xscale, *wscale;
@@ -42,22 +48,25 @@ struct Q8Params {
 };
 
 template <int BN>
-struct Q8TileCfg {
+struct Q8Cfg {
     static constexpr int A_BYTES = 16384;     // 128 rows x 128 stored int8
     static constexpr int B_PANEL = BN * 128;  // BN rows x 128 dense int8, 128-byte swizzle
     static constexpr int E_BYTES = 4096;      // 128 rows x 32 bytes of codes, 32-byte swizzle
     static constexpr int STAGE_BYTES = A_BYTES + 2 * B_PANEL + E_BYTES;
-    // two CTAs to an SM up to BN = 64, one above
-    static constexpr int NS = BN == 16 ? 4 : BN == 32 ? 3 : BN == 64 ? 3 : 4;
-    static constexpr int ADP_COL = BN;        // fp32 adapter accumulator
-    static constexpr int E_COL = 2 * BN;      // 8 columns per stage
-    static constexpr int TMEM_COLS = BN == 128 ? 512 : BN == 64 ? 256 : 128;
-    static constexpr int SMEM_BYTES = NS * STAGE_BYTES + 128 + 1024;
+    static constexpr int MAX_SPLITS = 8;
+    static constexpr int RED_BYTES = BN * 128 * 4 / MAX_SPLITS * (MAX_SPLITS - 1);  // partials of the other CTAs
+    static constexpr int XS_BYTES = BN * 4;   // a tile's token scales
+    static constexpr int BAR_BYTES = 256;
+    static constexpr int NS_RAW = (232448 - 1024 - BAR_BYTES - 2 * XS_BYTES - RED_BYTES) / STAGE_BYTES;
+    static constexpr int NS = NS_RAW > 8 ? 8 : NS_RAW;
+    static constexpr int ADP_COL = 2 * BN;    // fp32 adapter accumulator, after the two integer ones
+    static constexpr int E_COL = 3 * BN;      // 8 columns per stage
+    static constexpr int TMEM_COLS = BN == 128 ? 512 : BN >= 32 ? 256 : 128;
+    static constexpr int SMEM_BYTES = NS * STAGE_BYTES + RED_BYTES + 2 * XS_BYTES + BAR_BYTES + 1024;
     static_assert(E_COL + 8 * NS <= TMEM_COLS, "TMEM budget");
-    static_assert(BN * 128 * 4 <= NS * STAGE_BYTES, "partials fit the ring");
-    static_assert(128 >= 8 * (2 * NS + 1) + 8, "barrier area");
+    static_assert(BAR_BYTES >= 8 * (2 * NS + 6) + 8, "barrier area");
     static_assert(B_PANEL % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzle-atom alignment");
-    static_assert(SMEM_BYTES <= (BN <= 64 ? 115200 : 232448), "shared memory budget");
+    static_assert(NS >= 3 && SMEM_BYTES <= 232448, "shared memory budget");
 };
 
 // W token columns of one warp's 32 channels: v holds this lane's channel.
@@ -76,28 +85,29 @@ __device__ __forceinline__ void q8_store(const float (&v)[W], const Q8Params &p,
 }
 
 template <int BN>
-__global__ void __launch_bounds__(224)
+__global__ void __launch_bounds__(224, 1)
     q8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmR,
                    const __grid_constant__ CUtensorMap tmXL, const __grid_constant__ Q8Params p) {
-    using C = Q8TileCfg<BN>;
+    using C = Q8Cfg<BN>;
     constexpr int NS = C::NS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + NS * C::STAGE_BYTES);
+    uint32_t *red = reinterpret_cast<uint32_t *>(smem + NS * C::STAGE_BYTES);  // [source][token of the share][128 channels]
+    float *xs_buf = reinterpret_cast<float *>(smem + NS * C::STAGE_BYTES + C::RED_BYTES);  // [2][BN]
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + NS * C::STAGE_BYTES + C::RED_BYTES + 2 * C::XS_BYTES);
     uint64_t *empty = full + NS;
-    uint64_t *acc_full = empty + NS;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(acc_full + 1);
+    uint64_t *acc_full = empty + NS;     // [2]
+    uint64_t *acc_empty = acc_full + 2;  // [2], 4 arrivals
+    uint64_t *red_full = acc_empty + 2;  // every other CTA's four warps have pushed their partials of this CTA's share
+    uint64_t *red_empty = red_full + 1;  // every other CTA's four warps have read this CTA's partials
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(red_empty + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    int *partial = reinterpret_cast<int *>(smem);  // [BN tokens][128 channels], after the ring is done
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int S = p.splits;
     const int rank = S > 1 ? (int)cluster_ctarank() : 0;
-    const int tile = blockIdx.x / S;
-    const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
-    const int m0 = min(mt * 128, p.M - 128);  // M >= 128
-    const int n0 = nt * BN;
+    const int cluster = blockIdx.x / S, num_clusters = gridDim.x / S;
     const int kts = (p.K + 255) >> 8;
     const int k0 = (int)((int64_t)kts * rank / S), k1 = (int)((int64_t)kts * (rank + 1) / S);
     const int adp_kts = (p.r + 63) >> 6;
@@ -107,7 +117,12 @@ __global__ void __launch_bounds__(224)
             mbar_init(&full[s], p.meta_tma ? 1 : 2);
             mbar_init(&empty[s], 1);
         }
-        mbar_init(acc_full, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 4);
+        }
+        mbar_init(red_full, S > 1 ? 4 * (S - 1) : 1);
+        mbar_init(red_empty, S > 1 ? 4 * (S - 1) : 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -126,35 +141,39 @@ __global__ void __launch_bounds__(224)
     }
     tc_fence_before();
     __syncthreads();
+    if (S > 1) cluster_sync();  // the others' barriers are initialised before any remote arrive
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
     grid_dep_wait();
     grid_dep_launch();
 
-    bool done = false;  // epilogue warps: the accumulators are complete
     if (warp == 0) {
         // ------------------------------------------------------------ operand producer
         if (lane == 0) {
             int s = 0;
             uint32_t ph = 0;
-            for (int kt = k0; kt < k1 + adp_kts; ++kt) {
-                if (!mbar_wait(&empty[s], ph ^ 1, abort_flag)) break;
-                uint8_t *a = smem + s * C::STAGE_BYTES;
-                uint8_t *b = a + C::A_BYTES;
-                if (kt < k1) {
-                    mbar_arrive_expect_tx(&full[s], C::A_BYTES + 2 * C::B_PANEL + (p.meta_tma ? C::E_BYTES : 0));
-                    tma_load_2d(a, &tmA, &full[s], kt * 128, m0);
-                    if (p.meta_tma) tma_load_2d(b + 2 * C::B_PANEL, &tmE, &full[s], kt * 16, m0);
-                    tma_load_2d(b, &tmB, &full[s], kt * 256, n0);
-                    tma_load_2d(b + C::B_PANEL, &tmB, &full[s], kt * 256 + 128, n0);
-                } else {  // adapter: R^T (MN-major, two panels of 64 channels) and XL, 64 of the rank
-                    const int j0 = (kt - k1) * 64;
-                    mbar_arrive_expect_tx(&full[s], C::A_BYTES + C::B_PANEL);
-                    tma_load_2d(a, &tmR, &full[s], m0, j0);
-                    tma_load_2d(a + 8192, &tmR, &full[s], m0 + 64, j0);
-                    tma_load_2d(b, &tmXL, &full[s], j0, n0);
+            for (int w = cluster; w < p.num_work; w += num_clusters) {
+                const int mt = w % p.m_tiles, nt = w / p.m_tiles;
+                const int m0 = min(mt * 128, p.M - 128), n0 = nt * BN;  // M >= 128
+                for (int kt = k0; kt < k1 + adp_kts; ++kt) {
+                    if (!mbar_wait(&empty[s], ph ^ 1, abort_flag)) goto done;
+                    uint8_t *a = smem + s * C::STAGE_BYTES;
+                    uint8_t *b = a + C::A_BYTES;
+                    if (kt < k1) {
+                        mbar_arrive_expect_tx(&full[s], C::A_BYTES + 2 * C::B_PANEL + (p.meta_tma ? C::E_BYTES : 0));
+                        tma_load_2d(a, &tmA, &full[s], kt * 128, m0);
+                        if (p.meta_tma) tma_load_2d(b + 2 * C::B_PANEL, &tmE, &full[s], kt * 16, m0);
+                        tma_load_2d(b, &tmB, &full[s], kt * 256, n0);
+                        tma_load_2d(b + C::B_PANEL, &tmB, &full[s], kt * 256 + 128, n0);
+                    } else {  // adapter: R^T (MN-major, two panels of 64 channels) and XL, 64 of the rank
+                        const int j0 = (kt - k1) * 64;
+                        mbar_arrive_expect_tx(&full[s], C::A_BYTES + C::B_PANEL);
+                        tma_load_2d(a, &tmR, &full[s], m0, j0);
+                        tma_load_2d(a + 8192, &tmR, &full[s], m0 + 64, j0);
+                        tma_load_2d(b, &tmXL, &full[s], j0, n0);
+                    }
+                    if (++s == NS) { s = 0; ph ^= 1; }
                 }
-                if (++s == NS) { s = 0; ph ^= 1; }
             }
         }
     } else if (warp == 1) {
@@ -166,17 +185,16 @@ __global__ void __launch_bounds__(224)
         const uint64_t b_desc0 = smem_desc(base + C::A_BYTES, 16, 1024, SWZ_128B);
         const uint64_t e_desc0 = smem_desc(base + C::A_BYTES + 2 * C::B_PANEL, 16, 256, SWZ_32B);
         const uint64_t a2_desc0 = smem_desc(base, 8192, 1024, SWZ_128B);
-        int s = 0;
+        int s = 0, it = 0;
         uint32_t ph = 0;
-        bool ok = true;
-        for (int kt = k0; kt < k1 + adp_kts; ++kt) {
-            if (!mbar_wait_warp(&full[s], ph, abort_flag)) {
-                ok = false;
-                break;
-            }
+        for (int w = cluster; w < p.num_work; w += num_clusters, ++it) {
+            const uint32_t d = tmem_base + (it & 1) * BN;
+            if (!mbar_wait_warp(&acc_empty[it & 1], ((it >> 1) & 1) ^ 1, abort_flag)) goto done;
             tc_fence_after();
-            const uint64_t off = (uint64_t)((s * C::STAGE_BYTES) >> 4);
-            if (kt < k1) {
+            for (int kt = k0; kt < k1; ++kt) {
+                if (!mbar_wait_warp(&full[s], ph, abort_flag)) goto done;
+                tc_fence_after();
+                const uint64_t off = (uint64_t)((s * C::STAGE_BYTES) >> 4);
                 // the code columns of stage s: their last readers finished before the stage was refilled
                 const uint32_t ecol = tmem_base + C::E_COL + 8 * s;
                 elect_cp_128x256b<false>(ecol, e_desc0 + off);
@@ -184,36 +202,109 @@ __global__ void __launch_bounds__(224)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     if (c < nblk)
-                        elect_mma_sp_i8<false>(tmem_base, a_desc0 + off + (uint64_t)(2 * c),
+                        elect_mma_sp_i8<false>(d, a_desc0 + off + (uint64_t)(2 * c),
                                                b_desc0 + off + (uint64_t)(((c >> 1) * C::B_PANEL + (c & 1) * 64) >> 4),
                                                ecol + 2 * c, IDESC_SP, (kt > k0 || c > 0) ? 1u : 0u);
-            } else {
-                const int j0 = (kt - k1) * 64;
-                const int nblk = min(4, (p.r - j0 + 15) >> 4);
+                elect_commit<false>(&empty[s]);
+                if (++s == NS) { s = 0; ph ^= 1; }
+            }
+            if (adp_kts > 0 && it > 0) {  // the tile before has left the adapter's accumulator
+                if (!mbar_wait_warp(&acc_empty[(it - 1) & 1], ((it - 1) >> 1) & 1, abort_flag)) goto done;
+                tc_fence_after();
+            }
+            for (int kt = 0; kt < adp_kts; ++kt) {
+                if (!mbar_wait_warp(&full[s], ph, abort_flag)) goto done;
+                tc_fence_after();
+                const uint64_t off = (uint64_t)((s * C::STAGE_BYTES) >> 4);
+                const int nblk = min(4, (p.r - kt * 64 + 15) >> 4);
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     if (c < nblk)
                         elect_mma_bf16<false>(tmem_base + C::ADP_COL, a2_desc0 + off + (uint64_t)(128 * c),
-                                              b_desc0 + off + (uint64_t)(2 * c), IDESC_AD, (j0 > 0 || c > 0) ? 1u : 0u);
+                                              b_desc0 + off + (uint64_t)(2 * c), IDESC_AD, (kt > 0 || c > 0) ? 1u : 0u);
+                elect_commit<false>(&empty[s]);
+                if (++s == NS) { s = 0; ph ^= 1; }
             }
-            elect_commit<false>(&empty[s]);
-            if (++s == NS) { s = 0; ph ^= 1; }
+            elect_commit<false>(&acc_full[it & 1]);
         }
-        if (ok) elect_commit<false>(acc_full);
     } else if (warp < 6) {
-        // ------------------------------------------------------------ epilogue, first part
+        // ------------------------------------------------------------ epilogue
         const int q = warp & 3;
-        done = mbar_wait_warp(acc_full, 0, abort_flag);
-        tc_fence_after();
-        if (done && S > 1) {
-            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
-#pragma unroll 1
-            for (int c = 0; c < BN; c += 8) {
-                uint32_t v[8];
+        const int share = BN / S;
+        int it = 0;
+        for (int w = cluster; w < p.num_work; w += num_clusters, ++it) {
+            const int mt = w % p.m_tiles, nt = w / p.m_tiles;
+            const int m0 = min(mt * 128, p.M - 128), n0 = nt * BN;
+            const int cols = min(BN, (p.T - n0 + 1) & ~1);  // columns with tokens
+            const int f = m0 + 32 * q + lane;               // this lane's channel
+            const bool row_ok = f >= mt * 128;              // rows the tile before owns are not stored again
+            const float ws = in_bounds(f, 1, p.M) ? __ldg(p.wscale + f) : 0.0f;
+            // every warp writes the scales that it reads itself (the four write the same values)
+            float *xs = xs_buf + (it & 1) * BN;
+            for (int c = lane; c < BN; c += 32) xs[c] = n0 + c < p.T && in_bounds(n0 + c, 1, p.T) ? __ldg(p.xscale + n0 + c) : 0.0f;
+            __syncwarp();
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + (it & 1) * BN;
+            const uint32_t tadp = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + C::ADP_COL;
+            if (!mbar_wait_warp(&acc_full[it & 1], (it >> 1) & 1, abort_flag)) break;
+            tc_fence_after();
+            auto push = [&](auto width, int c, uint32_t dst) {
+                constexpr int W = decltype(width)::value;
+                uint32_t v[W];
                 tmem_ld_32x32_n(taddr + c, v);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 8; ++j) partial[(c + j) * 128 + 32 * q + lane] = (int)v[j];
+                for (int j = 0; j < W; ++j) st_cluster_u32(dst + j * 512, v[j]);
+            };
+            auto finish = [&](auto width, int c) {
+                constexpr int W = decltype(width)::value;
+                uint32_t ai[W], af[W];
+                tmem_ld_32x32_n(taddr + c, ai);
+                if (p.r > 0) tmem_ld_32x32_n(tadp + c, af);
+                tmem_ld_wait();
+                for (int u = 0; u < S - 1; ++u) {
+                    const uint32_t *src = red + (u * share + c - rank * share) * 128 + 32 * q + lane;
+#pragma unroll
+                    for (int j = 0; j < W; ++j) ai[j] += src[j * 128];
+                }
+                float v[W];
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    v[j] = fmaf((float)(int)ai[j], xs[c + j] * ws, p.r > 0 ? bits_to_f32(af[j]) : 0.0f);
+                q8_store(v, p, n0 + c, m0 + 32 * q, lane, row_ok);
+            };
+            using W8 = std::integral_constant<int, 8>;
+            using W2 = std::integral_constant<int, 2>;
+            if (S > 1) {
+                if (it > 0 && !__all_sync(0xffffffffu, mbar_wait_cluster(red_empty, (it - 1) & 1, abort_flag))) break;
+                for (int i = 1; i < S; ++i) {
+                    const int u = (rank + i) % S;  // the CTA that finishes columns [u share, (u + 1) share)
+                    const uint32_t dst = cluster_addr(red + (rank - (rank > u)) * share * 128 + 32 * q + lane, u);
+                    const int c_end = min((u + 1) * share, cols);
+                    if (share % 8 == 0) {
+#pragma unroll 1
+                        for (int c = u * share; c < c_end; c += 8) push(W8{}, c, dst + (c - u * share) * 512);
+                    } else {
+#pragma unroll 1
+                        for (int c = u * share; c < c_end; c += 2) push(W2{}, c, dst + (c - u * share) * 512);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_rel(cluster_addr(red_full, u));
+                }
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(red_full, it & 1, abort_flag))) break;
+            }
+            const int c_end = min((rank + 1) * share, cols);
+            if (share % 8 == 0) {
+#pragma unroll 1
+                for (int c = rank * share; c < c_end; c += 8) finish(W8{}, c);
+            } else {
+#pragma unroll 1
+                for (int c = rank * share; c < c_end; c += 2) finish(W2{}, c);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&acc_empty[it & 1]);
+                for (int i = 1; i < S; ++i) mbar_arrive_cluster_rel(cluster_addr(red_empty, (rank + i) % S));
             }
         }
     } else if (!p.meta_tma) {
@@ -221,81 +312,41 @@ __global__ void __launch_bounds__(224)
         const int words = p.K >> 4;  // code words of a row; a multiple of 4
         int s = 0;
         uint32_t ph = 0;
-        for (int kt = k0; kt < k1 + adp_kts; ++kt) {
-            if (!mbar_wait_warp(&empty[s], ph ^ 1, abort_flag)) break;
-            if (kt < k1) {
-                uint8_t *e = smem + s * C::STAGE_BYTES + C::A_BYTES + 2 * C::B_PANEL;
+        for (int w = cluster; w < p.num_work; w += num_clusters) {
+            const int m0 = min(w % p.m_tiles * 128, p.M - 128);
+            for (int kt = k0; kt < k1 + adp_kts; ++kt) {
+                if (!mbar_wait_warp(&empty[s], ph ^ 1, abort_flag)) goto done;
+                if (kt < k1) {
+                    uint8_t *e = smem + s * C::STAGE_BYTES + C::A_BYTES + 2 * C::B_PANEL;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = lane + 32 * i;
-                    uint2 w[4];
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = lane + 32 * i;
+                        uint2 cw[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int w0 = kt * 16 + 4 * c;
-                        const int64_t at = (int64_t)(m0 + row) * words + w0;
-                        w[c] = make_uint2(0x44444444u, 0x44444444u);
-                        if (w0 < words && in_bounds(at, 4, (int64_t)p.M * words))
-                            w[c] = *reinterpret_cast<const uint2 *>(p.meta + at);
+                        for (int c = 0; c < 4; ++c) {
+                            const int w0 = kt * 16 + 4 * c;
+                            const int64_t at = (int64_t)(m0 + row) * words + w0;
+                            cw[c] = make_uint2(0x44444444u, 0x44444444u);
+                            if (w0 < words && in_bounds(at, 4, (int64_t)p.M * words))
+                                cw[c] = *reinterpret_cast<const uint2 *>(p.meta + at);
+                        }
+                        const int x = (row >> 2) & 1;  // the 32-byte swizzle
+                        *reinterpret_cast<uint4 *>(e + row * 32 + 16 * x) = make_uint4(cw[0].x, cw[0].y, cw[1].x, cw[1].y);
+                        *reinterpret_cast<uint4 *>(e + row * 32 + 16 * (1 - x)) = make_uint4(cw[2].x, cw[2].y, cw[3].x, cw[3].y);
                     }
-                    const int x = (row >> 2) & 1;  // the 32-byte swizzle
-                    *reinterpret_cast<uint4 *>(e + row * 32 + 16 * x) = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
-                    *reinterpret_cast<uint4 *>(e + row * 32 + 16 * (1 - x)) = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
+                    fence_proxy_async_smem();
                 }
-                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[s]);
+                if (++s == NS) { s = 0; ph ^= 1; }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[s]);
-            if (++s == NS) { s = 0; ph ^= 1; }
         }
     }
-    __syncwarp();
-    if (S > 1) cluster_sync();  // every CTA's partial is in place
-    if (warp >= 2 && warp < 6) {
-        // ------------------------------------------------------------ epilogue, second part: this CTA's share of the tokens
-        const int q = warp & 3;
-        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
-        const int f = m0 + 32 * q + lane;          // this lane's channel
-        const bool row_ok = done && f >= mt * 128;  // rows the previous tile owns are not stored again
-        const float ws = done && in_bounds(f, 1, p.M) ? p.wscale[f] : 0.0f;
-        const int share = BN / S;
-        auto columns = [&](auto width, int c) {
-            constexpr int W = decltype(width)::value;
-            uint32_t ai[W], af[W];
-            if (S == 1) tmem_ld_32x32_n(taddr + c, ai);
-            if (p.r > 0) tmem_ld_32x32_n(taddr + C::ADP_COL + c, af);
-            tmem_ld_wait();
-            if (S > 1) {
-#pragma unroll
-                for (int j = 0; j < W; ++j) ai[j] = 0;
-                for (int u = 0; u < S; ++u) {
-                    const uint32_t src = cluster_addr(partial + c * 128 + 32 * q + lane, u);
-#pragma unroll
-                    for (int j = 0; j < W; ++j) ai[j] += (uint32_t)ld_cluster_s32(src + j * 512);
-                }
-            }
-            float v[W];
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const int t = n0 + c + j;
-                const float x = t < p.T && in_bounds(t, 1, p.T) ? __ldg(p.xscale + t) : 0.0f;
-                v[j] = fmaf((float)(int)ai[j], x * ws, p.r > 0 ? bits_to_f32(af[j]) : 0.0f);
-            }
-            q8_store(v, p, n0 + c, m0 + 32 * q, lane, row_ok);
-        };
-        // tokens past the end have no columns to write (their share may be empty)
-        const int c_end = min((rank + 1) * share, (p.T - n0 + 1) & ~1);
-        if (share % 8 == 0) {
-#pragma unroll 1
-            for (int c = rank * share; c < c_end; c += 8) columns(std::integral_constant<int, 8>{}, c);
-        } else {
-#pragma unroll 1
-            for (int c = rank * share; c < c_end; c += 2) columns(std::integral_constant<int, 2>{}, c);
-        }
-    }
+done:
     __syncwarp();
     tc_fence_before();
-    if (S > 1) cluster_sync();  // the partials have been read
-    else __syncthreads();
+    __syncthreads();
+    if (S > 1) cluster_sync();  // no CTA leaves while another may still signal it
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();

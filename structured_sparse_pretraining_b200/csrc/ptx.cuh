@@ -104,6 +104,30 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     }
 }
 
+// mbar_wait for arrivals of other CTAs of the cluster whose shared-memory
+// writes it publishes (they arrive with cluster-scope release).
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    const uint32_t a = smem_addr(bar);
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(a), "r"(parity), "r"(kSuspendNs)
+            : "memory");
+        if (ok) return true;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > kWaitLimitCycles) {
+            atomicOr(&g_status, ST_TIMEOUT);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+
 // mbar_wait by all 32 lanes of a warp, with a warp-uniform answer, for roles
 // whose lanes then meet in __syncwarp or a .sync.aligned instruction.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
@@ -322,10 +346,8 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
     return r;
 }
-__device__ __forceinline__ int ld_cluster_s32(uint32_t cluster_ptr) {
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_ptr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_ptr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_ptr), "r"(v) : "memory");
 }
 // Arrive on an mbarrier given by its shared::cluster address (possibly the
 // peer's), with the instruction's default (CTA-scope release) semantics.

@@ -234,8 +234,8 @@ int launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const slope::GemmPar
 template <typename Kern, typename... Args>
 int launch_clusters(Kern kern, int slot, int csize, int threads, int smem_bytes, int num_work, int sms,
                     cudaStream_t st, Args... args) {
-    static std::atomic<uint64_t> attr_set_mask[48];
-    static std::atomic<int> max_clusters[48][64];
+    static std::atomic<uint64_t> attr_set_mask[64];
+    static std::atomic<int> max_clusters[64][64];
     int dev = 0;
     cudaGetDevice(&dev);
     cudaLaunchConfig_t cfg = {};
@@ -1707,7 +1707,7 @@ int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, 
 
 namespace {
 // ------------------------------------------------------------------ int8 sparse product
-constexpr int Q8_WIDE_SLOT = 42;      // its entry in launch_clusters' table
+constexpr int Q8_WIDE_SLOT = 42, Q8_TILE_SLOT = 44;  // entries in launch_clusters' table (the tiles': 16)
 constexpr int64_t Q8_MAX_K = 131072;  // 128 * 128 * K / 2 stays below 2^31
 
 // Opt in to `bytes` of dynamic shared memory once per device.
@@ -1741,12 +1741,14 @@ Q8Plan pick_q8_plan(int64_t M, int64_t T, int64_t K, int sms) {
     }
     if (T >= 1024 && K % 128 == 0) return Q8Plan{224, 1, 0, true};
     const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+    // rounds of the persistent clusters times k-tiles of a round (the adapter's among them), and what joining
+    // the partials adds at the end
     const int64_t kts = (K + 255) / 256, tiles = (M + 127) / 128 * ((T + bn - 1) / bn);
-    const int64_t slots = (int64_t)sms * (bn <= 64 ? 2 : 1);
     Q8Plan best{bn, 1, 0, false};
     double best_cost = 1e300;
     for (int s = 1; s <= 8 && s <= kts; s *= 2) {
-        const double cost = (double)((tiles * s + slots - 1) / slots) * ((double)((kts + s - 1) / s) + 4.0) + 0.5 * (s > 1 ? s : 0);
+        const int64_t clusters = sms / s;
+        const double cost = (double)((tiles + clusters - 1) / clusters) * ((double)((kts + s - 1) / s) + 2.0) + (s > 1 ? 1.0 : 0.0);
         if (cost < best_cost) {
             best_cost = cost;
             best.splits = s;
@@ -1770,29 +1772,12 @@ int launch_skinny_q8(const slope::SkinnyQ8Params &p, int sms, cudaStream_t st) {
 
 template <int BN>
 int launch_q8_tile(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &e, const CUtensorMap &r2,
-                   const CUtensorMap &xl, const slope::Q8Params &p, cudaStream_t st) {
-    using C = slope::Q8TileCfg<BN>;
-    auto kern = slope::q8_tile_kernel<BN>;
-    static std::atomic<uint64_t> done{0};
-    if (int rc = allow_smem(kern, C::SMEM_BYTES, done)) return rc;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)p.splits;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)((int64_t)p.m_tiles * ((p.T + BN - 1) / BN) * p.splits), 1, 1);
-    cfg.blockDim = dim3(224, 1, 1);
-    cfg.dynamicSmemBytes = C::SMEM_BYTES;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.splits > 1 ? 2 : 1;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a, b, e, r2, xl, p);
-    if (err != cudaSuccess) return cuda_fail(err, "int8 product launch");
-    ++g_launches;
-    return SLOPE_OK;
+                   const CUtensorMap &xl, const slope::Q8Params &p, int sms, cudaStream_t st) {
+    // an entry of launch_clusters' table for each width and cluster size
+    const int slot = Q8_TILE_SLOT + 4 * (BN == 16 ? 0 : BN == 32 ? 1 : BN == 64 ? 2 : 3) +
+                     (p.splits == 1 ? 0 : p.splits == 2 ? 1 : p.splits == 4 ? 2 : 3);
+    return launch_clusters(slope::q8_tile_kernel<BN>, slot, p.splits, 224, slope::Q8Cfg<BN>::SMEM_BYTES, p.num_work, sms, st, a,
+                           b, e, r2, xl, p);
 }
 
 int q8_product(const int8_t *X, const float *xscale, const int8_t *W, const float *wscale, const uint16_t *meta,
@@ -1821,6 +1806,7 @@ int q8_product(const int8_t *X, const float *xscale, const int8_t *W, const floa
     p.K = (int)K;
     p.r = (int)r;
     p.m_tiles = (int)((M + 127) / 128);
+    p.num_work = plan.wide ? 0 : (int)(p.m_tiles * ((T + plan.bn - 1) / plan.bn));
     p.splits = plan.splits;
     p.meta_tma = K % 128 == 0;
     p.meta = meta;
@@ -1852,10 +1838,10 @@ int q8_product(const int8_t *X, const float *xscale, const int8_t *W, const floa
         return launch_pairs(slope::q8_wide_kernel, Q8_WIDE_SLOT, 320, C::SMEM_BYTES, wp.num_work, d.sms, st, a, b, e, r2, xl, wp);
     }
     switch (plan.bn) {
-        case 16: return launch_q8_tile<16>(a, b, e, r2, xl, p, st);
-        case 32: return launch_q8_tile<32>(a, b, e, r2, xl, p, st);
-        case 64: return launch_q8_tile<64>(a, b, e, r2, xl, p, st);
-        default: return launch_q8_tile<128>(a, b, e, r2, xl, p, st);
+        case 16: return launch_q8_tile<16>(a, b, e, r2, xl, p, d.sms, st);
+        case 32: return launch_q8_tile<32>(a, b, e, r2, xl, p, d.sms, st);
+        case 64: return launch_q8_tile<64>(a, b, e, r2, xl, p, d.sms, st);
+        default: return launch_q8_tile<128>(a, b, e, r2, xl, p, d.sms, st);
     }
 }
 }  // namespace

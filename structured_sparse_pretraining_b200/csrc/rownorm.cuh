@@ -105,9 +105,87 @@ struct RowParams {
     float eps;
 };
 
+// h = bf16(x + e), eight values.
+__device__ __forceinline__ uint4 add_bf16x8(uint4 x, uint4 e) {
+    uint32_t a[4] = {x.x, x.y, x.z, x.w};
+    const uint32_t b[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 u = bf16x2_to_float2(a[k]), v = bf16x2_to_float2(b[k]);
+        a[k] = pack_bf16x2(u.x + v.x, u.y + v.y);
+    }
+    return make_uint4(a[0], a[1], a[2], a[3]);
+}
+
+// Eight values' share of the row's sum of squares and of its largest |p| (as
+// bits: an infinity or a NaN, whose bits are larger than any number's, wins).
+template <bool NORM>
+__device__ __forceinline__ void row_stats(uint4 h, uint4 w, bool want_max, float &ss, uint32_t &mx) {
+    const uint32_t a[4] = {h.x, h.y, h.z, h.w}, b[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 u = bf16x2_to_float2(a[k]);
+        if (NORM) {
+            ss = fmaf(u.x, u.x, fmaf(u.y, u.y, ss));
+            if (want_max) {
+                const float2 v = bf16x2_to_float2(b[k]);
+                mx = max(mx, max(__float_as_uint(u.x * v.x) & 0x7FFFFFFFu, __float_as_uint(u.y * v.y) & 0x7FFFFFFFu));
+            }
+        } else {
+            mx = max(mx, max(__float_as_uint(u.x) & 0x7FFFFFFFu, __float_as_uint(u.y) & 0x7FFFFFFFu));
+        }
+    }
+}
+
+// Sum of squares of h 2^-80, eight values (rows whose squares overflow binary32).
+__device__ __forceinline__ float scaled_squares(uint4 h, float s2) {
+    const uint32_t a[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 u = bf16x2_to_float2(a[k]);
+        s2 = fmaf(u.x * 0x1p-80f, u.x * 0x1p-80f, fmaf(u.y * 0x1p-80f, u.y * 0x1p-80f, s2));
+    }
+    return s2;
+}
+
+// Eight outputs of a row from its h: y = h rstd w and the codes of h w.
+template <bool NORM>
+__device__ __forceinline__ void row_outputs(const RowParams &p, int64_t at, uint4 h, uint4 w, float rstd, const QuantRow &q,
+                                            bool finite) {
+    const uint32_t a[4] = {h.x, h.y, h.z, h.w}, b[4] = {w.x, w.y, w.z, w.w};
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 u = bf16x2_to_float2(a[k]);
+        v[2 * k] = u.x;
+        v[2 * k + 1] = u.y;
+    }
+    if (NORM) {
+        if (p.Y) {
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 g = bf16x2_to_float2(b[k]);
+                o[k] = pack_bf16x2(v[2 * k] * rstd * g.x, v[2 * k + 1] * rstd * g.y);
+            }
+            *reinterpret_cast<uint4 *>(p.Y + at) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 g = bf16x2_to_float2(b[k]);
+            v[2 * k] *= g.x;
+            v[2 * k + 1] *= g.y;
+        }
+    }
+    if (p.Q) *reinterpret_cast<uint2 *>(p.Q + at) = finite ? quant8(v, q) : make_uint2(0, 0);
+}
+
+__device__ __forceinline__ float row_rstd(float ss, int D, float eps) { return __frcp_rn(__fsqrt_rn(ss / (float)D + eps)); }
+
 // NORM: the norm; otherwise the quantiser.  WARP: a warp per row, otherwise a
-// CTA per row.  H may be the buffer of X or res, and Y that of any of them: a
-// thread reads its chunks of a row before it writes those same chunks.
+// CTA per row, held in registers.  H may be the buffer of X or res, and Y that
+// of any of them: a thread reads its chunks of a row before it writes those
+// same chunks.
 template <int NV, bool WARP, bool NORM>
 __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const __grid_constant__ RowParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -134,43 +212,20 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
         for (int i = 0; i < NV; ++i) {
             const int c = gi + i * gsize;
             if (c < nchunk && in_bounds(base + 8 * c, 8, total)) {
-                const uint4 e = *reinterpret_cast<const uint4 *>(p.res + base + 8 * c);
-                uint32_t *a = reinterpret_cast<uint32_t *>(&h[i]);
-                const uint32_t b[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 u = bf16x2_to_float2(a[k]), v = bf16x2_to_float2(b[k]);
-                    a[k] = pack_bf16x2(u.x + v.x, u.y + v.y);
-                }
+                h[i] = add_bf16x8(h[i], *reinterpret_cast<const uint4 *>(p.res + base + 8 * c));
                 if (p.H) *reinterpret_cast<uint4 *>(p.H + base + 8 * c) = h[i];
             }
         }
     }
-
-    // the row's sum of squares and its largest |p| (as bits: an infinity or a
-    // NaN, whose bits are larger than any number's, wins)
+    auto weight = [&](int c) {
+        return NORM && c < nchunk && in_bounds(8 * c, 8, p.D) ? __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c))
+                                                              : make_uint4(0, 0, 0, 0);
+    };
     float ss = 0.0f;
     uint32_t mx = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = gi + i * gsize;
-        uint4 wv = make_uint4(0, 0, 0, 0);
-        if (NORM && p.Q && c < nchunk && in_bounds(8 * c, 8, p.D)) wv = __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c));
-        const uint32_t a[4] = {h[i].x, h[i].y, h[i].z, h[i].w}, b[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 u = bf16x2_to_float2(a[k]);
-            if (NORM) {
-                ss = fmaf(u.x, u.x, fmaf(u.y, u.y, ss));
-                if (p.Q) {
-                    const float2 v = bf16x2_to_float2(b[k]);
-                    mx = max(mx, max(__float_as_uint(u.x * v.x) & 0x7FFFFFFFu, __float_as_uint(u.y * v.y) & 0x7FFFFFFFu));
-                }
-            } else {
-                mx = max(mx, max(__float_as_uint(u.x) & 0x7FFFFFFFu, __float_as_uint(u.y) & 0x7FFFFFFFu));
-            }
-        }
-    }
+    for (int i = 0; i < NV; ++i)
+        row_stats<NORM>(h[i], p.Q ? weight(gi + i * gsize) : make_uint4(0, 0, 0, 0), p.Q != nullptr, ss, mx);
     if (NORM) ss = warp_sum(ss);
     mx = __reduce_max_sync(0xffffffffu, mx);
     if (!WARP) {
@@ -191,14 +246,7 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
             // in the row stays one, and gives rstd = 0 and NaN beside it)
             float s2 = 0.0f;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const uint32_t a[4] = {h[i].x, h[i].y, h[i].z, h[i].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 u = bf16x2_to_float2(a[k]);
-                    s2 = fmaf(u.x * 0x1p-80f, u.x * 0x1p-80f, fmaf(u.y * 0x1p-80f, u.y * 0x1p-80f, s2));
-                }
-            }
+            for (int i = 0; i < NV; ++i) s2 = scaled_squares(h[i], s2);
             s2 = warp_sum(s2);
             if (!WARP) {
                 __syncthreads();  // every thread has read the first sums
@@ -206,9 +254,9 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
                 __syncthreads();
                 s2 = warp_sum(lane < (int)(blockDim.x >> 5) ? s_sum[lane] : 0.0f);
             }
-            rstd = __frcp_rn(__fsqrt_rn(s2 / (float)p.D)) * 0x1p-80f;
+            rstd = row_rstd(s2, p.D, 0.0f) * 0x1p-80f;
         } else {
-            rstd = __frcp_rn(__fsqrt_rn(ss / (float)p.D + p.eps));
+            rstd = row_rstd(ss, p.D, p.eps);
         }
         if (p.rstd && gi == 0 && in_bounds(row, 1, p.T)) p.rstd[row] = rstd;
     }
@@ -220,36 +268,126 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = gi + i * gsize;
-        if (c >= nchunk || !in_bounds(base + 8 * c, 8, total)) continue;
-        const uint32_t a[4] = {h[i].x, h[i].y, h[i].z, h[i].w};
-        float v[8];
+        if (c < nchunk && in_bounds(base + 8 * c, 8, total)) row_outputs<NORM>(p, base + 8 * c, h[i], weight(c), rstd, q, finite);
+    }
+}
+
+// The same for many rows: persistent CTAs, each with a ring of `stages` rows
+// (X, and res beside it) that bulk copies keep filled, so that the loads of
+// the next rows run beside the arithmetic and the stores of this one.  With
+// one row per CTA and nothing ahead the norm of 8192 x 9216 (9 bytes a value)
+// took 150 us, 69% of the measured copy rate.  The weight stays in registers.
+// One barrier a row: when it falls every thread holds its chunks, and the
+// row's stage is refilled.
+constexpr int STREAM_MAX_STAGES = 4;
+// Up to 384 threads a CTA with NV <= 4 and as many CTAs an SM as the plan asks
+// for; above that one CTA (512 threads of the norm, whose weight takes half
+// the registers, 1024 of the quantiser).
+constexpr int stream_threads(int nv, bool norm) { return nv <= 4 ? 384 : norm ? 512 : 1024; }
+constexpr int stream_ctas(int nv) { return nv <= 3 ? 3 : nv == 4 ? 2 : 1; }
+constexpr int stream_bwd_ctas(int nv) { return nv <= 2 ? 3 : nv == 3 ? 2 : 1; }
+template <int NV, bool NORM>
+__global__ void __launch_bounds__(stream_threads(NV, NORM), stream_ctas(NV)) row_stream_kernel(const __grid_constant__ RowParams p, int stages) {
+    extern __shared__ __align__(16) uint8_t row_smem[];
+    __shared__ __align__(8) uint64_t full[STREAM_MAX_STAGES];
+    __shared__ float s_sum[2][32];
+    __shared__ uint32_t s_max[2][32];
+    __shared__ int abort_flag;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+    const int nchunk = p.D >> 3;
+    const int64_t total = p.T * p.D;
+    const uint32_t row_bytes = (uint32_t)p.D * 2;
+    const bool has_res = NORM && p.res;
+    const uint32_t stage_bytes = has_res ? 2 * row_bytes : row_bytes;
+    if (tid == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    grid_dep_wait();
+    grid_dep_launch();
+    auto fetch = [&](int64_t row, int s) {  // one thread
+        if (row >= p.T || !in_bounds(row * p.D, p.D, total)) return;
+        uint8_t *dst = row_smem + s * stage_bytes;
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        bulk_load(dst, p.X + row * p.D, row_bytes, &full[s]);
+        if (has_res) bulk_load(dst + row_bytes, p.res + row * p.D, row_bytes, &full[s]);
+    };
+    if (tid == 0)
+        for (int s = 0; s < stages; ++s) fetch((int64_t)blockIdx.x + (int64_t)s * gridDim.x, s);
+    uint4 w[NV];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 u = bf16x2_to_float2(a[k]);
-            v[2 * k] = u.x;
-            v[2 * k + 1] = u.y;
+    for (int i = 0; i < NV; ++i) {
+        const int c = tid + i * blockDim.x;
+        w[i] = NORM && c < nchunk && in_bounds(8 * c, 8, p.D) ? __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c))
+                                                              : make_uint4(0, 0, 0, 0);
+    }
+    int s = 0, turn = 0;
+    uint32_t ph = 0;
+    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+        const int64_t base = row * p.D;
+        const uint8_t *src = row_smem + s * stage_bytes;
+        // a copy that does not come gives up after its limit, and the thread works on what is there
+        mbar_wait(&full[s], ph, &abort_flag);
+        uint4 h[NV];
+        float ss = 0.0f;
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = tid + i * blockDim.x;
+            h[i] = make_uint4(0, 0, 0, 0);
+            if (c < nchunk) {
+                h[i] = *reinterpret_cast<const uint4 *>(src + 16 * c);
+                if (has_res) h[i] = add_bf16x8(h[i], *reinterpret_cast<const uint4 *>(src + row_bytes + 16 * c));
+            }
+            row_stats<NORM>(h[i], w[i], p.Q != nullptr, ss, mx);
         }
+        if (NORM) ss = warp_sum(ss);
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        if (lane == 0) {
+            s_sum[turn][warp] = ss;
+            s_max[turn][warp] = mx;
+        }
+        __syncthreads();
+        if (tid == 0) fetch(row + (int64_t)stages * gridDim.x, s);
+        if (++s == stages) {
+            s = 0;
+            ph ^= 1;
+        }
+        ss = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
+        mx = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[turn][lane] : 0u);
+        float rstd = 1.0f;
         if (NORM) {
-            const uint4 wv = __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c));
-            const uint32_t b[4] = {wv.x, wv.y, wv.z, wv.w};
-            if (p.Y) {
-                uint32_t o[4];
+            if (__float_as_uint(ss) == kInfBits) {  // see row_kernel
+                float s2 = 0.0f;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 g = bf16x2_to_float2(b[k]);
-                    o[k] = pack_bf16x2(v[2 * k] * rstd * g.x, v[2 * k + 1] * rstd * g.y);
-                }
-                *reinterpret_cast<uint4 *>(p.Y + base + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+                for (int i = 0; i < NV; ++i) s2 = scaled_squares(h[i], s2);
+                s2 = warp_sum(s2);
+                __syncthreads();
+                if (lane == 0) s_sum[turn][warp] = s2;
+                __syncthreads();
+                s2 = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
+                rstd = row_rstd(s2, p.D, 0.0f) * 0x1p-80f;
+            } else {
+                rstd = row_rstd(ss, p.D, p.eps);
             }
+            if (p.rstd && tid == 0 && in_bounds(row, 1, p.T)) p.rstd[row] = rstd;
+        }
+        turn ^= 1;  // the next row's sums go beside this row's, which other warps may still read
+        const bool finite = mx < kInfBits;
+        const float pmax = __uint_as_float(mx);
+        const QuantRow q = quant_row(finite ? pmax : 0.0f);
+        if (p.Q && tid == 0 && in_bounds(row, 1, p.T))
+            p.qscale[row] = finite ? rstd * pmax / 127.0f : __uint_as_float(0x7FC00000u);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 g = bf16x2_to_float2(b[k]);
-                v[2 * k] *= g.x;
-                v[2 * k + 1] *= g.y;
+        for (int i = 0; i < NV; ++i) {
+            const int c = tid + i * blockDim.x;
+            if (c < nchunk && in_bounds(base + 8 * c, 8, total)) {
+                if (has_res && p.H) *reinterpret_cast<uint4 *>(p.H + base + 8 * c) = h[i];
+                row_outputs<NORM>(p, base + 8 * c, h[i], w[i], rstd, q, finite);
             }
         }
-        if (p.Q)
-            *reinterpret_cast<uint2 *>(p.Q + base + 8 * c) = finite ? quant8(v, q) : make_uint2(0, 0);
     }
 }
 
@@ -377,6 +515,122 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_bwd_kernel(c
                 dst[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
                 dst[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
             }
+        }
+    }
+}
+
+// The same with the ring of row_stream_kernel: dY, H and dres of the next rows
+// arrive by bulk copy while this row is worked on; the second pass reads the
+// row again from shared memory, so registers hold only the sums of dY n and
+// the weight.  A stage is refilled after the next row's barrier, when every
+// thread is done with it.
+template <int NV>
+__global__ void __launch_bounds__(384, stream_bwd_ctas(NV)) row_bwd_stream_kernel(const __grid_constant__ RowBwdParams p, int stages) {
+    extern __shared__ __align__(16) uint8_t row_smem[];
+    __shared__ __align__(8) uint64_t full[STREAM_MAX_STAGES];
+    __shared__ float s_sum[2][32];
+    __shared__ int abort_flag;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+    const int nchunk = p.D >> 3;
+    const int64_t total = p.T * p.D;
+    const uint32_t row_bytes = (uint32_t)p.D * 2;
+    const uint32_t stage_bytes = (p.dres ? 3 : 2) * row_bytes;
+    if (tid == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    grid_dep_wait();
+    grid_dep_launch();
+    auto fetch = [&](int64_t row, int s) {  // one thread
+        if (row >= p.T || !in_bounds(row * p.D, p.D, total)) return;
+        uint8_t *dst = row_smem + s * stage_bytes;
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        bulk_load(dst, p.H + row * p.D, row_bytes, &full[s]);
+        bulk_load(dst + row_bytes, p.dY + row * p.D, row_bytes, &full[s]);
+        if (p.dres) bulk_load(dst + 2 * row_bytes, p.dres + row * p.D, row_bytes, &full[s]);
+    };
+    if (tid == 0)
+        for (int s = 0; s < stages; ++s) fetch((int64_t)blockIdx.x + (int64_t)s * gridDim.x, s);
+    uint4 w[NV];
+    float acc[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = tid + i * blockDim.x;
+        w[i] = c < nchunk && in_bounds(8 * c, 8, p.D) ? __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+    }
+    const float inv_d = 1.0f / (float)p.D;
+    int s = 0, turn = 0;
+    uint32_t ph = 0;
+    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+        const int64_t base = row * p.D;
+        const uint8_t *src = row_smem + s * stage_bytes;
+        const float rstd = in_bounds(row, 1, p.T) ? __ldg(p.rstd + row) : 0.0f;
+        mbar_wait(&full[s], ph, &abort_flag);
+        float dot = 0.0f;  // sum of g n
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = tid + i * blockDim.x;
+            if (c < nchunk) {
+                const uint4 hv = *reinterpret_cast<const uint4 *>(src + 16 * c);
+                const uint4 gv = *reinterpret_cast<const uint4 *>(src + row_bytes + 16 * c);
+                const uint32_t a[4] = {hv.x, hv.y, hv.z, hv.w}, b[4] = {gv.x, gv.y, gv.z, gv.w};
+                const uint32_t d[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 hh = bf16x2_to_float2(a[k]), gg = bf16x2_to_float2(b[k]), ww = bf16x2_to_float2(d[k]);
+                    const float dnx = gg.x * (hh.x * rstd), dny = gg.y * (hh.y * rstd);  // dY n
+                    dot = fmaf(dnx, ww.x, fmaf(dny, ww.y, dot));
+                    acc[i][2 * k] += dnx;
+                    acc[i][2 * k + 1] += dny;
+                }
+            }
+        }
+        dot = warp_sum(dot);
+        if (lane == 0) s_sum[turn][warp] = dot;
+        __syncthreads();
+        // the stage of the row before: every thread has left its second pass
+        if (tid == 0 && row > blockIdx.x) fetch(row + (int64_t)(stages - 1) * gridDim.x, s == 0 ? stages - 1 : s - 1);
+        dot = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
+        turn ^= 1;
+        const float mean = dot * inv_d;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = tid + i * blockDim.x;
+            if (c < nchunk && in_bounds(base + 8 * c, 8, total)) {
+                const uint4 hv = *reinterpret_cast<const uint4 *>(src + 16 * c);
+                const uint4 gv = *reinterpret_cast<const uint4 *>(src + row_bytes + 16 * c);
+                uint4 ev = make_uint4(0, 0, 0, 0);
+                if (p.dres) ev = *reinterpret_cast<const uint4 *>(src + 2 * row_bytes + 16 * c);
+                const uint32_t a[4] = {hv.x, hv.y, hv.z, hv.w}, b[4] = {gv.x, gv.y, gv.z, gv.w};
+                const uint32_t d[4] = {w[i].x, w[i].y, w[i].z, w[i].w}, e[4] = {ev.x, ev.y, ev.z, ev.w};
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 hh = bf16x2_to_float2(a[k]), gg = bf16x2_to_float2(b[k]), ww = bf16x2_to_float2(d[k]);
+                    const float2 ee = bf16x2_to_float2(e[k]);
+                    o[k] = pack_bf16x2(fmaf(rstd, fmaf(-hh.x * rstd, mean, gg.x * ww.x), ee.x),
+                                       fmaf(rstd, fmaf(-hh.y * rstd, mean, gg.y * ww.y), ee.y));
+                }
+                *reinterpret_cast<uint4 *>(p.dH + base + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+        if (++s == stages) {
+            s = 0;
+            ph ^= 1;
+        }
+    }
+    const int64_t pbase = (int64_t)blockIdx.x * p.D, ptotal = (int64_t)p.parts * p.D;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = tid + i * blockDim.x;
+        if (c < nchunk && in_bounds(pbase + 8 * c, 8, ptotal)) {
+            float4 *dst = reinterpret_cast<float4 *>(p.part + pbase + 8 * c);
+            dst[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+            dst[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
         }
     }
 }

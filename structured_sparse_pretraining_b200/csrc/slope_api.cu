@@ -1595,9 +1595,60 @@ RowPlan pick_row_plan(int64_t D) {
     return RowPlan{false, nv, (chunks + 32 * nv - 1) / (32 * nv) * 32};
 }
 
+// Rings of rows for many rows (row_stream_kernel and row_bwd_stream_kernel):
+// nv 16-byte chunks per thread, CTAs per SM by their threads, and as many
+// stages as shared memory holds; stages = 0 where not two rows of
+// `row_bytes` fit.
+struct StreamPlan {
+    int nv, threads, per_sm, stages;
+};
+constexpr int STREAM_SMEM = 224 * 1024;  // of an SM, for its CTAs' rings
+StreamPlan pick_stream_plan(int64_t D, int64_t row_bytes, bool backward) {
+    const int chunks = (int)(D / 8);
+    const int nv = chunks <= 4 * 384 ? (chunks + 383) / 384 : 8;
+    StreamPlan s{nv, (chunks + 32 * nv - 1) / (32 * nv) * 32, 0, 0};
+    for (s.per_sm = backward ? slope::stream_bwd_ctas(nv) : slope::stream_ctas(nv); s.per_sm >= 1; --s.per_sm) {
+        const int64_t fit = (STREAM_SMEM / s.per_sm - 2048) / row_bytes;
+        s.stages = (int)(fit > slope::STREAM_MAX_STAGES ? slope::STREAM_MAX_STAGES : fit);
+        if (s.stages >= 2) break;
+    }
+    if (s.stages < 2) s.stages = 0;
+    return s;
+}
+
+// Opt in to `bytes` of dynamic shared memory once per device.
+template <typename Kern>
+int allow_smem(Kern kern, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64 && (done.load() & (1ull << dev))) return SLOPE_OK;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(dynamic shared memory)");
+    if (dev < 64) done.fetch_or(1ull << dev);
+    return SLOPE_OK;
+}
+
+template <int NV, bool NORM>
+int row_stream_launch(const slope::RowParams &p, const StreamPlan &s, int row_bytes, int sms, cudaStream_t st, const char *what) {
+    static std::atomic<uint64_t> done{0};
+    if (int rc = allow_smem(slope::row_stream_kernel<NV, NORM>, STREAM_SMEM - 2048, done)) return rc;
+    const int64_t most = (int64_t)sms * s.per_sm;
+    return launch_pdl(slope::row_stream_kernel<NV, NORM>, dim3((unsigned)(p.T < most ? p.T : most)), dim3((unsigned)s.threads),
+                      s.stages * row_bytes, st, what, p, s.stages);
+}
+
 template <bool NORM>
-int row_launch(const slope::RowParams &p, cudaStream_t st, const char *what) {
+int row_launch(const slope::RowParams &p, int sms, cudaStream_t st, const char *what) {
     const RowPlan r = pick_row_plan(p.D);
+    const int row_bytes = p.D * (p.res ? 4 : 2);
+    const StreamPlan s = pick_stream_plan(p.D, row_bytes, false);
+    if (!r.warp && s.stages > 0 && p.T >= 2 * (int64_t)sms * s.per_sm) {
+        if (s.nv == 1) return row_stream_launch<1, NORM>(p, s, row_bytes, sms, st, what);
+        if (s.nv == 2) return row_stream_launch<2, NORM>(p, s, row_bytes, sms, st, what);
+        if (s.nv == 3) return row_stream_launch<3, NORM>(p, s, row_bytes, sms, st, what);
+        if (s.nv == 4) return row_stream_launch<4, NORM>(p, s, row_bytes, sms, st, what);
+        return row_stream_launch<8, NORM>(p, s, row_bytes, sms, st, what);
+    }
     const int64_t blocks = r.warp ? (p.T + slope::ROW_WARPS - 1) / slope::ROW_WARPS : p.T;
     const dim3 grid((unsigned)blocks), block((unsigned)r.threads);
     if (r.warp) {
@@ -1611,13 +1662,28 @@ int row_launch(const slope::RowParams &p, cudaStream_t st, const char *what) {
     return launch_pdl(slope::row_kernel<4, false, NORM>, grid, block, 0, st, what, p);
 }
 
-// CTAs of the gradient kernel, and so rows of its partial sums of dw: enough
-// to fill 148 SMs with about 1536 threads each.
-int64_t norm_bwd_parts(int64_t T, int64_t D) {
-    const RowPlan r = pick_row_plan(D);
-    const int64_t per_sm = 1536 / r.threads < 1 ? 1 : 1536 / r.threads > 4 ? 4 : 1536 / r.threads;
-    const int64_t blocks = r.warp ? (T + slope::ROW_WARPS - 1) / slope::ROW_WARPS : T;
-    return blocks < 148 * per_sm ? blocks : 148 * per_sm;
+// The gradient kernel's form, and its CTAs: the rows of its partial sums of dw.
+// It does not know the device (the scratch query has none), so 148 SMs are taken.
+struct BwdPlan {
+    RowPlan row;
+    StreamPlan stream;  // stages = 0: row_bwd_kernel
+    int64_t parts;
+};
+BwdPlan pick_bwd_plan(int64_t T, int64_t D) {
+    BwdPlan b{pick_row_plan(D), pick_stream_plan(D, 6 * D, true), 0};
+    if (b.row.warp || b.stream.nv > 4 || T < 2 * 148 * (int64_t)b.stream.per_sm) b.stream.stages = 0;
+    const int64_t per_sm = b.stream.stages ? b.stream.per_sm : 1536 / b.row.threads < 1 ? 1 : 1536 / b.row.threads > 4 ? 4 : 1536 / b.row.threads;
+    const int64_t blocks = b.row.warp ? (T + slope::ROW_WARPS - 1) / slope::ROW_WARPS : T;
+    b.parts = blocks < 148 * per_sm ? blocks : 148 * per_sm;
+    return b;
+}
+
+template <int NV>
+int row_bwd_stream_launch(const slope::RowBwdParams &p, const StreamPlan &s, cudaStream_t st, const char *what) {
+    static std::atomic<uint64_t> done{0};
+    if (int rc = allow_smem(slope::row_bwd_stream_kernel<NV>, STREAM_SMEM - 2048, done)) return rc;
+    return launch_pdl(slope::row_bwd_stream_kernel<NV>, dim3((unsigned)p.parts), dim3((unsigned)s.threads),
+                      s.stages * p.D * (p.dres ? 6 : 4), st, what, p, s.stages);
 }
 }  // namespace
 
@@ -1642,7 +1708,7 @@ int slope_rmsnorm(const uint16_t *X, const uint16_t *res, const uint16_t *w, int
     DevInfo d;
     if (int rc = device_info(d)) return rc;
     slope::RowParams p{X, res, w, H, Y, Q, Q ? qscale : nullptr, rstd, T, (int)D, eps};
-    return row_launch<true>(p, static_cast<cudaStream_t>(stream), "rmsnorm launch");
+    return row_launch<true>(p, d.sms, static_cast<cudaStream_t>(stream), "rmsnorm launch");
 }
 
 int slope_quant_rows(const uint16_t *A, int64_t rows, int64_t K, int8_t *Q, float *scale, void *stream) {
@@ -1655,14 +1721,14 @@ int slope_quant_rows(const uint16_t *A, int64_t rows, int64_t K, int8_t *Q, floa
     DevInfo d;
     if (int rc = device_info(d)) return rc;
     slope::RowParams p{A, nullptr, nullptr, nullptr, nullptr, Q, scale, nullptr, rows, (int)K, 0.0f};
-    return row_launch<false>(p, static_cast<cudaStream_t>(stream), "quant_rows launch");
+    return row_launch<false>(p, d.sms, static_cast<cudaStream_t>(stream), "quant_rows launch");
 }
 
 int slope_rmsnorm_bwd_ws(int64_t T, int64_t D, int64_t *floats) {
     if (!floats) return fail(SLOPE_ERR_ARG, "floats is NULL");
     if (int rc = check_tokens(T)) return rc;
     if (int rc = check_width(D, NORM_MAX_D, "D")) return rc;
-    *floats = norm_bwd_parts(T, D) * D;
+    *floats = pick_bwd_plan(T, D).parts * D;
     return SLOPE_OK;
 }
 
@@ -1678,7 +1744,8 @@ int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, 
     CHECK_OPT(dres);
     if (int rc = check_tokens(T)) return rc;
     if (int rc = check_width(D, NORM_MAX_D, "D")) return rc;
-    const int64_t parts = norm_bwd_parts(T, D);
+    const BwdPlan plan = pick_bwd_plan(T, D);
+    const int64_t parts = plan.parts;
     if (ws_floats < parts * D)
         return fail(SLOPE_ERR_SHAPE, "rmsnorm_bwd: ws holds %lld floats, %lld are needed (slope_rmsnorm_bwd_ws)",
                     (long long)ws_floats, (long long)(parts * D));
@@ -1686,12 +1753,17 @@ int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, 
     if (int rc = device_info(d)) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     slope::RowBwdParams p{dY, H, w, rstd, dres, dH, ws, T, (int)D, (int)parts};
-    const RowPlan r = pick_row_plan(D);
+    const RowPlan r = plan.row;
     const dim3 grid((unsigned)parts), block((unsigned)r.threads);
     const char *what = "rmsnorm_bwd launch";
     const int smem = r.warp ? (int)(slope::ROW_WARPS * D * sizeof(float)) : 0;
     int rc;
-    if (r.warp)
+    if (plan.stream.stages > 0)
+        rc = plan.stream.nv == 1   ? row_bwd_stream_launch<1>(p, plan.stream, st, what)
+             : plan.stream.nv == 2 ? row_bwd_stream_launch<2>(p, plan.stream, st, what)
+             : plan.stream.nv == 3 ? row_bwd_stream_launch<3>(p, plan.stream, st, what)
+                                   : row_bwd_stream_launch<4>(p, plan.stream, st, what);
+    else if (r.warp)
         rc = r.nv == 1   ? launch_pdl(slope::row_bwd_kernel<1, true, true>, grid, block, smem, st, what, p)
              : r.nv == 2 ? launch_pdl(slope::row_bwd_kernel<2, true, true>, grid, block, smem, st, what, p)
                          : launch_pdl(slope::row_bwd_kernel<4, true, true>, grid, block, smem, st, what, p);
@@ -1709,18 +1781,6 @@ namespace {
 // ------------------------------------------------------------------ int8 sparse product
 constexpr int Q8_WIDE_SLOT = 42, Q8_TILE_SLOT = 44;  // entries in launch_clusters' table (the tiles': 16)
 constexpr int64_t Q8_MAX_K = 131072;  // 128 * 128 * K / 2 stays below 2^31
-
-// Opt in to `bytes` of dynamic shared memory once per device.
-template <typename Kern>
-int allow_smem(Kern kern, int bytes, std::atomic<uint64_t> &done) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 64 && (done.load() & (1ull << dev))) return SLOPE_OK;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(int8 product)");
-    if (dev < 64) done.fetch_or(1ull << dev);
-    return SLOPE_OK;
-}
 
 struct Q8Plan {
     int bn;      // 0: CUDA cores, else the token width of the tensor-core tile

@@ -52,8 +52,25 @@ __device__ __forceinline__ QuantRow quant_row(float pmax) {
     QuantRow q;
     q.f = pmax < 0x1p-60f ? 0x1p100f : pmax > 0x1p60f ? 0x1p-100f : 1.0f;
     q.pm = pmax * q.f;
-    q.inv = pmax > 0.0f ? __fdiv_rn(127.0f, q.pm) : 0.0f;
+    q.inv = pmax > 0.0f ? __fdividef(127.0f, q.pm) : 0.0f;
     return q;
+}
+
+__device__ __forceinline__ uint2 pack_codes(const float (&m)[8]) {  // the low bytes
+    uint2 r;
+    r.x = __byte_perm(__byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0040),
+                      __byte_perm(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0040), 0x5410);
+    r.y = __byte_perm(__byte_perm(__float_as_uint(m[4]), __float_as_uint(m[5]), 0x0040),
+                      __byte_perm(__float_as_uint(m[6]), __float_as_uint(m[7]), 0x0040), 0x5410);
+    return r;
+}
+constexpr float ROUND_MAGIC = 12582912.0f;  // 1.5 2^23: adding it rounds to an integer in the float's low bits
+
+// The largest of |a|, |b|, |c|, or NaN if one is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // round(127 p / max|p|), ties to even, decided exactly for t = p f: k is the
@@ -61,34 +78,52 @@ __device__ __forceinline__ QuantRow quant_row(float pmax) {
 // 127 t has at most 23 significant bits and k pm too (7 + 16), and their
 // difference d, a multiple of t's last place, fits 24, so d is exact:
 // |d| > pm / 2 moves k by one, |d| = pm / 2 is a tie.
-__device__ __noinline__ float quant_exact(float t, float k, float pm) {
+__device__ __forceinline__ float quant_exact(float t, float k, float pm) {
     const float d = fmaf(-k, pm, 127.0f * t), a = fabsf(d), half = 0.5f * pm;
     const bool odd = (static_cast<int>(k) & 1) != 0;
     return (a > half || (a == half && odd)) ? k + copysignf(1.0f, d) : k;
 }
 
-// Eight values to eight int8 codes.  Adding 1.5 2^23 rounds to an integer in
-// the float's low bits; a quotient within 2^-13 of a border (2.4 in 10^4 of
-// them) is decided again by quant_exact.
-__device__ __forceinline__ uint2 quant8(const float (&p)[8], const QuantRow &q) {
-    constexpr float MAGIC = 12582912.0f;
+// Eight products of two bf16 numbers to int8 codes.  The quotient p inv is off
+// by at most 2^-14 (four units of 2^-24 at 127, p f inv two roundings and inv
+// two units); one within 2^-13 of a border (2.4 in 10^4 of them) is decided
+// again by quant_exact.
+__device__ __forceinline__ uint2 quant8(float (&p)[8], const QuantRow &q) {
+    if (q.f != 1.0f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] *= q.f;
+    }
     float m[8], worst = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float t = p[j] * q.f * q.inv;
-        m[j] = t + MAGIC;
-        worst = fmaxf(worst, fabsf(t - (m[j] - MAGIC)));
+    for (int j = 0; j < 8; j += 2) {
+        const float t0 = p[j] * q.inv, t1 = p[j + 1] * q.inv;
+        m[j] = t0 + ROUND_MAGIC;
+        m[j + 1] = t1 + ROUND_MAGIC;
+        worst = max_abs3(worst, t0 - (m[j] - ROUND_MAGIC), t1 - (m[j + 1] - ROUND_MAGIC));
     }
     if (worst > 0.5f - 0x1p-13f) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = quant_exact(p[j] * q.f, m[j] - MAGIC, q.pm) + MAGIC;
+        for (int j = 0; j < 8; ++j) m[j] = quant_exact(p[j], m[j] - ROUND_MAGIC, q.pm) + ROUND_MAGIC;
     }
-    uint2 r;
-    r.x = __byte_perm(__byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0040),
-                      __byte_perm(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0040), 0x5410);
-    r.y = __byte_perm(__byte_perm(__float_as_uint(m[4]), __float_as_uint(m[5]), 0x0040),
-                      __byte_perm(__float_as_uint(m[6]), __float_as_uint(m[7]), 0x0040), 0x5410);
-    return r;
+    return pack_codes(m);
+}
+
+// Eight bf16 values to int8 codes.  With eight significant bits on either
+// side, a quotient t = 127 a / max|a| that is not a border k + 1/2 is further
+// than t / (254 255) = 1.5 10^-5 t from it, and the computed one is off by at
+// most 3 10^-7 t: rounding it to 18 bits after the leading one (steps of 2^-18,
+// at most 3.8 10^-6 of it) leaves every border exact and moves nothing else
+// onto one or across it, and the rounding to an integer then breaks ties to even.
+__device__ __forceinline__ uint2 quant8_rows(float (&a)[8], const QuantRow &q) {
+    if (q.f != 1.0f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] *= q.f;
+    }
+    float m[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        m[j] = __uint_as_float((__float_as_uint(a[j] * q.inv) + 16u) & ~31u) + ROUND_MAGIC;
+    return pack_codes(m);
 }
 
 struct RowParams {
@@ -117,24 +152,31 @@ __device__ __forceinline__ uint4 add_bf16x8(uint4 x, uint4 e) {
     return make_uint4(a[0], a[1], a[2], a[3]);
 }
 
-// Eight values' share of the row's sum of squares and of its largest |p| (as
-// bits: an infinity or a NaN, whose bits are larger than any number's, wins).
+// Eight values' share of a row's statistics.  The norm: the sum of squares and
+// the largest |h w| as a float's bits (NaN, larger than any number, if one
+// is).  The quantiser: the largest |a| of the even and of the odd values, as
+// two bf16 patterns (an infinity's or a NaN's is larger than any number's).
 template <bool NORM>
 __device__ __forceinline__ void row_stats(uint4 h, uint4 w, bool want_max, float &ss, uint32_t &mx) {
     const uint32_t a[4] = {h.x, h.y, h.z, h.w}, b[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const float2 u = bf16x2_to_float2(a[k]);
         if (NORM) {
+            const float2 u = bf16x2_to_float2(a[k]);
             ss = fmaf(u.x, u.x, fmaf(u.y, u.y, ss));
             if (want_max) {
                 const float2 v = bf16x2_to_float2(b[k]);
-                mx = max(mx, max(__float_as_uint(u.x * v.x) & 0x7FFFFFFFu, __float_as_uint(u.y * v.y) & 0x7FFFFFFFu));
+                mx = __float_as_uint(max_abs3(__uint_as_float(mx), u.x * v.x, u.y * v.y));
             }
         } else {
-            mx = max(mx, max(__float_as_uint(u.x) & 0x7FFFFFFFu, __float_as_uint(u.y) & 0x7FFFFFFFu));
+            mx = __vmaxu2(mx, a[k] & 0x7FFF7FFFu);
         }
     }
+}
+// A thread's statistic as the bits of a float, comparable as an integer.
+template <bool NORM>
+__device__ __forceinline__ uint32_t row_max_bits(uint32_t mx) {
+    return NORM ? mx & 0x7FFFFFFFu : max(mx << 16, mx & 0xFFFF0000u);
 }
 
 // Sum of squares of h 2^-80, eight values (rows whose squares overflow binary32).
@@ -177,10 +219,10 @@ __device__ __forceinline__ void row_outputs(const RowParams &p, int64_t at, uint
             v[2 * k + 1] *= g.y;
         }
     }
-    if (p.Q) *reinterpret_cast<uint2 *>(p.Q + at) = finite ? quant8(v, q) : make_uint2(0, 0);
+    if (p.Q) *reinterpret_cast<uint2 *>(p.Q + at) = !finite ? make_uint2(0, 0) : NORM ? quant8(v, q) : quant8_rows(v, q);
 }
 
-__device__ __forceinline__ float row_rstd(float ss, int D, float eps) { return __frcp_rn(__fsqrt_rn(ss / (float)D + eps)); }
+__device__ __forceinline__ float row_rstd(float ss, float inv_d, float eps) { return rsqrtf(fmaf(ss, inv_d, eps)); }
 
 // NORM: the norm; otherwise the quantiser.  WARP: a warp per row, otherwise a
 // CTA per row, held in registers.  H may be the buffer of X or res, and Y that
@@ -200,6 +242,7 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
     if (WARP && row >= p.T) return;
 
     uint4 h[NV];
+    const float inv_d = 1.0f / (float)p.D;
     const int64_t base = row * p.D;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -227,7 +270,7 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
     for (int i = 0; i < NV; ++i)
         row_stats<NORM>(h[i], p.Q ? weight(gi + i * gsize) : make_uint4(0, 0, 0, 0), p.Q != nullptr, ss, mx);
     if (NORM) ss = warp_sum(ss);
-    mx = __reduce_max_sync(0xffffffffu, mx);
+    mx = __reduce_max_sync(0xffffffffu, row_max_bits<NORM>(mx));
     if (!WARP) {
         if (lane == 0) {
             s_sum[warp] = ss;
@@ -254,9 +297,9 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
                 __syncthreads();
                 s2 = warp_sum(lane < (int)(blockDim.x >> 5) ? s_sum[lane] : 0.0f);
             }
-            rstd = row_rstd(s2, p.D, 0.0f) * 0x1p-80f;
+            rstd = row_rstd(s2, inv_d, 0.0f) * 0x1p-80f;
         } else {
-            rstd = row_rstd(ss, p.D, p.eps);
+            rstd = row_rstd(ss, inv_d, p.eps);
         }
         if (p.rstd && gi == 0 && in_bounds(row, 1, p.T)) p.rstd[row] = rstd;
     }
@@ -323,6 +366,7 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM), stream_ctas(NV)) row
         w[i] = NORM && c < nchunk && in_bounds(8 * c, 8, p.D) ? __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c))
                                                               : make_uint4(0, 0, 0, 0);
     }
+    const float inv_d = 1.0f / (float)p.D;
     int s = 0, turn = 0;
     uint32_t ph = 0;
     for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
@@ -344,7 +388,7 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM), stream_ctas(NV)) row
             row_stats<NORM>(h[i], w[i], p.Q != nullptr, ss, mx);
         }
         if (NORM) ss = warp_sum(ss);
-        mx = __reduce_max_sync(0xffffffffu, mx);
+        mx = __reduce_max_sync(0xffffffffu, row_max_bits<NORM>(mx));
         if (lane == 0) {
             s_sum[turn][warp] = ss;
             s_max[turn][warp] = mx;
@@ -368,9 +412,9 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM), stream_ctas(NV)) row
                 if (lane == 0) s_sum[turn][warp] = s2;
                 __syncthreads();
                 s2 = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
-                rstd = row_rstd(s2, p.D, 0.0f) * 0x1p-80f;
+                rstd = row_rstd(s2, inv_d, 0.0f) * 0x1p-80f;
             } else {
-                rstd = row_rstd(ss, p.D, p.eps);
+                rstd = row_rstd(ss, inv_d, p.eps);
             }
             if (p.rstd && tid == 0 && in_bounds(row, 1, p.T)) p.rstd[row] = rstd;
         }

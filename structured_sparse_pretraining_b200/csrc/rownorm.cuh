@@ -152,23 +152,26 @@ __device__ __forceinline__ uint4 add_bf16x8(uint4 x, uint4 e) {
     return make_uint4(a[0], a[1], a[2], a[3]);
 }
 
-// Eight values' share of a row's statistics.  The norm: the sum of squares and
-// the largest |h w| as a float's bits (NaN, larger than any number, if one
-// is).  The quantiser: the largest |a| of the even and of the odd values, as
-// two bf16 patterns (an infinity's or a NaN's is larger than any number's).
+// Eight values' p = h w (the quantiser: a), and their share of a row's
+// statistics.  The norm: the sum of squares and the largest |p| as a float's
+// bits (NaN, larger than any number, if one is).  The quantiser: the largest
+// |a| of the even and of the odd values, as two bf16 patterns (an infinity's
+// or a NaN's is larger than any number's).
 template <bool NORM>
-__device__ __forceinline__ void row_stats(uint4 h, uint4 w, bool want_max, float &ss, uint32_t &mx) {
+__device__ __forceinline__ void row_stats(uint4 h, uint4 w, float (&v)[8], float &ss, uint32_t &mx) {
     const uint32_t a[4] = {h.x, h.y, h.z, h.w}, b[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
+        const float2 u = bf16x2_to_float2(a[k]);
         if (NORM) {
-            const float2 u = bf16x2_to_float2(a[k]);
+            const float2 g = bf16x2_to_float2(b[k]);
             ss = fmaf(u.x, u.x, fmaf(u.y, u.y, ss));
-            if (want_max) {
-                const float2 v = bf16x2_to_float2(b[k]);
-                mx = __float_as_uint(max_abs3(__uint_as_float(mx), u.x * v.x, u.y * v.y));
-            }
+            v[2 * k] = u.x * g.x;
+            v[2 * k + 1] = u.y * g.y;
+            mx = __float_as_uint(max_abs3(__uint_as_float(mx), v[2 * k], v[2 * k + 1]));
         } else {
+            v[2 * k] = u.x;
+            v[2 * k + 1] = u.y;
             mx = __vmaxu2(mx, a[k] & 0x7FFF7FFFu);
         }
     }
@@ -190,35 +193,14 @@ __device__ __forceinline__ float scaled_squares(uint4 h, float s2) {
     return s2;
 }
 
-// Eight outputs of a row from its h: y = h rstd w and the codes of h w.
+// Eight outputs of a row from its p (h w, or the quantiser's values): y = p rstd and the codes of p.
 template <bool NORM>
-__device__ __forceinline__ void row_outputs(const RowParams &p, int64_t at, uint4 h, uint4 w, float rstd, const QuantRow &q,
+__device__ __forceinline__ void row_outputs(const RowParams &p, int64_t at, float (&v)[8], float rstd, const QuantRow &q,
                                             bool finite) {
-    const uint32_t a[4] = {h.x, h.y, h.z, h.w}, b[4] = {w.x, w.y, w.z, w.w};
-    float v[8];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float2 u = bf16x2_to_float2(a[k]);
-        v[2 * k] = u.x;
-        v[2 * k + 1] = u.y;
-    }
-    if (NORM) {
-        if (p.Y) {
-            uint32_t o[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 g = bf16x2_to_float2(b[k]);
-                o[k] = pack_bf16x2(v[2 * k] * rstd * g.x, v[2 * k + 1] * rstd * g.y);
-            }
-            *reinterpret_cast<uint4 *>(p.Y + at) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 g = bf16x2_to_float2(b[k]);
-            v[2 * k] *= g.x;
-            v[2 * k + 1] *= g.y;
-        }
-    }
+    if (NORM && p.Y)
+        *reinterpret_cast<uint4 *>(p.Y + at) =
+            make_uint4(pack_bf16x2(v[0] * rstd, v[1] * rstd), pack_bf16x2(v[2] * rstd, v[3] * rstd),
+                       pack_bf16x2(v[4] * rstd, v[5] * rstd), pack_bf16x2(v[6] * rstd, v[7] * rstd));
     if (p.Q) *reinterpret_cast<uint2 *>(p.Q + at) = !finite ? make_uint2(0, 0) : NORM ? quant8(v, q) : quant8_rows(v, q);
 }
 
@@ -267,8 +249,10 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
     float ss = 0.0f;
     uint32_t mx = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        row_stats<NORM>(h[i], p.Q ? weight(gi + i * gsize) : make_uint4(0, 0, 0, 0), p.Q != nullptr, ss, mx);
+    for (int i = 0; i < NV; ++i) {
+        float v[8];
+        row_stats<NORM>(h[i], weight(gi + i * gsize), v, ss, mx);
+    }
     if (NORM) ss = warp_sum(ss);
     mx = __reduce_max_sync(0xffffffffu, row_max_bits<NORM>(mx));
     if (!WARP) {
@@ -311,125 +295,159 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = gi + i * gsize;
-        if (c < nchunk && in_bounds(base + 8 * c, 8, total)) row_outputs<NORM>(p, base + 8 * c, h[i], weight(c), rstd, q, finite);
+        if (c < nchunk && in_bounds(base + 8 * c, 8, total)) {
+            float v[8], s_unused = 0.0f;
+            uint32_t m_unused = 0;
+            row_stats<NORM>(h[i], weight(c), v, s_unused, m_unused);
+            row_outputs<NORM>(p, base + 8 * c, v, rstd, q, finite);
+        }
     }
 }
 
-// The same for many rows: persistent CTAs, each with a ring of `stages` rows
-// (X, and res beside it) that bulk copies keep filled, so that the loads of
-// the next rows run beside the arithmetic and the stores of this one.  With
-// one row per CTA and nothing ahead the norm of 8192 x 9216 (9 bytes a value)
-// took 150 us, 69% of the measured copy rate.  The weight stays in registers.
-// One barrier a row: when it falls every thread holds its chunks, and the
-// row's stage is refilled.
+// The same for many rows: persistent groups of threads (a warp up to 1024
+// values, a CTA above), each with a ring of `stages` rows (X, and res beside
+// it) that bulk copies keep filled, so that the loads of the next rows run
+// beside the arithmetic and the stores of this one.  The row and the
+// weight stay in registers between the statistics and the outputs.  With one row per
+// CTA and nothing ahead the norm of 8192 x 9216 (9 bytes a value) took 150 us,
+// 69% of the measured copy rate; here 114 us, 91%.  A CTA's rows take one barrier each: when it
+// falls every thread has read its chunks, and the row's stage is refilled.
 constexpr int STREAM_MAX_STAGES = 4;
-// Up to 384 threads a CTA with NV <= 4 and as many CTAs an SM as the plan asks
-// for; above that one CTA (512 threads of the norm, whose weight takes half
-// the registers, 1024 of the quantiser).
-constexpr int stream_threads(int nv, bool norm) { return nv <= 4 ? 384 : norm ? 512 : 1024; }
-constexpr int stream_ctas(int nv) { return nv <= 3 ? 3 : nv == 4 ? 2 : 1; }
-constexpr int stream_bwd_ctas(int nv) { return nv <= 2 ? 3 : nv == 3 ? 2 : 1; }
-template <int NV, bool NORM>
-__global__ void __launch_bounds__(stream_threads(NV, NORM), stream_ctas(NV)) row_stream_kernel(const __grid_constant__ RowParams p, int stages) {
+constexpr int STREAM_WARPS = 8;  // rows in work at once in a CTA of the warp form
+// Threads at most and CTAs per SM of a form with NV chunks a thread, by
+// measurement at 8192 rows or more.  The norm wants one CTA and a deep ring
+// where a row is long (9216 with residual and both outputs: 114 us with one
+// CTA per SM, 119 with two, 129 with three, which spill) and three below
+// (5120 in bf16: 59 us with three, 62 with two; 2048: 60 with three, 85 with
+// four); the quantiser three (27648 x 4608: 69 us with three, 80 with two, 76
+// with four).  Few chunks to many threads beat more to fewer (16384: 102 us
+// with six, 196 with eight, which spill).
+constexpr int stream_threads(int nv, bool norm, bool warp) { return warp ? 32 * STREAM_WARPS : nv <= 6 ? 384 : norm ? 512 : 1024; }
+constexpr int stream_ctas(int nv, bool norm, bool warp) {
+    return warp ? (nv <= 2 ? 4 : 3) : norm ? (nv <= 2 ? 3 : 1) : nv <= 2 ? 3 : nv <= 4 ? 2 : 1;
+}
+constexpr int stream_bwd_ctas(int nv, bool warp) { return warp ? (nv <= 2 ? 3 : 2) : nv <= 2 ? 3 : nv == 3 ? 2 : 1; }
+template <int NV, bool NORM, bool WARP>
+__global__ void __launch_bounds__(stream_threads(NV, NORM, WARP), stream_ctas(NV, NORM, WARP))
+    row_stream_kernel(const __grid_constant__ RowParams p, int stages) {
     extern __shared__ __align__(16) uint8_t row_smem[];
-    __shared__ __align__(8) uint64_t full[STREAM_MAX_STAGES];
+    constexpr int GROUPS = WARP ? STREAM_WARPS : 1;
+    __shared__ __align__(8) uint64_t s_full[GROUPS][STREAM_MAX_STAGES];
     __shared__ float s_sum[2][32];
     __shared__ uint32_t s_max[2][32];
     __shared__ int abort_flag;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int gi = WARP ? lane : threadIdx.x, gsize = WARP ? 32 : blockDim.x, group = WARP ? warp : 0;
     const int nchunk = p.D >> 3;
     const int64_t total = p.T * p.D;
     const uint32_t row_bytes = (uint32_t)p.D * 2;
     const bool has_res = NORM && p.res;
     const uint32_t stage_bytes = has_res ? 2 * row_bytes : row_bytes;
-    if (tid == 0) {
-        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    uint8_t *ring = row_smem + (uint32_t)(group * stages) * stage_bytes;
+    uint64_t *full = s_full[group];
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < GROUPS * STREAM_MAX_STAGES; ++i) mbar_init(&s_full[0][0] + i, 1);
         abort_flag = 0;
         fence_barrier_init();
     }
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
-    auto fetch = [&](int64_t row, int s) {  // one thread
+    const int64_t row0 = (int64_t)blockIdx.x * GROUPS + group, step = (int64_t)gridDim.x * GROUPS;
+    auto fetch = [&](int64_t row, int s) {  // one thread of the group
         if (row >= p.T || !in_bounds(row * p.D, p.D, total)) return;
-        uint8_t *dst = row_smem + s * stage_bytes;
+        uint8_t *dst = ring + s * stage_bytes;
         mbar_arrive_expect_tx(&full[s], stage_bytes);
         bulk_load(dst, p.X + row * p.D, row_bytes, &full[s]);
         if (has_res) bulk_load(dst + row_bytes, p.res + row * p.D, row_bytes, &full[s]);
     };
-    if (tid == 0)
-        for (int s = 0; s < stages; ++s) fetch((int64_t)blockIdx.x + (int64_t)s * gridDim.x, s);
+    if (gi == 0)
+        for (int s = 0; s < stages; ++s) fetch(row0 + s * step, s);
     uint4 w[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = tid + i * blockDim.x;
+        const int c = gi + i * gsize;
         w[i] = NORM && c < nchunk && in_bounds(8 * c, 8, p.D) ? __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c))
                                                               : make_uint4(0, 0, 0, 0);
     }
     const float inv_d = 1.0f / (float)p.D;
     int s = 0, turn = 0;
     uint32_t ph = 0;
-    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+    for (int64_t row = row0; row < p.T; row += step) {
         const int64_t base = row * p.D;
-        const uint8_t *src = row_smem + s * stage_bytes;
+        const uint8_t *src = ring + s * stage_bytes;
+        auto load_h = [&](int c) {
+            uint4 h = *reinterpret_cast<const uint4 *>(src + 16 * c);
+            if (has_res) h = add_bf16x8(h, *reinterpret_cast<const uint4 *>(src + row_bytes + 16 * c));
+            return h;
+        };
         // a copy that does not come gives up after its limit, and the thread works on what is there
         mbar_wait(&full[s], ph, &abort_flag);
-        uint4 h[NV];
+        __syncwarp();
+        uint4 held[NV];  // h, or the quantiser's row
+        float v[8];
         float ss = 0.0f;
         uint32_t mx = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = tid + i * blockDim.x;
-            h[i] = make_uint4(0, 0, 0, 0);
+            const int c = gi + i * gsize;
+            uint4 h = make_uint4(0, 0, 0, 0);
             if (c < nchunk) {
-                h[i] = *reinterpret_cast<const uint4 *>(src + 16 * c);
-                if (has_res) h[i] = add_bf16x8(h[i], *reinterpret_cast<const uint4 *>(src + row_bytes + 16 * c));
+                h = load_h(c);
+                if (has_res && p.H && in_bounds(base + 8 * c, 8, total)) *reinterpret_cast<uint4 *>(p.H + base + 8 * c) = h;
             }
-            row_stats<NORM>(h[i], w[i], p.Q != nullptr, ss, mx);
+            row_stats<NORM>(h, w[i], v, ss, mx);
+            held[i] = h;
         }
         if (NORM) ss = warp_sum(ss);
         mx = __reduce_max_sync(0xffffffffu, row_max_bits<NORM>(mx));
-        if (lane == 0) {
-            s_sum[turn][warp] = ss;
-            s_max[turn][warp] = mx;
+        if (!WARP) {
+            if (lane == 0) {
+                s_sum[turn][warp] = ss;
+                s_max[turn][warp] = mx;
+            }
+            __syncthreads();
+            if (NORM) ss = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
+            mx = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[turn][lane] : 0u);
         }
-        __syncthreads();
-        if (tid == 0) fetch(row + (int64_t)stages * gridDim.x, s);
-        if (++s == stages) {
-            s = 0;
-            ph ^= 1;
-        }
-        ss = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
-        mx = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[turn][lane] : 0u);
         float rstd = 1.0f;
         if (NORM) {
+            rstd = row_rstd(ss, inv_d, p.eps);
             if (__float_as_uint(ss) == kInfBits) {  // see row_kernel
                 float s2 = 0.0f;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) s2 = scaled_squares(h[i], s2);
+                for (int i = 0; i < NV; ++i) s2 = scaled_squares(held[i], s2);
                 s2 = warp_sum(s2);
-                __syncthreads();
-                if (lane == 0) s_sum[turn][warp] = s2;
-                __syncthreads();
-                s2 = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
+                if (!WARP) {
+                    __syncthreads();
+                    if (lane == 0) s_sum[turn][warp] = s2;
+                    __syncthreads();
+                    s2 = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
+                }
                 rstd = row_rstd(s2, inv_d, 0.0f) * 0x1p-80f;
-            } else {
-                rstd = row_rstd(ss, inv_d, p.eps);
             }
-            if (p.rstd && tid == 0 && in_bounds(row, 1, p.T)) p.rstd[row] = rstd;
+        }
+        if (gi == 0) {
+            // every thread of the group has read the stage
+            fetch(row + stages * step, s);
+            if (NORM && p.rstd && in_bounds(row, 1, p.T)) p.rstd[row] = rstd;
+        }
+        if (++s == stages) {
+            s = 0;
+            ph ^= 1;
         }
         turn ^= 1;  // the next row's sums go beside this row's, which other warps may still read
         const bool finite = mx < kInfBits;
         const float pmax = __uint_as_float(mx);
         const QuantRow q = quant_row(finite ? pmax : 0.0f);
-        if (p.Q && tid == 0 && in_bounds(row, 1, p.T))
+        if (p.Q && gi == 0 && in_bounds(row, 1, p.T))
             p.qscale[row] = finite ? rstd * pmax / 127.0f : __uint_as_float(0x7FC00000u);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = tid + i * blockDim.x;
+            const int c = gi + i * gsize;
             if (c < nchunk && in_bounds(base + 8 * c, 8, total)) {
-                if (has_res && p.H) *reinterpret_cast<uint4 *>(p.H + base + 8 * c) = h[i];
-                row_outputs<NORM>(p, base + 8 * c, h[i], w[i], rstd, q, finite);
+                row_stats<NORM>(held[i], w[i], v, ss, mx);  // p again
+                row_outputs<NORM>(p, base + 8 * c, v, rstd, q, finite);
             }
         }
     }
@@ -566,42 +584,48 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_bwd_kernel(c
 // The same with the ring of row_stream_kernel: dY, H and dres of the next rows
 // arrive by bulk copy while this row is worked on; the second pass reads the
 // row again from shared memory, so registers hold only the sums of dY n and
-// the weight.  A stage is refilled after the next row's barrier, when every
-// thread is done with it.
-template <int NV>
-__global__ void __launch_bounds__(384, stream_bwd_ctas(NV)) row_bwd_stream_kernel(const __grid_constant__ RowBwdParams p, int stages) {
+// the weight.  A warp refills a stage after its own second pass, a CTA after
+// the next row's barrier, when every thread is done with it.
+template <int NV, bool WARP>
+__global__ void __launch_bounds__(stream_threads(NV, true, WARP), stream_bwd_ctas(NV, WARP))
+    row_bwd_stream_kernel(const __grid_constant__ RowBwdParams p, int stages) {
     extern __shared__ __align__(16) uint8_t row_smem[];
-    __shared__ __align__(8) uint64_t full[STREAM_MAX_STAGES];
+    constexpr int GROUPS = WARP ? STREAM_WARPS : 1;
+    __shared__ __align__(8) uint64_t s_full[GROUPS][STREAM_MAX_STAGES];
     __shared__ float s_sum[2][32];
     __shared__ int abort_flag;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int gi = WARP ? lane : threadIdx.x, gsize = WARP ? 32 : blockDim.x, group = WARP ? warp : 0;
     const int nchunk = p.D >> 3;
     const int64_t total = p.T * p.D;
     const uint32_t row_bytes = (uint32_t)p.D * 2;
     const uint32_t stage_bytes = (p.dres ? 3 : 2) * row_bytes;
-    if (tid == 0) {
-        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    uint8_t *ring = row_smem + (uint32_t)(group * stages) * stage_bytes;
+    uint64_t *full = s_full[group];
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < GROUPS * STREAM_MAX_STAGES; ++i) mbar_init(&s_full[0][0] + i, 1);
         abort_flag = 0;
         fence_barrier_init();
     }
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
-    auto fetch = [&](int64_t row, int s) {  // one thread
+    const int64_t row0 = (int64_t)blockIdx.x * GROUPS + group, step = (int64_t)gridDim.x * GROUPS;
+    auto fetch = [&](int64_t row, int s) {  // one thread of the group
         if (row >= p.T || !in_bounds(row * p.D, p.D, total)) return;
-        uint8_t *dst = row_smem + s * stage_bytes;
+        uint8_t *dst = ring + s * stage_bytes;
         mbar_arrive_expect_tx(&full[s], stage_bytes);
         bulk_load(dst, p.H + row * p.D, row_bytes, &full[s]);
         bulk_load(dst + row_bytes, p.dY + row * p.D, row_bytes, &full[s]);
         if (p.dres) bulk_load(dst + 2 * row_bytes, p.dres + row * p.D, row_bytes, &full[s]);
     };
-    if (tid == 0)
-        for (int s = 0; s < stages; ++s) fetch((int64_t)blockIdx.x + (int64_t)s * gridDim.x, s);
+    if (gi == 0)
+        for (int s = 0; s < stages; ++s) fetch(row0 + s * step, s);
     uint4 w[NV];
     float acc[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = tid + i * blockDim.x;
+        const int c = gi + i * gsize;
         w[i] = c < nchunk && in_bounds(8 * c, 8, p.D) ? __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
@@ -609,15 +633,16 @@ __global__ void __launch_bounds__(384, stream_bwd_ctas(NV)) row_bwd_stream_kerne
     const float inv_d = 1.0f / (float)p.D;
     int s = 0, turn = 0;
     uint32_t ph = 0;
-    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
+    for (int64_t row = row0; row < p.T; row += step) {
         const int64_t base = row * p.D;
-        const uint8_t *src = row_smem + s * stage_bytes;
+        const uint8_t *src = ring + s * stage_bytes;
         const float rstd = in_bounds(row, 1, p.T) ? __ldg(p.rstd + row) : 0.0f;
         mbar_wait(&full[s], ph, &abort_flag);
+        __syncwarp();
         float dot = 0.0f;  // sum of g n
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = tid + i * blockDim.x;
+            const int c = gi + i * gsize;
             if (c < nchunk) {
                 const uint4 hv = *reinterpret_cast<const uint4 *>(src + 16 * c);
                 const uint4 gv = *reinterpret_cast<const uint4 *>(src + row_bytes + 16 * c);
@@ -634,16 +659,18 @@ __global__ void __launch_bounds__(384, stream_bwd_ctas(NV)) row_bwd_stream_kerne
             }
         }
         dot = warp_sum(dot);
-        if (lane == 0) s_sum[turn][warp] = dot;
-        __syncthreads();
-        // the stage of the row before: every thread has left its second pass
-        if (tid == 0 && row > blockIdx.x) fetch(row + (int64_t)(stages - 1) * gridDim.x, s == 0 ? stages - 1 : s - 1);
-        dot = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
-        turn ^= 1;
+        if (!WARP) {
+            if (lane == 0) s_sum[turn][warp] = dot;
+            __syncthreads();
+            // the stage of the row before: every thread has left its second pass
+            if (gi == 0 && row > row0) fetch(row + (stages - 1) * step, s == 0 ? stages - 1 : s - 1);
+            dot = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
+            turn ^= 1;
+        }
         const float mean = dot * inv_d;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = tid + i * blockDim.x;
+            const int c = gi + i * gsize;
             if (c < nchunk && in_bounds(base + 8 * c, 8, total)) {
                 const uint4 hv = *reinterpret_cast<const uint4 *>(src + 16 * c);
                 const uint4 gv = *reinterpret_cast<const uint4 *>(src + row_bytes + 16 * c);
@@ -662,19 +689,35 @@ __global__ void __launch_bounds__(384, stream_bwd_ctas(NV)) row_bwd_stream_kerne
                 *reinterpret_cast<uint4 *>(p.dH + base + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
             }
         }
+        if (WARP) {
+            __syncwarp();
+            if (gi == 0) fetch(row + stages * step, s);
+        }
         if (++s == stages) {
             s = 0;
             ph ^= 1;
         }
     }
+    // this CTA's partial row; the warps of the warp form add theirs in warp order, in the rings' memory
     const int64_t pbase = (int64_t)blockIdx.x * p.D, ptotal = (int64_t)p.parts * p.D;
+    float *s_dw = reinterpret_cast<float *>(row_smem);  // [STREAM_WARPS][D], no more than the rings' 4 D bytes a stage
+    if (WARP) __syncthreads();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = tid + i * blockDim.x;
-        if (c < nchunk && in_bounds(pbase + 8 * c, 8, ptotal)) {
-            float4 *dst = reinterpret_cast<float4 *>(p.part + pbase + 8 * c);
+        const int c = gi + i * gsize;
+        if (c < nchunk && (WARP || in_bounds(pbase + 8 * c, 8, ptotal))) {
+            float4 *dst = reinterpret_cast<float4 *>((WARP ? s_dw + warp * p.D : p.part + pbase) + 8 * c);
             dst[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
             dst[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+        }
+    }
+    if (WARP) {
+        __syncthreads();
+        for (int d = threadIdx.x; d < p.D; d += blockDim.x) {
+            float t = s_dw[d];
+#pragma unroll
+            for (int k = 1; k < STREAM_WARPS; ++k) t += s_dw[k * p.D + d];
+            if (in_bounds(pbase + d, 1, ptotal)) p.part[pbase + d] = t;
         }
     }
 }

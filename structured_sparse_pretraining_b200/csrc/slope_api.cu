@@ -1595,24 +1595,31 @@ RowPlan pick_row_plan(int64_t D) {
     return RowPlan{false, nv, (chunks + 32 * nv - 1) / (32 * nv) * 32};
 }
 
-// Rings of rows for many rows (row_stream_kernel and row_bwd_stream_kernel):
-// nv 16-byte chunks per thread, CTAs per SM by their threads, and as many
-// stages as shared memory holds; stages = 0 where not two rows of
-// `row_bytes` fit.
+// Rings of rows for many rows (row_stream_kernel and row_bwd_stream_kernel): a
+// warp's or a CTA's, nv 16-byte chunks per thread, CTAs per SM, and as many
+// stages as shared memory holds; stages = 0 where not two rows of `row_bytes`
+// fit.
 struct StreamPlan {
-    int nv, threads, per_sm, stages;
+    bool warp;
+    int nv, threads, per_sm, stages, smem, rows;  // rows in work at once in a CTA
 };
 constexpr int STREAM_SMEM = 224 * 1024;  // of an SM, for its CTAs' rings
-StreamPlan pick_stream_plan(int64_t D, int64_t row_bytes, bool backward) {
+StreamPlan pick_stream_plan(int64_t D, int64_t row_bytes, bool norm, bool backward) {
     const int chunks = (int)(D / 8);
-    const int nv = chunks <= 4 * 384 ? (chunks + 383) / 384 : 8;
-    StreamPlan s{nv, (chunks + 32 * nv - 1) / (32 * nv) * 32, 0, 0};
-    for (s.per_sm = backward ? slope::stream_bwd_ctas(nv) : slope::stream_ctas(nv); s.per_sm >= 1; --s.per_sm) {
-        const int64_t fit = (STREAM_SMEM / s.per_sm - 2048) / row_bytes;
+    StreamPlan s{};
+    s.warp = chunks <= 128;
+    const int most_nv = norm && !backward ? 6 : 4;  // with 384 threads; longer rows take 8
+    s.nv = s.warp ? (chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4) : chunks <= most_nv * 384 ? (chunks + 383) / 384 : 8;
+    s.threads = s.warp ? 32 * slope::STREAM_WARPS : (chunks + 32 * s.nv - 1) / (32 * s.nv) * 32;
+    s.rows = s.warp ? slope::STREAM_WARPS : 1;
+    s.per_sm = backward ? slope::stream_bwd_ctas(s.nv, s.warp) : slope::stream_ctas(s.nv, norm, s.warp);
+    for (; s.per_sm >= 1; --s.per_sm) {
+        const int64_t fit = (STREAM_SMEM / s.per_sm - 2048) / (row_bytes * s.rows);
         s.stages = (int)(fit > slope::STREAM_MAX_STAGES ? slope::STREAM_MAX_STAGES : fit);
         if (s.stages >= 2) break;
     }
     if (s.stages < 2) s.stages = 0;
+    s.smem = (int)(s.stages * s.rows * row_bytes);
     return s;
 }
 
@@ -1628,26 +1635,35 @@ int allow_smem(Kern kern, int bytes, std::atomic<uint64_t> &done) {
     return SLOPE_OK;
 }
 
-template <int NV, bool NORM>
-int row_stream_launch(const slope::RowParams &p, const StreamPlan &s, int row_bytes, int sms, cudaStream_t st, const char *what) {
+template <int NV, bool NORM, bool WARP>
+int row_stream_launch(const slope::RowParams &p, const StreamPlan &s, int sms, cudaStream_t st, const char *what) {
     static std::atomic<uint64_t> done{0};
-    if (int rc = allow_smem(slope::row_stream_kernel<NV, NORM>, STREAM_SMEM - 2048, done)) return rc;
+    if (int rc = allow_smem(slope::row_stream_kernel<NV, NORM, WARP>, STREAM_SMEM - 2048, done)) return rc;
     const int64_t most = (int64_t)sms * s.per_sm;
-    return launch_pdl(slope::row_stream_kernel<NV, NORM>, dim3((unsigned)(p.T < most ? p.T : most)), dim3((unsigned)s.threads),
-                      s.stages * row_bytes, st, what, p, s.stages);
+    return launch_pdl(slope::row_stream_kernel<NV, NORM, WARP>, dim3((unsigned)most), dim3((unsigned)s.threads), s.smem, st, what,
+                      p, s.stages);
 }
 
 template <bool NORM>
 int row_launch(const slope::RowParams &p, int sms, cudaStream_t st, const char *what) {
     const RowPlan r = pick_row_plan(p.D);
-    const int row_bytes = p.D * (p.res ? 4 : 2);
-    const StreamPlan s = pick_stream_plan(p.D, row_bytes, false);
-    if (!r.warp && s.stages > 0 && p.T >= 2 * (int64_t)sms * s.per_sm) {
-        if (s.nv == 1) return row_stream_launch<1, NORM>(p, s, row_bytes, sms, st, what);
-        if (s.nv == 2) return row_stream_launch<2, NORM>(p, s, row_bytes, sms, st, what);
-        if (s.nv == 3) return row_stream_launch<3, NORM>(p, s, row_bytes, sms, st, what);
-        if (s.nv == 4) return row_stream_launch<4, NORM>(p, s, row_bytes, sms, st, what);
-        return row_stream_launch<8, NORM>(p, s, row_bytes, sms, st, what);
+    const StreamPlan s = pick_stream_plan(p.D, p.D * (p.res ? 4 : 2), NORM, false);
+    // rings pay from two rows for each of their groups on
+    if (s.stages > 0 && p.T >= 2 * (int64_t)sms * s.per_sm * s.rows) {
+        if (s.warp) {
+            if (s.nv == 1) return row_stream_launch<1, NORM, true>(p, s, sms, st, what);
+            if (s.nv == 2) return row_stream_launch<2, NORM, true>(p, s, sms, st, what);
+            return row_stream_launch<4, NORM, true>(p, s, sms, st, what);
+        }
+        if (s.nv == 1) return row_stream_launch<1, NORM, false>(p, s, sms, st, what);
+        if (s.nv == 2) return row_stream_launch<2, NORM, false>(p, s, sms, st, what);
+        if (s.nv == 3) return row_stream_launch<3, NORM, false>(p, s, sms, st, what);
+        if (s.nv == 4) return row_stream_launch<4, NORM, false>(p, s, sms, st, what);
+        if constexpr (NORM) {
+            if (s.nv == 5) return row_stream_launch<5, NORM, false>(p, s, sms, st, what);
+            if (s.nv == 6) return row_stream_launch<6, NORM, false>(p, s, sms, st, what);
+        }
+        return row_stream_launch<8, NORM, false>(p, s, sms, st, what);
     }
     const int64_t blocks = r.warp ? (p.T + slope::ROW_WARPS - 1) / slope::ROW_WARPS : p.T;
     const dim3 grid((unsigned)blocks), block((unsigned)r.threads);
@@ -1670,20 +1686,20 @@ struct BwdPlan {
     int64_t parts;
 };
 BwdPlan pick_bwd_plan(int64_t T, int64_t D) {
-    BwdPlan b{pick_row_plan(D), pick_stream_plan(D, 6 * D, true), 0};
-    if (b.row.warp || b.stream.nv > 4 || T < 2 * 148 * (int64_t)b.stream.per_sm) b.stream.stages = 0;
+    BwdPlan b{pick_row_plan(D), pick_stream_plan(D, 6 * D, true, true), 0};
+    if (b.stream.nv > 4 || T < 2 * 148 * (int64_t)b.stream.per_sm * b.stream.rows) b.stream.stages = 0;
     const int64_t per_sm = b.stream.stages ? b.stream.per_sm : 1536 / b.row.threads < 1 ? 1 : 1536 / b.row.threads > 4 ? 4 : 1536 / b.row.threads;
     const int64_t blocks = b.row.warp ? (T + slope::ROW_WARPS - 1) / slope::ROW_WARPS : T;
     b.parts = blocks < 148 * per_sm ? blocks : 148 * per_sm;
     return b;
 }
 
-template <int NV>
+template <int NV, bool WARP>
 int row_bwd_stream_launch(const slope::RowBwdParams &p, const StreamPlan &s, cudaStream_t st, const char *what) {
     static std::atomic<uint64_t> done{0};
-    if (int rc = allow_smem(slope::row_bwd_stream_kernel<NV>, STREAM_SMEM - 2048, done)) return rc;
-    return launch_pdl(slope::row_bwd_stream_kernel<NV>, dim3((unsigned)p.parts), dim3((unsigned)s.threads),
-                      s.stages * p.D * (p.dres ? 6 : 4), st, what, p, s.stages);
+    if (int rc = allow_smem(slope::row_bwd_stream_kernel<NV, WARP>, STREAM_SMEM - 2048, done)) return rc;
+    return launch_pdl(slope::row_bwd_stream_kernel<NV, WARP>, dim3((unsigned)p.parts), dim3((unsigned)s.threads), s.smem, st,
+                      what, p, s.stages);
 }
 }  // namespace
 
@@ -1759,10 +1775,13 @@ int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, 
     const int smem = r.warp ? (int)(slope::ROW_WARPS * D * sizeof(float)) : 0;
     int rc;
     if (plan.stream.stages > 0)
-        rc = plan.stream.nv == 1   ? row_bwd_stream_launch<1>(p, plan.stream, st, what)
-             : plan.stream.nv == 2 ? row_bwd_stream_launch<2>(p, plan.stream, st, what)
-             : plan.stream.nv == 3 ? row_bwd_stream_launch<3>(p, plan.stream, st, what)
-                                   : row_bwd_stream_launch<4>(p, plan.stream, st, what);
+        rc = plan.stream.warp ? (plan.stream.nv == 1   ? row_bwd_stream_launch<1, true>(p, plan.stream, st, what)
+                                 : plan.stream.nv == 2 ? row_bwd_stream_launch<2, true>(p, plan.stream, st, what)
+                                                       : row_bwd_stream_launch<4, true>(p, plan.stream, st, what))
+             : plan.stream.nv == 1 ? row_bwd_stream_launch<1, false>(p, plan.stream, st, what)
+             : plan.stream.nv == 2 ? row_bwd_stream_launch<2, false>(p, plan.stream, st, what)
+             : plan.stream.nv == 3 ? row_bwd_stream_launch<3, false>(p, plan.stream, st, what)
+                                   : row_bwd_stream_launch<4, false>(p, plan.stream, st, what);
     else if (r.warp)
         rc = r.nv == 1   ? launch_pdl(slope::row_bwd_kernel<1, true, true>, grid, block, smem, st, what, p)
              : r.nv == 2 ? launch_pdl(slope::row_bwd_kernel<2, true, true>, grid, block, smem, st, what, p)
@@ -1789,8 +1808,53 @@ struct Q8Plan {
     bool wide;   // q8_wide_kernel: 512 x 224 pair tiles
 };
 
-Q8Plan pick_q8_plan(int64_t M, int64_t T, int64_t K, int sms) {
-    if (T <= 4 || M < 128) {
+// The product's form, by a model of each form's time in microseconds, from
+// sweeps on B200 (layers of 512 to 36864 channels, 1 to 8192 tokens).
+//  * Tensor-core tiles of 128 channels x bn tokens: a round of the persistent
+//    clusters costs its k-tiles (a split's share of K, and the adapter's) at
+//    0.48 us each, 0.62 at bn = 128 (the ring then holds three stages), or its
+//    epilogue where that is longer, after 4.5 us and half a microsecond for
+//    each doubling of the split.
+//  * 512 x 224 tiles: 0.82 us a k-tile of a round, about 3.7 us for its drain,
+//    and 7 us.  From about 400 tokens on they win wherever the layer has tiles
+//    for most SM pairs (5120 -> 20480 at 400 tokens: 43 us against 57; 1024 ->
+//    4096: 12.5 against 8.3).
+//  * CUDA cores, up to 4 tokens: 3 us, and 0.3 us for each megabyte of weights,
+//    a third as much again for each further token (1024 -> 4096 at one token
+//    4.3 us against the tiles' 5.3, 4096 -> 4096 5.7 against 8.3; 9216 -> 27648
+//    37 against 32).
+Q8Plan pick_q8_plan(int64_t M, int64_t T, int64_t K, int64_t r, int sms) {
+    const int64_t kts = (K + 255) / 256, adp = (r + 63) / 64;
+    Q8Plan best{0, 1, 0, false};
+    double best_us = 1e300;
+    if (M >= 128) {
+        const int bns[4] = {16, 32, 64, 128};
+        for (int bn : bns) {
+            if (bn > 16 && T <= bn / 2) break;  // half the columns would be empty
+            const int64_t tiles = (M + 127) / 128 * ((T + bn - 1) / bn);
+            double us = 4.5;
+            for (int s = 1; s <= 8 && s <= kts; s *= 2, us += 0.5) {
+                const int64_t clusters = sms / s > 0 ? sms / s : 1;
+                const double main_us = (double)((kts + s - 1) / s + adp) * (bn == 128 ? 0.62 : 0.48);
+                const double drain_us = 0.6 + 0.027 * bn / s;
+                const double t = us + (double)((tiles + clusters - 1) / clusters) * (main_us > drain_us ? main_us : drain_us);
+                if (t < best_us) {
+                    best_us = t;
+                    best = Q8Plan{bn, s, 0, false};
+                }
+            }
+        }
+        if (K % 128 == 0) {
+            const int64_t tiles = (M + 511) / 512 * ((T + 223) / 224), pairs = sms / 2 > 0 ? sms / 2 : 1;
+            const double t = 7.0 + (double)((tiles + pairs - 1) / pairs) * ((double)kts + 4.5) * 0.82;
+            if (t < best_us) {
+                best_us = t;
+                best = Q8Plan{224, 1, 0, true};
+            }
+        }
+    }
+    const double mb = (double)M * (double)K * 0.625e-6;
+    if (M < 128 || (T <= 4 && 3.0 + mb * 0.3 * (1.0 + 0.35 * (double)(T - 1)) < best_us)) {
         const int64_t row = (K + 1023) / 1024 * 1024;
         int tb = T >= 3 ? 4 : (int)T;
         while (tb > 1 && tb * row > 200 * 1024) tb /= 2;
@@ -1798,21 +1862,6 @@ Q8Plan pick_q8_plan(int64_t M, int64_t T, int64_t K, int sms) {
         int ks = 1;
         while (ks < slope::SQ8_WARPS && M / slope::SQ8_ROWS * ks * 2 <= (int64_t)sms * slope::SQ8_WARPS && ks * 1024 < K) ks *= 2;
         return Q8Plan{0, ks, tb, false};
-    }
-    if (T >= 1024 && K % 128 == 0) return Q8Plan{224, 1, 0, true};
-    const int bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
-    // rounds of the persistent clusters times k-tiles of a round (the adapter's among them), and what joining
-    // the partials adds at the end
-    const int64_t kts = (K + 255) / 256, tiles = (M + 127) / 128 * ((T + bn - 1) / bn);
-    Q8Plan best{bn, 1, 0, false};
-    double best_cost = 1e300;
-    for (int s = 1; s <= 8 && s <= kts; s *= 2) {
-        const int64_t clusters = sms / s;
-        const double cost = (double)((tiles + clusters - 1) / clusters) * ((double)((kts + s - 1) / s) + 2.0) + (s > 1 ? 1.0 : 0.0);
-        if (cost < best_cost) {
-            best_cost = cost;
-            best.splits = s;
-        }
     }
     return best;
 }
@@ -1844,7 +1893,7 @@ int q8_product(const int8_t *X, const float *xscale, const int8_t *W, const floa
                const uint16_t *XL, const uint16_t *R, int64_t T, int64_t K, int64_t M, int64_t r, uint16_t *Y, cudaStream_t st) {
     DevInfo d;
     if (int rc = device_info(d)) return rc;
-    const Q8Plan plan = pick_q8_plan(M, T, K, d.sms);
+    const Q8Plan plan = pick_q8_plan(M, T, K, r, d.sms);
     if (plan.bn == 0) {
         // the grid's second dimension counts blocks of tb tokens
         for (int64_t t0 = 0; t0 < T;) {

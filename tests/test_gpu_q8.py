@@ -38,7 +38,7 @@ def depth(D):
 # ------------------------------------------------------------------ quantiser
 @pytest.mark.parametrize("rows,K", [(1, 8), (3, 16), (5, 64), (130, 264), (33, 512), (7, 520), (4, 1000), (9, 1024), (6, 1032),
                                     (3, 4608), (2, 16384), (2, 16392), (2, 36864), (1, 65536), (2000, 96),
-                                    (1000, 1032), (2049, 4608), (900, 8200), (700, 12288), (333, 36864), (300, 65536)])
+                                    (10000, 72), (9600, 512), (7201, 1000), (1000, 1032), (2049, 4608), (900, 8200), (700, 12288), (333, 36864), (300, 65536)])
 def test_quant_rows(rows, K):
     A = P.random_bf16((rows, K), 0.02, 1)
     if rows > 2:
@@ -85,7 +85,7 @@ def test_quant_rows_not_finite():
 NORM_SHAPES = [(1, 8), (1, 9216), (5, 64), (7, 248), (9, 256), (6, 264), (3, 520), (130, 768), (4, 1000), (5, 1024), (3, 1032),
                (11, 5120), (2, 16384), (3, 16392), (2, 32768), (1027, 512),
               # many rows: the ring of rows, every number of chunks per thread, one and several stages' turns
-              (1100, 1040), (1201, 3080), (1333, 5120), (903, 6152), (950, 9216), (700, 12288), (400, 12296), (310, 24576), (300, 32768)]
+              (5000, 64), (4801, 264), (7200, 520), (8000, 1000), (9001, 1024), (1100, 1040), (1201, 3080), (1333, 5120), (903, 6152), (950, 9216), (700, 12288), (400, 12296), (310, 24576), (300, 32768)]
 
 
 @pytest.mark.parametrize("T,D", NORM_SHAPES)
@@ -163,6 +163,14 @@ def test_rmsnorm_not_finite_and_huge():
     within(rss[ok], rstds[ok], rel * rstds[ok], "rstd")
     within(ss[ok], qss[ok], (rel + 3 * P.F32) * qss[ok], "qscale")
     within(Ys[ok], ys[ok], (P.BF16 + 3 * rel) * ys[ok].abs() + 2.0 ** -134, "Y")
+    Xs = Xs[:, :512].repeat(8, 1).contiguous()  # and by warps
+    Qs, ss, Ys, _, rss = ops.rmsnorm_q8(Xs, wq[:512].contiguous(), EPS, with_y=True, with_rstd=True)
+    _, ys, rstds, qs_, qss = P.norm(Xs, wq[:512], EPS)
+    assert torch.equal(Qs, qs_) and torch.equal(torch.isnan(ss), torch.isnan(qss))
+    ok = torch.isfinite(Xs.float()).all(1)
+    within(rss[ok], rstds[ok], rel * rstds[ok], "rstd")
+    within(ss[ok], qss[ok], (rel + 3 * P.F32) * qss[ok], "qscale")
+    within(Ys[ok], ys[ok], (P.BF16 + 3 * rel) * ys[ok].abs() + 2.0 ** -134, "Y")
     # a wide row takes the CTA's path through the same branch
     Xw = P.random_bf16((2, 5120), 1.0, 7) * 2.0 ** 110
     Yw, _, rw = ops.rmsnorm(Xw, torch.ones(5120, dtype=torch.bfloat16, device="cuda"), EPS, with_rstd=True)
@@ -171,7 +179,7 @@ def test_rmsnorm_not_finite_and_huge():
     within(Yw, yw, (P.BF16 + 3 * rel) * yw.abs(), "Y")
 
 
-@pytest.mark.parametrize("T,D", [(5, 512), (3, 5120), (1500, 2048)])
+@pytest.mark.parametrize("T,D", [(5, 512), (3, 5120), (1500, 2048), (9000, 512)])
 def test_rmsnorm_in_place(T, D):
     X, e = P.random_bf16((T, D), 1.0, 8), P.random_bf16((T, D), 2.0, 9)
     w = P.random_bf16((D,), 1.0, 10)
@@ -434,7 +442,7 @@ def test_refusals_on_the_gpu():
         ops.fwd_q8(Xq.float(), xs, Wq, ws, meta, XL, R, 64)
 
 
-@pytest.mark.parametrize("T,D", [(9, 264), (5, 5120), (1201, 1544)])
+@pytest.mark.parametrize("T,D", [(9, 264), (5, 5120), (1201, 1544), (8001, 520)])
 def test_no_writes_outside_outputs(T, D):
     X, e, w = P.random_bf16((T, D), 1.0, 1), P.random_bf16((T, D), 1.0, 2), P.random_bf16((D,), 1.0, 3)
     G = lambda shape, t: guarded_empty(shape, t)  # noqa: E731

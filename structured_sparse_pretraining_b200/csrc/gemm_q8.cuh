@@ -84,6 +84,24 @@ __device__ __forceinline__ void q8_store(const float (&v)[W], const Q8Params &p,
     }
 }
 
+// A 128 x 32-byte code tile (rows from m0, k-tile kt) into `e` in the 32-byte
+// swizzle, as 8-byte copies of one warp: for code rows of K/8 bytes that are
+// not a multiple of 16, which TMA cannot address.  Words past the row are
+// zeros that no MMA reads.
+__device__ __forceinline__ void q8_copy_codes(uint8_t *e, const uint16_t *meta, int M, int K, int m0, int kt, int lane) {
+    const int words = K >> 4;  // a multiple of 4
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = lane + 32 * i, x = (row >> 2) & 1;
+        const int64_t at = (int64_t)(m0 + row) * words + kt * 16;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const bool in = kt * 16 + 4 * c < words && in_bounds(at + 4 * c, 4, (int64_t)M * words);
+            cp_async8(e + row * 32 + 16 * ((c >> 1) ^ x) + 8 * (c & 1), in ? meta + at + 4 * c : meta, in ? 8u : 0u);
+        }
+    }
+}
+
 template <int BN>
 __global__ void __launch_bounds__(224, 1)
     q8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -318,38 +336,35 @@ __global__ void __launch_bounds__(224, 1)
         }
     } else if (!p.meta_tma) {
         // ------------------------------------------------------------ code loader
-        const int words = p.K >> 4;  // code words of a row; a multiple of 4
-        int s = 0;
+        // LAG stages of copies stay in flight: a stage is published once the copies of the LAG after it are issued,
+        // which needs stages that the MMAs have already passed (LAG < NS)
+        constexpr int LAG = NS >= 4 ? NS - 2 : 1;
+        int s = 0, issued = 0, published = 0;
         uint32_t ph = 0;
+        auto publish = [&]() {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[published % NS]);
+            ++published;
+        };
         for (int w = cluster; w < p.num_work; w += num_clusters) {
             const int m0 = min(w % p.m_tiles * 128, p.M - 128);
             for (int kt = k0; kt < k1 + adp_kts; ++kt) {
-                if (!mbar_wait_warp(&empty[s], ph ^ 1, abort_flag)) goto done;
-                if (kt < k1) {
-                    uint8_t *e = smem + s * C::STAGE_BYTES + C::A_BYTES + 2 * C::B_PANEL;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = lane + 32 * i;
-                        uint2 cw[4];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int w0 = kt * 16 + 4 * c;
-                            const int64_t at = (int64_t)(m0 + row) * words + w0;
-                            cw[c] = make_uint2(0x44444444u, 0x44444444u);
-                            if (w0 < words && in_bounds(at, 4, (int64_t)p.M * words))
-                                cw[c] = *reinterpret_cast<const uint2 *>(p.meta + at);
-                        }
-                        const int x = (row >> 2) & 1;  // the 32-byte swizzle
-                        *reinterpret_cast<uint4 *>(e + row * 32 + 16 * x) = make_uint4(cw[0].x, cw[0].y, cw[1].x, cw[1].y);
-                        *reinterpret_cast<uint4 *>(e + row * 32 + 16 * (1 - x)) = make_uint4(cw[2].x, cw[2].y, cw[3].x, cw[3].y);
-                    }
-                    fence_proxy_async_smem();
+                if (!mbar_wait_warp(&empty[s], ph ^ 1, abort_flag)) {
+                    cp_async_wait<0>();
+                    goto done;
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[s]);
+                if (kt < k1) q8_copy_codes(smem + s * C::STAGE_BYTES + C::A_BYTES + 2 * C::B_PANEL, p.meta, p.M, p.K, m0, kt, lane);
+                cp_async_commit();
+                if (++issued > LAG) {
+                    cp_async_wait<LAG>();
+                    publish();
+                }
                 if (++s == NS) { s = 0; ph ^= 1; }
             }
         }
+        cp_async_wait<0>();
+        while (published < issued) publish();
     }
 done:
     __syncwarp();

@@ -15,8 +15,9 @@
 // bf16 MMAs then accumulate onto that, and the result is read and rounded
 // once.
 //
-// Roles (320 threads): warp 0 operand producer, warp 1 TMEM owner and (pair
-// leader) MMA issuer, warps 2..5 epilogue of block 0, warps 6..9 of block 1.
+// Roles (384 threads): warp 0 operand producer, warp 1 TMEM owner and (pair
+// leader) MMA issuer, warps 2..5 epilogue of block 0, warps 6..9 of block 1,
+// warps 10 and 11 the codes of block 0 and 1 where TMA cannot address them.
 // An epilogue warp takes its 32 channels x 224 tokens into registers as bf16
 // pairs, releases the accumulator, and only then transposes and stores, beside
 // the next tile's MMAs.  Row blocks past the end start at M - 128 instead and
@@ -48,11 +49,13 @@ struct Q8WideCfg {
 struct Q8WideParams {
     int M, T, K, r;
     int m_tiles, n_tiles, raster_g, num_work;
+    int meta_tma;          // 1: codes by TMA, 0: by warps 10 and 11
+    const uint16_t *meta;  // [M x K/16]
     const float *xscale, *wscale;
     uint16_t *Y;
 };
 
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(384, 1)
     q8_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmR,
                    const __grid_constant__ CUtensorMap tmXL, const __grid_constant__ Q8WideParams p) {
@@ -77,7 +80,7 @@ __global__ void __launch_bounds__(320, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], p.meta_tma ? 1 : 1 + 2 * NBLK);
             mbar_init(&empty[s], 1);
         }
         mbar_init(acc_full, 1);
@@ -92,7 +95,7 @@ __global__ void __launch_bounds__(320, 1)
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
-        tma_prefetch_desc(&tmE);
+        if (p.meta_tma) tma_prefetch_desc(&tmE);
         if (p.r > 0) {
             tma_prefetch_desc(&tmR);
             tma_prefetch_desc(&tmXL);
@@ -129,11 +132,11 @@ __global__ void __launch_bounds__(320, 1)
                     uint8_t *e = b + 2 * C::B_PANEL;
                     const uint32_t lead_full = cluster_addr(&full[s], 0);
                     if (kt < kts) {
-                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (C::STAGE_BYTES - (p.meta_tma ? 0 : NBLK * C::E_BYTES)));
 #pragma unroll
                         for (int blk = 0; blk < NBLK; ++blk) {
                             tma_load_2d_pair(a + blk * C::A_BYTES, &tmA, lead_full, kt * 128, m0[blk]);
-                            tma_load_2d_pair(e + blk * C::E_BYTES, &tmE, lead_full, kt * 16, m0[blk]);
+                            if (p.meta_tma) tma_load_2d_pair(e + blk * C::E_BYTES, &tmE, lead_full, kt * 16, m0[blk]);
                         }
                         tma_load_2d_pair(b, &tmB, lead_full, kt * 256, n0);
                         tma_load_2d_pair(b + C::B_PANEL, &tmB, lead_full, kt * 256 + 128, n0);
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(320, 1)
                 }
             }
         }
-    } else {
+    } else if (warp < 10) {
         // ------------------------------------------------------------ epilogue (both CTAs)
         const int q = warp & 3, blk = (warp - 2) >> 2;
         uint8_t *tile = staging + (warp - 2) * 2048;  // [32 tokens][32 channels] bf16
@@ -324,6 +327,43 @@ __global__ void __launch_bounds__(320, 1)
                 __syncwarp();  // every lane has read the tile before the next chunk overwrites it
             }
         }
+    } else if (!p.meta_tma) {
+        // ------------------------------------------------------------ code loaders (both CTAs), see q8_tile_kernel
+        const int blk = warp - 10;
+        constexpr int LAG = 1;
+        int s = 0, issued = 0, published = 0;
+        uint32_t ph = 0;
+        auto publish = [&]() {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (rank == 0) mbar_arrive(&full[published % NS]);
+                else mbar_arrive_cluster(cluster_addr(&full[published % NS], 0));
+            }
+            ++published;
+        };
+        for (int w = pair; w < p.num_work; w += num_pairs) {
+            int mt, nt;
+            grouped_tile(w, p.m_tiles, p.n_tiles, p.raster_g, mt, nt);
+            const int m0 = min(mt * C::TILE_M + 256 * blk + 128 * (int)rank, p.M - 128);
+            for (int kt = 0; kt < kts + adp_kts; ++kt) {
+                if (!mbar_wait_warp(&empty[s], ph ^ 1, abort_flag)) {
+                    cp_async_wait<0>();
+                    goto done;
+                }
+                if (kt < kts)
+                    q8_copy_codes(smem + s * C::STAGE_BYTES + NBLK * C::A_BYTES + 2 * C::B_PANEL + blk * C::E_BYTES, p.meta, p.M, p.K,
+                                  m0, kt, lane);
+                cp_async_commit();
+                if (++issued > LAG) {
+                    cp_async_wait<LAG>();
+                    publish();
+                }
+                if (++s == NS) { s = 0; ph ^= 1; }
+            }
+        }
+        cp_async_wait<0>();
+        while (published < issued) publish();
     }
 done:
     tc_fence_before();

@@ -1844,7 +1844,7 @@ Q8Plan pick_q8_plan(int64_t M, int64_t T, int64_t K, int64_t r, int sms) {
                 }
             }
         }
-        if (K % 128 == 0) {
+        {
             const int64_t tiles = (M + 511) / 512 * ((T + 223) / 224), pairs = sms / 2 > 0 ? sms / 2 : 1;
             const double t = 7.0 + (double)((tiles + pairs - 1) / pairs) * ((double)kts + 4.5) * 0.82;
             if (t < best_us) {
@@ -1941,10 +1941,12 @@ int q8_product(const int8_t *X, const float *xscale, const int8_t *W, const floa
         wp.n_tiles = (p.T + C::BN - 1) / C::BN;
         wp.raster_g = wide_raster_group(wp.m_tiles, d.sms);
         wp.num_work = wp.m_tiles * wp.n_tiles;
+        wp.meta_tma = p.meta_tma;
+        wp.meta = meta;
         wp.xscale = xscale;
         wp.wscale = wscale;
         wp.Y = Y;
-        return launch_pairs(slope::q8_wide_kernel, Q8_WIDE_SLOT, 320, C::SMEM_BYTES, wp.num_work, d.sms, st, a, b, e, r2, xl, wp);
+        return launch_pairs(slope::q8_wide_kernel, Q8_WIDE_SLOT, 384, C::SMEM_BYTES, wp.num_work, d.sms, st, a, b, e, r2, xl, wp);
     }
     switch (plan.bn) {
         case 16: return launch_q8_tile<16>(a, b, e, r2, xl, p, d.sms, st);

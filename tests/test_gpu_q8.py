@@ -258,7 +258,8 @@ PRODUCT = [
     (5, 64, 128, 8), (16, 256, 128, 0), (13, 4096, 192, 96), (17, 512, 320, 16), (32, 1024, 256, 256), (33, 384, 512, 40), (64, 2048, 640, 64),
     (65, 128, 192, 8), (128, 512, 128, 0), (200, 640, 1088, 24), (129, 9216, 256, 96), (1000, 768, 832, 64),
     # codes that TMA cannot load (K an odd multiple of 64)
-    (9, 192, 128, 8), (40, 832, 320, 72), (300, 4160, 192, 0), (8, 12352, 256, 16),
+    (9, 192, 128, 8), (40, 832, 320, 72), (300, 4160, 192, 0), (8, 12352, 256, 16), (5, 64, 256, 8), (20, 320, 3200, 200),
+    (100, 5824, 1088, 40), (2500, 64, 640, 8), (3300, 832, 1984, 200), (4000, 1472, 2752, 64), (2222, 5824, 960, 0),
     # long sums on few tiles: split over clusters of up to eight CTAs
     (16, 36864, 256, 96), (8, 131072, 128, 8), (48, 16384, 384, 8), (100, 8192, 128, 64), (12, 2048, 128, 0),
     # many tiles

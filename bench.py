@@ -13,7 +13,7 @@ Metric: dense-equivalent TFLOP/s of the layer's fwd+bwd (6*T*in*out per
 linear, plus the adapter's 6*T*r*(in+out)) over the device time of the step.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--config C5] [--impl ours|reference]
-    python bench.py --fwd-sweep --config C5 [--steps K] [--warmup W]
+    python bench.py --fwd-sweep [--int8] --config C5 [--steps K] [--warmup W]
     python bench.py --adamw-step --config C5 [--steps K] [--warmup W]
 
 The default workload is the largest one that fits one GPU (C5, OPT-66B-shaped
@@ -23,7 +23,10 @@ under torchrun it uses the ranks it is given.  Prints one JSON line (rank 0).
 `--impl reference` times the CPU oracle on a bounded sample of the same
 workload instead.  `--fwd-sweep` times inference
 (adapter_fwd + fwd over the layers) at 1, 16, 128 and 2048 tokens, one line
-per token count, against HBM bandwidth.
+per token count, against HBM bandwidth; with `--int8` the int8 path instead:
+the norm with the residual's addition and its int8 and bf16 outputs (or the
+quantiser, where no norm precedes), the adapter's down-projection, and the
+int8 product, per layer.
 """
 import argparse
 import json
@@ -97,6 +100,14 @@ def kernel_work(op, T, inn, out, r):
     if op == "bwd_dw_fused":  # masked dW (the kept half), dR and dL
         return (1.0 * T * inn * out + 2.0 * T * r * (inn + out),
                 2.0 * T * (inn + out + 2 * r) + 1.125 * inn * out + 4.0 * r * (inn + out))
+    # the int8 inference path (--fwd-sweep --int8)
+    if op == "rmsnorm_q8":  # X, residual in; residual, bf16 and int8 tokens out
+        return 0.0, 9.0 * T * inn + 4.0 * T + 2.0 * inn
+    if op == "quant_rows":
+        return 0.0, 3.0 * T * inn + 4.0 * T
+    if op == "fwd_q8":  # Xq, kept int8 weights + codes, scales, XL, R in; Y out
+        return (2.0 * T * inn * out + 2.0 * T * r * out,
+                1.0 * T * inn + 0.625 * inn * out + 4.0 * (T + out) + 2.0 * r * (T + out) + 2.0 * T * out)
     raise KeyError(op)
 
 
@@ -562,7 +573,9 @@ def run_fwd_sweep(args):
     the compressed weights (values + codes, 1.125 B per dense weight) and is
     bound by HBM; it is reported as algorithmic bytes over device time, as a
     fraction of the measured HBM bandwidth, next to its tensor-core rate.
-    One JSON line per token count."""
+    One JSON line per token count.  With --int8 the layer is rmsnorm_q8
+    (or quant_rows), adapter_fwd and fwd_q8 on weights quantised once
+    beforehand (0.625 B per dense weight)."""
     from structured_sparse_pretraining_b200 import ops
     device = torch.device("cuda", 0)
     torch.cuda.set_device(device)
@@ -580,6 +593,9 @@ def run_fwd_sweep(args):
         R = I.normal_bf16((w.rank, lay.out_features), w.std_r, dp.WEIGHT_SEED, li, "R", device) if w.rank else None
         L, R = I.pad_rank(L, R, r)
         layers.append(dict(inn=lay.in_features, out=lay.out_features, vals=vals, meta=meta, L=L, R=R))
+        if args.int8:
+            layers[-1].update(zip(("vals_q", "wscale"), ops.quant_rows(vals)))
+            layers[-1].update(vals=None, wn=torch.ones(lay.in_features, dtype=torch.bfloat16, device=device))
     ops.status_sync()
     flush = torch.empty(L2_FLUSH_BYTES // 4, dtype=torch.float32, device=device)
     for T in SWEEP_TOKENS:
@@ -588,6 +604,22 @@ def run_fwd_sweep(args):
             X = I.normal_bf16((T, l["inn"]), w.std_x, dp.token_seed(0), li, "X", device)
             XL = torch.empty(T, r, dtype=torch.bfloat16, device=device) if r else None
             Y = torch.empty(T, l["out"], dtype=torch.bfloat16, device=device)
+            if args.int8:
+                # linears that widen (QKV, FFN up) take the normalised residual stream; the others take
+                # tokens that no norm produced (attention's output, the FFN's middle)
+                b = dict(Q=torch.empty(T, l["inn"], dtype=torch.int8, device=device),
+                         qscale=torch.empty(T, dtype=torch.float32, device=device), Y=X)
+                if l["out"] > l["inn"]:
+                    b.update(res=torch.zeros_like(X), H=torch.empty_like(X), Y=torch.empty_like(X))
+                    calls.append((("rmsnorm_q8", l["inn"], l["out"]), lambda X=X, l=l, b=b: ops.rmsnorm_q8(X, l["wn"], 1e-5, **b)))
+                else:
+                    calls.append((("quant_rows", l["inn"], l["out"]), lambda X=X, b=b: ops.quant_rows(X, b["Q"], b["qscale"])))
+                if r:
+                    calls.append((("adapter_fwd", l["inn"], l["out"]), lambda l=l, b=b, XL=XL: ops.adapter_fwd(b["Y"], l["L"], XL)))
+                calls.append((("fwd_q8", l["inn"], l["out"]),
+                              lambda l=l, b=b, XL=XL, Y=Y: ops.fwd_q8(b["Q"], b["qscale"], l["vals_q"], l["wscale"], l["meta"],
+                                                                      XL, l["R"], l["out"], Y)))
+                continue
             # the public fused call: one launch where the shape allows, else adapter_fwd + fwd
             calls.append((("fwd_fused", l["inn"], l["out"]),
                           (lambda X=X, l=l, XL=XL, Y=Y: ops.fwd_fused(X, l["vals"], l["meta"], l["L"], l["R"], l["out"],
@@ -648,13 +680,17 @@ def run_fwd_sweep(args):
                            kernel=kernel_of(name, T, inn, out, r, sms),
                            launches=1 if fused_one else 2,
                            token_tile=224 if fused_one else bn, k_splits=1 if fused_one else sp)
+            if name == "fwd_q8":
+                rows, bn, sp = ops.q8_plan(out, T, inn, r, sms)
+                ent.update(tflops=round(fl / (avg * 1e-3) / 1e12, 2), tile_rows=rows, token_tile=bn, k_splits=sp)
             kernels[f"{name}[{inn}x{out}]"] = ent
         gbs = tot_bytes / (ms * 1e-3) / 1e9
         tflops = tot_flops / (ms * 1e-3) / 1e12
-        line = {"metric": "SLoPe inference fwd sweep: algorithmic HBM GB/s and % of HBM (adapter_fwd + fwd, "
-                          "all layers)",
+        what = "rmsnorm_q8 / quant_rows + adapter_fwd + fwd_q8" if args.int8 else "adapter_fwd + fwd"
+        line = {"metric": f"SLoPe inference fwd sweep: algorithmic HBM GB/s and % of HBM ({what}, all layers)",
                 "value": round(gbs, 1), "unit": "GB/s", "tokens": T, "n_gpus": 1, "steps": args.steps,
-                "warmup": args.warmup, "ms_per_step": round(ms, 5), "higher_is_better": True, "dtype": "bf16",
+                "warmup": args.warmup, "ms_per_step": round(ms, 5), "higher_is_better": True,
+                "dtype": "int8" if args.int8 else "bf16",
                 "data": "synthetic", "config": {"workload": w.name, "tokens": T, "adapter_rank": w.rank,
                                                 "layers": [f"{l['inn']}->{l['out']}" for l in layers],
                                                 "l2": "flushed between timed steps (256 MiB write, untimed)"},
@@ -915,6 +951,7 @@ def main():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--fwd-sweep", action="store_true",
                     help="inference sweep (fwd only) over 1, 16, 128, 2048 tokens; one line per token count")
+    ap.add_argument("--int8", action="store_true", help="with --fwd-sweep: the int8 path (norm, adapter, int8 product)")
     ap.add_argument("--adamw-step", action="store_true",
                     help="the fused compressed AdamW step + second pruning over the layers, against HBM")
     ap.add_argument("--plumbing-check", action="store_true",

@@ -369,12 +369,24 @@ int slope_quant_rows(const uint16_t *A, int64_t rows, int64_t K, int8_t *Q, floa
  * adapter, both may be NULL); Y [T x out] bf16.  The int8 sums are exact in
  * 32-bit integers (so in is at most 131072, SLOPE_ERR_SHAPE), the adapter's
  * are fp32, and the two are joined and rounded once.  A NaN or infinite scale
- * reaches every output of its token or channel.  One launch and no workspace:
- * calls may overlap on any streams; bit-reproducible.
+ * reaches every output of its token or channel.  No workspace: calls may
+ * overlap on any streams; bit-reproducible.  One launch (slope_q8_plan says of
+ * which form; with out = 64 one for every 65535 blocks of tokens).
  */
 int slope_fwd_q8(const int8_t *Xq, const float *xscale, const int8_t *vals_q, const float *wscale, const uint16_t *meta,
                  const uint16_t *XL, const uint16_t *R, int64_t T, int64_t in, int64_t out, int64_t r, uint16_t *Y,
                  void *stream);
+
+/*
+ * Form of slope_fwd_q8's launch (host only, no device call; no counterpart in
+ * the pages) for M = out output channels, T tokens, K = in and rank r on a
+ * device with `sms` SMs: rows = 0 (CUDA cores, a few tokens; bn = tokens per
+ * pass, splits = warps that share the sum over K), 128 (tensor-core tiles of
+ * 128 channels x bn tokens on clusters of `splits` CTAs that share it) or 512
+ * (512 x 224 tiles on SM pairs, no split).  Sizes as slope_fwd_q8; returns
+ * SLOPE_ERR_ARG for NULL outputs or bad sizes.
+ */
+int slope_q8_plan(int64_t M, int64_t T, int64_t K, int64_t r, int sms, int *rows, int *bn, int *splits);
 
 /*
  * Wait for `stream`, then read and clear the current device's error word:

@@ -37,6 +37,7 @@ SIGNATURES = {
     "slope_rmsnorm_bwd_ws": (_int, [_i64, _i64, ctypes.POINTER(_i64)]),
     "slope_quant_rows": (_int, [_p, _i64, _i64, _p, _p, _p]),
     "slope_fwd_q8": (_int, [_p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _p, _p]),
+    "slope_q8_plan": (_int, [_i64, _i64, _i64, _i64, _int, ctypes.POINTER(_int), ctypes.POINTER(_int), ctypes.POINTER(_int)]),
     "slope_selftest_wait_timeout": (_int, [_p]),
     "slope_sparse_plan": (_int, [_i64, _i64, _i64, _int, ctypes.POINTER(_int), ctypes.POINTER(_int)]),
     "slope_sparse_tile_rows": (_int, [_i64, _i64, _i64, _int, ctypes.POINTER(_int)]),

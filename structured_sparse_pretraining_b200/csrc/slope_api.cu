@@ -1980,4 +1980,14 @@ int slope_fwd_q8(const int8_t *Xq, const float *xscale, const int8_t *vals_q, co
     return q8_product(Xq, xscale, vals_q, wscale, meta, XL, R, T, in, out, r, Y, static_cast<cudaStream_t>(stream));
 }
 
+int slope_q8_plan(int64_t M, int64_t T, int64_t K, int64_t r, int sms, int *rows, int *bn, int *splits) {
+    if (!rows || !bn || !splits || M <= 0 || T <= 0 || K <= 0 || r < 0 || sms <= 0)
+        return fail(SLOPE_ERR_ARG, "slope_q8_plan: NULL output or a size that is not positive");
+    const Q8Plan p = pick_q8_plan(M, T, K, r, sms);
+    *rows = p.wide ? 512 : p.bn == 0 ? 0 : 128;
+    *bn = p.bn == 0 ? p.tb : p.bn;
+    *splits = p.splits;
+    return SLOPE_OK;
+}
+
 }  // extern "C"

@@ -389,6 +389,14 @@ def fwd_q8(Xq, xscale, vals_q, wscale, meta, XL, R, out_features, Y=None):
     return Y
 
 
+def q8_plan(M, T, K, r=0, sms=148):
+    """(rows, token width, splits) of fwd_q8's launch for M output channels, T
+    tokens, K input features and rank r (rows 0: CUDA cores; host-only query)."""
+    rows, bn, splits = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_int(0)
+    _lib.call("slope_q8_plan", M, T, K, r, sms, ctypes.byref(rows), ctypes.byref(bn), ctypes.byref(splits))
+    return rows.value, bn.value, splits.value
+
+
 def sparse_plan(M, T, K, sms=148):
     """(BN, splits) the sparse products use for an M x K operand and T tokens
     on a device with `sms` SMs (host-only query, no GPU needed)."""

@@ -266,8 +266,19 @@ PRODUCT = [
     (24, 512, 40000, 8), (700, 1024, 5120, 96), (2100, 1536, 2048, 16), (4096, 512, 512, 8),
     # 512 x 224 pair tiles: ragged in channels (clamped blocks), tokens and the sum; every count of adapter k-tiles
     (5000, 128, 128, 0), (4100, 256, 192, 8), (2300, 640, 1088, 256), (1792, 1024, 2560, 96), (3001, 1408, 832, 136), (2048, 2048, 4096, 0),
-    (9000, 384, 704, 64),
+    (9000, 384, 704, 64), (8000, 2048, 4096, 0), (4501, 4096, 5120, 96), (6000, 832, 5184, 0),
+    # every width at every split
+    (500, 1024, 320, 64), (300, 2048, 192, 64), (151, 4096, 192, 64), (501, 1024, 640, 64), (500, 2048, 320, 64), (299, 4096, 192, 64),
+    (1000, 1536, 640, 64), (503, 2048, 640, 64), (500, 4096, 320, 64),
 ]
+
+
+def test_the_cases_cover_every_form():
+    forms = {ops.q8_plan(M, T, K, r) for T, K, M, r in PRODUCT}
+    assert {f[:2] for f in forms} >= {(0, 1), (0, 2), (0, 4), (128, 16), (128, 32), (128, 64), (128, 128), (512, 224)}
+    assert {f[1:] for f in forms if f[0] == 128} == {(bn, s) for bn in (16, 32, 64, 128) for s in (1, 2, 4, 8)}
+    odd = {ops.q8_plan(M, T, K, r)[0] for T, K, M, r in PRODUCT if K % 128}
+    assert odd == {0, 128, 512}
 
 
 @pytest.mark.parametrize("T,K,M,r", PRODUCT)
@@ -414,6 +425,40 @@ def test_calls_on_several_streams_overlap_safely(T, K, M):
     ops.status_sync()
     for i, y in enumerate(got):
         assert torch.equal(y, want[i % 4])
+
+
+def test_captured_before_any_call():
+    """A process whose first calls are captured: set-up that a warm-up would have done works during capture."""
+    import subprocess
+    import sys
+    code = """
+import sys, torch
+sys.path.insert(0, 'tests')
+import q8_plain as P
+from structured_sparse_pretraining_b200 import ops
+T, K, M, r = 1500, 1280, 640, 16
+X, w = P.random_bf16((T, K), 1.0, 1), P.random_bf16((K,), 1.0, 2)
+A = P.random_bf16((M, K // 2), 0.02, 3)
+meta, XL, R = P.random_codes(M, K, 4), P.random_bf16((T, r), 1.0, 5), P.random_bf16((r, M), 0.1, 6)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    vq, ws = ops.quant_rows(A)
+    Q, s, Y, _, rstd = ops.rmsnorm_q8(X, w, 1e-5, with_y=True, with_rstd=True)
+    dH, dw = ops.rmsnorm_bwd(Y, X, w, rstd)
+    out = [ops.fwd_q8(Q[:t], s[:t], vq, ws, meta, XL[:t], R, M) for t in (1, 16, 200, T)]
+g.replay()
+torch.cuda.synchronize()
+for t, y in zip((1, 16, 200, T), out):
+    want, tol = P.product(Q[:t], s[:t], vq, ws, meta, XL[:t], R)
+    assert ((y.double() - want).abs() <= tol).all(), t
+ops.status_sync()
+print('captured first')
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and "captured first" in res.stdout, res.stdout[-2000:] + res.stderr[-2000:]
 
 
 def test_refusals_on_the_gpu():

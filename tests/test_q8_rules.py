@@ -94,6 +94,33 @@ def test_ops_refuse_cpu_tensors_and_wrong_types():
         ops.fwd_q8(X.to(torch.int8), w, X, w, X, None, None, 64)
 
 
+@pytest.mark.parametrize("M,T,K,r", [(64, 1, 64, 0), (64, 5000, 4096, 8), (128, 1, 64, 0), (192, 300, 131072, 256), (27648, 1, 9216, 96),
+                                     (9216, 16, 36864, 96), (36864, 8192, 9216, 96), (1024, 333, 4096, 0), (512, 16, 16384, 64)])
+def test_q8_plan_is_well_formed(M, T, K, r):
+    rows, bn, splits = ops.q8_plan(M, T, K, r)
+    kts = -(-K // 256)
+    if rows == 0:
+        assert (T <= 4 or M < 128) and bn in (1, 2, 4) and splits in (1, 2, 4, 8, 16)
+        assert bn * -(-K // 1024) * 1024 <= 200 * 1024, "the tokens' rows fit shared memory"
+    elif rows == 128:
+        assert M >= 128 and bn in (16, 32, 64, 128) and splits in (1, 2, 4, 8) and splits <= kts
+    else:
+        assert rows == 512 and M >= 128 and bn == 224 and splits == 1
+
+
+def test_q8_plan_of_the_largest_layers():
+    """Weight streaming on clusters at a decode step, the 512-row tiles at a prefill batch, CUDA cores for one token
+    of a small layer."""
+    assert ops.q8_plan(27648, 1, 9216, 96) == (128, 16, 2)
+    assert ops.q8_plan(9216, 16, 36864, 96) == (128, 16, 2)
+    assert ops.q8_plan(36864, 8192, 9216, 96) == (512, 224, 1)
+    assert ops.q8_plan(1024, 1, 1024, 64)[0] == 0
+    lib = _lib.load()
+    assert lib.slope_q8_plan(64, 1, 64, 0, 148, None, None, None) == 1
+    x = ctypes.c_int(0)
+    assert lib.slope_q8_plan(0, 1, 64, 0, 148, ctypes.byref(x), ctypes.byref(x), ctypes.byref(x)) == 1
+
+
 # ------------------------------------------------------------------ the plain forms themselves
 def test_plain_norm_gradient_is_the_forward_s_derivative():
     """norm_bwd against autograd of the forward formula and against central differences, in 64 bits."""

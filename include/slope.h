@@ -382,8 +382,8 @@ int slope_fwd_q8(const int8_t *Xq, const float *xscale, const int8_t *vals_q, co
  * the pages) for M = out output channels, T tokens, K = in and rank r on a
  * device with `sms` SMs: rows = 0 (CUDA cores, a few tokens; bn = tokens per
  * pass, splits = warps that share the sum over K), 128 (tensor-core tiles of
- * 128 channels x bn tokens on clusters of `splits` CTAs that share it) or 512
- * (512 x 224 tiles on SM pairs, no split).  Sizes as slope_fwd_q8; returns
+ * 128 channels x bn tokens on clusters of `splits` CTAs that share it), 256 or
+ * 512 (256 x 256 or 512 x 224 tiles on SM pairs, no split).  Sizes as slope_fwd_q8; returns
  * SLOPE_ERR_ARG for NULL outputs or bad sizes.
  */
 int slope_q8_plan(int64_t M, int64_t T, int64_t K, int64_t r, int sms, int *rows, int *bn, int *splits);

@@ -17,6 +17,7 @@
 #include "gemm.cuh"
 #include "gemm_pair.cuh"
 #include "gemm_q8.cuh"
+#include "gemm_q8_pair.cuh"
 #include "gemm_q8_wide.cuh"
 #include "gemm_wide.cuh"
 #include "prune.cuh"
@@ -1798,7 +1799,7 @@ int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, 
 
 namespace {
 // ------------------------------------------------------------------ int8 sparse product
-constexpr int Q8_WIDE_SLOT = 42, Q8_TILE_SLOT = 44;  // entries in launch_clusters' table (the tiles': 16)
+constexpr int Q8_WIDE_SLOT = 42, Q8_TILE_SLOT = 44, Q8_PAIR_SLOT = 60;  // entries in launch_clusters' table (the tiles': 16)
 constexpr int64_t Q8_MAX_K = 131072;  // 128 * 128 * K / 2 stays below 2^31
 
 struct Q8Plan {
@@ -1806,6 +1807,7 @@ struct Q8Plan {
     int splits;  // CTAs that share a tile's sum over K (or warps a group of channels, on CUDA cores)
     int tb;      // CUDA cores: tokens per pass
     bool wide;   // q8_wide_kernel: 512 x 224 pair tiles
+    // bn = 256: q8_pair_kernel, 256 x 256 pair tiles
 };
 
 // The product's form, by a model of each form's time in microseconds, from
@@ -1815,10 +1817,12 @@ struct Q8Plan {
 //    0.48 us each, 0.62 at bn = 128 (the ring then holds three stages), or its
 //    epilogue where that is longer, after 4.5 us and half a microsecond for
 //    each doubling of the split.
+//  * 256 x 256 pair tiles: 0.55 us a k-tile of a round, about 2 us for its
+//    drain, and 6 us (9216 -> 27648 at 256 tokens: 49 us against 75 with 128 x
+//    128 tiles and 65 with 512 x 224 ones; at 128 tokens 45 against 43 and 44).
 //  * 512 x 224 tiles: 0.82 us a k-tile of a round, about 3.7 us for its drain,
-//    and 7 us.  From about 400 tokens on they win wherever the layer has tiles
-//    for most SM pairs (5120 -> 20480 at 400 tokens: 43 us against 57; 1024 ->
-//    4096: 12.5 against 8.3).
+//    and 7 us (9216 -> 9216 at 8192 tokens: 296 us against 363 with 256 x 256
+//    tiles; at 2048 tokens, where they fill 2.4 rounds, 102 against 85).
 //  * CUDA cores, up to 4 tokens: 3 us, and 0.3 us for each megabyte of weights,
 //    a third as much again for each further token (1024 -> 4096 at one token
 //    4.3 us against the tiles' 5.3, 4096 -> 4096 5.7 against 8.3; 9216 -> 27648
@@ -1844,11 +1848,18 @@ Q8Plan pick_q8_plan(int64_t M, int64_t T, int64_t K, int64_t r, int sms) {
                 }
             }
         }
-        {
-            const int64_t tiles = (M + 511) / 512 * ((T + 223) / 224), pairs = sms / 2 > 0 ? sms / 2 : 1;
-            const double t = 7.0 + (double)((tiles + pairs - 1) / pairs) * ((double)kts + 4.5) * 0.82;
+        const int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
+        if (T > 64) {
+            const int64_t tiles = (M + 255) / 256 * ((T + 255) / 256);
+            const double t = 6.0 + (double)((tiles + pairs - 1) / pairs) * ((double)(kts + adp) + 3.5) * 0.55;
             if (t < best_us) {
                 best_us = t;
+                best = Q8Plan{256, 1, 0, false};
+            }
+            const int64_t wide_tiles = (M + 511) / 512 * ((T + 223) / 224);
+            const double t_wide = 7.0 + (double)((wide_tiles + pairs - 1) / pairs) * ((double)kts + 4.5) * 0.82;
+            if (t_wide < best_us) {
+                best_us = t_wide;
                 best = Q8Plan{224, 1, 0, true};
             }
         }
@@ -1915,14 +1926,15 @@ int q8_product(const int8_t *X, const float *xscale, const int8_t *W, const floa
     p.K = (int)K;
     p.r = (int)r;
     p.m_tiles = (int)((M + 127) / 128);
-    p.num_work = plan.wide ? 0 : (int)(p.m_tiles * ((T + plan.bn - 1) / plan.bn));
+    p.num_work = plan.wide || plan.bn == 256 ? 0 : (int)(p.m_tiles * ((T + plan.bn - 1) / plan.bn));
     p.splits = plan.splits;
     p.meta_tma = K % 128 == 0;
     p.meta = meta;
     p.xscale = xscale;
     p.wscale = wscale;
     p.Y = Y;
-    const int box_t = plan.wide ? slope::Q8WideCfg::BNH : plan.bn;  // token rows of a TMA box
+    // token rows of a TMA box
+    const int box_t = plan.wide ? slope::Q8WideCfg::BNH : plan.bn == 256 ? slope::Q8PairCfg::BNH : plan.bn;
     if (int rc = make_map_i8(a, W, M, K / 2, 128, 128)) return rc;
     if (int rc = make_map_i8(b, X, T, K, 128, box_t)) return rc;
     e = a;  // unused maps are copies of a valid one
@@ -1947,6 +1959,18 @@ int q8_product(const int8_t *X, const float *xscale, const int8_t *W, const floa
         wp.wscale = wscale;
         wp.Y = Y;
         return launch_pairs(slope::q8_wide_kernel, Q8_WIDE_SLOT, 384, C::SMEM_BYTES, wp.num_work, d.sms, st, a, b, e, r2, xl, wp);
+    }
+    if (plan.bn == 256) {
+        using C = slope::Q8PairCfg;
+        slope::Q8PairParams pp{p.M, p.T, p.K, p.r};
+        pp.n_tiles = (p.T + C::BN - 1) / C::BN;
+        pp.num_work = (p.M + 255) / 256 * pp.n_tiles;
+        pp.meta_tma = p.meta_tma;
+        pp.meta = meta;
+        pp.xscale = xscale;
+        pp.wscale = wscale;
+        pp.Y = Y;
+        return launch_pairs(slope::q8_pair_kernel, Q8_PAIR_SLOT, 352, C::SMEM_BYTES, pp.num_work, d.sms, st, a, b, e, r2, xl, pp);
     }
     switch (plan.bn) {
         case 16: return launch_q8_tile<16>(a, b, e, r2, xl, p, d.sms, st);
@@ -1984,7 +2008,7 @@ int slope_q8_plan(int64_t M, int64_t T, int64_t K, int64_t r, int sms, int *rows
     if (!rows || !bn || !splits || M <= 0 || T <= 0 || K <= 0 || r < 0 || sms <= 0)
         return fail(SLOPE_ERR_ARG, "slope_q8_plan: NULL output or a size that is not positive");
     const Q8Plan p = pick_q8_plan(M, T, K, r, sms);
-    *rows = p.wide ? 512 : p.bn == 0 ? 0 : 128;
+    *rows = p.wide ? 512 : p.bn == 0 ? 0 : p.bn == 256 ? 256 : 128;
     *bn = p.bn == 0 ? p.tb : p.bn;
     *splits = p.splits;
     return SLOPE_OK;

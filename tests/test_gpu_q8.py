@@ -266,7 +266,7 @@ PRODUCT = [
     (24, 512, 40000, 8), (700, 1024, 5120, 96), (2100, 1536, 2048, 16), (4096, 512, 512, 8),
     # 512 x 224 pair tiles: ragged in channels (clamped blocks), tokens and the sum; every count of adapter k-tiles
     (5000, 128, 128, 0), (4100, 256, 192, 8), (2300, 640, 1088, 256), (1792, 1024, 2560, 96), (3001, 1408, 832, 136), (2048, 2048, 4096, 0),
-    (9000, 384, 704, 64), (8000, 2048, 4096, 0), (4501, 4096, 5120, 96), (6000, 832, 5184, 0),
+    (9000, 384, 704, 64), (8000, 2048, 4096, 0), (4501, 4096, 5120, 96), (6000, 832, 5184, 0), (8100, 1984, 4160, 0), (350, 9216, 5184, 256), (256, 4160, 5120, 0),
     # every width at every split
     (500, 1024, 320, 64), (300, 2048, 192, 64), (151, 4096, 192, 64), (501, 1024, 640, 64), (500, 2048, 320, 64), (299, 4096, 192, 64),
     (1000, 1536, 640, 64), (503, 2048, 640, 64), (500, 4096, 320, 64),
@@ -275,10 +275,10 @@ PRODUCT = [
 
 def test_the_cases_cover_every_form():
     forms = {ops.q8_plan(M, T, K, r) for T, K, M, r in PRODUCT}
-    assert {f[:2] for f in forms} >= {(0, 1), (0, 2), (0, 4), (128, 16), (128, 32), (128, 64), (128, 128), (512, 224)}
+    assert {f[:2] for f in forms} >= {(0, 1), (0, 2), (0, 4), (128, 16), (128, 32), (128, 64), (128, 128), (256, 256), (512, 224)}
     assert {f[1:] for f in forms if f[0] == 128} == {(bn, s) for bn in (16, 32, 64, 128) for s in (1, 2, 4, 8)}
     odd = {ops.q8_plan(M, T, K, r)[0] for T, K, M, r in PRODUCT if K % 128}
-    assert odd == {0, 128, 512}
+    assert odd == {0, 128, 256, 512}
 
 
 @pytest.mark.parametrize("T,K,M,r", PRODUCT)

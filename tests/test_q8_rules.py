@@ -105,15 +105,16 @@ def test_q8_plan_is_well_formed(M, T, K, r):
     elif rows == 128:
         assert M >= 128 and bn in (16, 32, 64, 128) and splits in (1, 2, 4, 8) and splits <= kts
     else:
-        assert rows == 512 and M >= 128 and bn == 224 and splits == 1
+        assert (rows, bn) in ((256, 256), (512, 224)) and M >= 128 and splits == 1
 
 
 def test_q8_plan_of_the_largest_layers():
-    """Weight streaming on clusters at a decode step, the 512-row tiles at a prefill batch, CUDA cores for one token
+    """Weight streaming on clusters at a decode step, 256-row tiles at a few hundred tokens, 512-row ones at a prefill batch, CUDA cores for one token
     of a small layer."""
     assert ops.q8_plan(27648, 1, 9216, 96) == (128, 16, 2)
     assert ops.q8_plan(9216, 16, 36864, 96) == (128, 16, 2)
     assert ops.q8_plan(36864, 8192, 9216, 96) == (512, 224, 1)
+    assert ops.q8_plan(27648, 256, 9216, 96) == (256, 256, 1)
     assert ops.q8_plan(1024, 1, 1024, 64)[0] == 0
     lib = _lib.load()
     assert lib.slope_q8_plan(64, 1, 64, 0, 148, None, None, None) == 1

@@ -330,11 +330,12 @@ int slope_rmsnorm(const uint16_t *X, const uint16_t *res, const uint16_t *w, int
  * dY, H, dres, dH [T x D] bf16 (dres, the gradient that reaches h along the
  * residual stream, may be NULL); w [D] bf16; rstd [T], dw [D] fp32
  * (overwritten).  dH is the gradient of both X and res.  dH may be the buffer
- * of dY, H or dres.  ws: scratch of at least slope_rmsnorm_bwd_ws(T, D)
- * floats on the device, the caller's (so calls with their own ws may
- * overlap); less is SLOPE_ERR_SHAPE.  Its contents do not matter before and
- * mean nothing after.  Sizes as slope_rmsnorm.  Two launches; sums in a fixed
- * order, bit-reproducible.
+ * of dres; it must not overlap dY or H (SLOPE_ERR_ARG).  ws: scratch of at
+ * least slope_rmsnorm_bwd_ws(T, D) floats on the device, the caller's (so calls
+ * with their own ws may overlap); less is SLOPE_ERR_SHAPE, and none is needed
+ * (ws may be NULL) where that is 0.  Its contents do not matter before and
+ * mean nothing after.  Sizes as slope_rmsnorm.  One launch up to 1024 rows,
+ * else two; sums in a fixed order, bit-reproducible.
  */
 int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, const float *rstd, const uint16_t *dres,
                       int64_t T, int64_t D, uint16_t *dH, float *dw, float *ws, int64_t ws_floats, void *stream);

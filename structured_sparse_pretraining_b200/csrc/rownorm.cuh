@@ -458,134 +458,134 @@ struct RowBwdParams {
     const float *rstd;
     const uint16_t *dres;  // or null
     uint16_t *dH;
+    float *dw;             // [D], written by row_bwd_once_kernel
     float *part;           // [parts x D] partial sums of dw
     int64_t T;
     int D;
     int parts;             // CTAs of the launch
 };
 
-// A CTA takes rows blockIdx.x, + gridDim.x, ... (ROW_WARPS at a time where a
-// warp takes a row), keeps its sum of dY n in registers and writes it as one
-// row of `part`; dw_sum_kernel adds those rows in a fixed order.  HOLD: the
-// row stays in registers between the reduction and the gradient; without it
-// (rows too long beside the sums) it is read again, from L2.
-template <int NV, bool WARP, bool HOLD>
-__global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_bwd_kernel(const __grid_constant__ RowBwdParams p) {
+// Both gradients in one launch, without partial sums: dw needs no row's
+// statistics but rstd, which is given, so the launch's last CTAs compute it
+// from columns while the others compute dH from rows.  They read dY and H once
+// more (from L2, where few rows leave them), which costs less than a second
+// launch and its scratch up to about a thousand rows.
+//
+// Row CTAs: one row (a warp's each where they are short) held in registers.
+// Column CTAs: 32 columns, 16 bytes to a thread, the rows spread over the
+// CTA's groups of four threads and their sums added in a fixed order.
+constexpr int BWD_COLS = 32;
+template <int NV, bool WARP>
+__global__ void __launch_bounds__(WARP ? 64 * ROW_WARPS : 1024) row_bwd_once_kernel(const __grid_constant__ RowBwdParams p, int row_ctas) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int gsize = WARP ? 32 : blockDim.x, gi = WARP ? lane : threadIdx.x;
     const int nchunk = p.D >> 3;
     const int64_t total = p.T * p.D;
-    extern __shared__ float s_dw[];  // WARP: [ROW_WARPS][D]
-    __shared__ float s_sum[2][32];
+    __shared__ float s_sum[32][BWD_COLS];
     grid_dep_wait();
     grid_dep_launch();
-    float acc[NV][8];
+    if ((int)blockIdx.x >= row_ctas) {
+        const int c = ((int)blockIdx.x - row_ctas) * (BWD_COLS / 8) + (threadIdx.x & 3);  // this thread's 16 bytes of a row
+        const int groups = blockDim.x >> 2;
+        float acc[8];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+        for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+        if (c < nchunk) {
+#pragma unroll 4
+            for (int64_t t = threadIdx.x >> 2; t < p.T; t += groups) {
+                const int64_t at = t * p.D + 8 * c;
+                if (!in_bounds(at, 8, total) || !in_bounds(t, 1, p.T)) continue;
+                const uint4 hv = *reinterpret_cast<const uint4 *>(p.H + at), gv = *reinterpret_cast<const uint4 *>(p.dY + at);
+                const float rstd = p.rstd[t];
+                const uint32_t a[4] = {hv.x, hv.y, hv.z, hv.w}, b[4] = {gv.x, gv.y, gv.z, gv.w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
-    const float inv_d = 1.0f / (float)p.D;
-    int turn = 0;
-    for (int64_t row = WARP ? (int64_t)blockIdx.x * ROW_WARPS + warp : (int64_t)blockIdx.x; row < p.T;
-         row += WARP ? (int64_t)gridDim.x * ROW_WARPS : (int64_t)gridDim.x) {
-        const int64_t base = row * p.D;
-        uint4 h[HOLD ? NV : 1], g[HOLD ? NV : 1];
-        const float rstd = in_bounds(row, 1, p.T) ? p.rstd[row] : 0.0f;
-        auto load = [&](int i, uint4 &hv, uint4 &gv) {
-            const int c = gi + i * gsize;
-            hv = gv = make_uint4(0, 0, 0, 0);
-            if (c < nchunk && in_bounds(base + 8 * c, 8, total)) {
-                hv = *reinterpret_cast<const uint4 *>(p.H + base + 8 * c);
-                gv = *reinterpret_cast<const uint4 *>(p.dY + base + 8 * c);
-            }
-        };
-        if (HOLD) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) load(i, h[i], g[i]);
-        }
-        float dot = 0.0f;  // sum of g h
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = gi + i * gsize;
-            if (!HOLD) load(i, h[0], g[0]);
-            uint4 wv = make_uint4(0, 0, 0, 0);
-            if (c < nchunk && in_bounds(8 * c, 8, p.D)) wv = __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c));
-            const uint4 hv = h[HOLD ? i : 0], gv = g[HOLD ? i : 0];
-            const uint32_t a[4] = {hv.x, hv.y, hv.z, hv.w}, b[4] = {gv.x, gv.y, gv.z, gv.w}, d[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 hh = bf16x2_to_float2(a[k]), gg = bf16x2_to_float2(b[k]), ww = bf16x2_to_float2(d[k]);
-                dot = fmaf(gg.x * ww.x, hh.x * rstd, fmaf(gg.y * ww.y, hh.y * rstd, dot));
-                acc[i][2 * k] = fmaf(gg.x, hh.x * rstd, acc[i][2 * k]);
-                acc[i][2 * k + 1] = fmaf(gg.y, hh.y * rstd, acc[i][2 * k + 1]);
+                for (int k = 0; k < 4; ++k) {
+                    const float2 hh = bf16x2_to_float2(a[k]), gg = bf16x2_to_float2(b[k]);
+                    acc[2 * k] = fmaf(gg.x, hh.x * rstd, acc[2 * k]);
+                    acc[2 * k + 1] = fmaf(gg.y, hh.y * rstd, acc[2 * k + 1]);
+                }
             }
         }
-        dot = warp_sum(dot);
-        if (!WARP) {
-            if (lane == 0) s_sum[turn][warp] = dot;
-            __syncthreads();
-            dot = warp_sum(lane < (int)(blockDim.x >> 5) ? s_sum[turn][lane] : 0.0f);
-            turn ^= 1;  // the next row's sums go beside this row's, which other warps may still read
-        }
-        const float mean = dot * inv_d;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = gi + i * gsize;
-            if (!HOLD) load(i, h[0], g[0]);
-            if (c >= nchunk || !in_bounds(base + 8 * c, 8, total)) continue;
-            const uint4 wv = __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c));
-            uint4 ev = make_uint4(0, 0, 0, 0);
-            if (p.dres) ev = *reinterpret_cast<const uint4 *>(p.dres + base + 8 * c);
-            const uint4 hv = h[HOLD ? i : 0], gv = g[HOLD ? i : 0];
-            const uint32_t a[4] = {hv.x, hv.y, hv.z, hv.w}, b[4] = {gv.x, gv.y, gv.z, gv.w}, d[4] = {wv.x, wv.y, wv.z, wv.w};
-            const uint32_t e[4] = {ev.x, ev.y, ev.z, ev.w};
-            uint32_t o[4];
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 hh = bf16x2_to_float2(a[k]), gg = bf16x2_to_float2(b[k]), ww = bf16x2_to_float2(d[k]);
-                const float2 ee = bf16x2_to_float2(e[k]);
-                o[k] = pack_bf16x2(fmaf(rstd, fmaf(-hh.x * rstd, mean, gg.x * ww.x), ee.x),
-                                   fmaf(rstd, fmaf(-hh.y * rstd, mean, gg.y * ww.y), ee.y));
-            }
-            *reinterpret_cast<uint4 *>(p.dH + base + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-    }
-    // this CTA's partial row
-    const int64_t pbase = (int64_t)blockIdx.x * p.D, ptotal = (int64_t)p.parts * p.D;
-    if (WARP) {
+            for (int o = 4; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+        if (lane < 4) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = gi + i * gsize;
-            if (c < nchunk) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s_dw[warp * p.D + 8 * c + j] = acc[i][j];
-            }
+            for (int j = 0; j < 8; ++j) s_sum[warp][8 * lane + j] = acc[j];
         }
         __syncthreads();
-        for (int d = threadIdx.x; d < p.D; d += blockDim.x) {
-            float s = s_dw[d];
-#pragma unroll
-            for (int k = 1; k < ROW_WARPS; ++k) s += s_dw[k * p.D + d];
-            if (in_bounds(pbase + d, 1, ptotal)) p.part[pbase + d] = s;
+        const int d = ((int)blockIdx.x - row_ctas) * BWD_COLS + threadIdx.x;
+        if (threadIdx.x < BWD_COLS && d < p.D) {
+            float t = s_sum[0][threadIdx.x];
+            for (int k = 1; k < (int)(blockDim.x >> 5); ++k) t += s_sum[k][threadIdx.x];
+            if (in_bounds(d, 1, p.D)) p.dw[d] = t;
         }
-    } else {
+        return;
+    }
+    const int gsize = WARP ? 32 : blockDim.x, gi = WARP ? lane : threadIdx.x;
+    const int64_t row = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + warp : (int64_t)blockIdx.x;
+    if (WARP && row >= p.T) return;
+    const int64_t base = row * p.D;
+    const float rstd = in_bounds(row, 1, p.T) ? p.rstd[row] : 0.0f;
+    uint4 h[NV], g[NV];
+    float dot = 0.0f;  // sum of g n
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = gi + i * gsize;
-            if (c < nchunk && in_bounds(pbase + 8 * c, 8, ptotal)) {
-                float4 *dst = reinterpret_cast<float4 *>(p.part + pbase + 8 * c);
-                dst[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-                dst[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
-            }
+    for (int i = 0; i < NV; ++i) {
+        const int c = gi + i * gsize;
+        h[i] = g[i] = make_uint4(0, 0, 0, 0);
+        if (c < nchunk && in_bounds(base + 8 * c, 8, total)) {
+            h[i] = *reinterpret_cast<const uint4 *>(p.H + base + 8 * c);
+            g[i] = *reinterpret_cast<const uint4 *>(p.dY + base + 8 * c);
         }
+    }
+    auto weight = [&](int c) {
+        return c < nchunk && in_bounds(8 * c, 8, p.D) ? __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c)) : make_uint4(0, 0, 0, 0);
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const uint4 wv = weight(gi + i * gsize);
+        const uint32_t a[4] = {h[i].x, h[i].y, h[i].z, h[i].w}, b[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
+        const uint32_t d[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 hh = bf16x2_to_float2(a[k]), gg = bf16x2_to_float2(b[k]), ww = bf16x2_to_float2(d[k]);
+            dot = fmaf(gg.x * ww.x, hh.x * rstd, fmaf(gg.y * ww.y, hh.y * rstd, dot));
+        }
+    }
+    dot = warp_sum(dot);
+    if (!WARP) {
+        if (lane == 0) s_sum[0][warp] = dot;
+        __syncthreads();
+        dot = warp_sum(lane < (int)(blockDim.x >> 5) ? s_sum[0][lane] : 0.0f);
+    }
+    const float mean = dot / (float)p.D;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = gi + i * gsize;
+        if (c >= nchunk || !in_bounds(base + 8 * c, 8, total)) continue;
+        const uint4 wv = weight(c);
+        uint4 ev = make_uint4(0, 0, 0, 0);
+        if (p.dres) ev = *reinterpret_cast<const uint4 *>(p.dres + base + 8 * c);
+        const uint32_t a[4] = {h[i].x, h[i].y, h[i].z, h[i].w}, b[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
+        const uint32_t d[4] = {wv.x, wv.y, wv.z, wv.w}, e[4] = {ev.x, ev.y, ev.z, ev.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 hh = bf16x2_to_float2(a[k]), gg = bf16x2_to_float2(b[k]), ww = bf16x2_to_float2(d[k]);
+            const float2 ee = bf16x2_to_float2(e[k]);
+            o[k] = pack_bf16x2(fmaf(rstd, fmaf(-hh.x * rstd, mean, gg.x * ww.x), ee.x),
+                               fmaf(rstd, fmaf(-hh.y * rstd, mean, gg.y * ww.y), ee.y));
+        }
+        *reinterpret_cast<uint4 *>(p.dH + base + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
-// The same with the ring of row_stream_kernel: dY, H and dres of the next rows
-// arrive by bulk copy while this row is worked on; the second pass reads the
-// row again from shared memory, so registers hold only the sums of dY n and
-// the weight.  A warp refills a stage after its own second pass, a CTA after
-// the next row's barrier, when every thread is done with it.
+// Many rows: persistent groups with the rings of row_stream_kernel.  A group
+// keeps its sum of dY n in registers, a CTA writes its groups' sum as one row
+// of `part`, and dw_sum_kernel adds those rows in a fixed order.  The second
+// pass reads the row again from shared memory, so registers hold only the sums
+// and the weight.  A warp refills a stage after its own second pass, a CTA
+// after the next row's barrier, when every thread is done with it.
 template <int NV, bool WARP>
 __global__ void __launch_bounds__(stream_threads(NV, true, WARP), stream_bwd_ctas(NV, WARP))
     row_bwd_stream_kernel(const __grid_constant__ RowBwdParams p, int stages) {

@@ -1679,20 +1679,31 @@ int row_launch(const slope::RowParams &p, int sms, cudaStream_t st, const char *
     return launch_pdl(slope::row_kernel<4, false, NORM>, grid, block, 0, st, what, p);
 }
 
-// The gradient kernel's form, and its CTAs: the rows of its partial sums of dw.
-// It does not know the device (the scratch query has none), so 148 SMs are taken.
+// The gradients' form: one launch up to BWD_ONCE_ROWS rows (and for rows too
+// long for a ring), else rings and a second launch for dw, with `parts` rows of
+// partial sums (the rings' CTAs; the scratch query has no device, so 148 SMs
+// are taken).
+constexpr int64_t BWD_ONCE_ROWS = 1024;
 struct BwdPlan {
     RowPlan row;
-    StreamPlan stream;  // stages = 0: row_bwd_kernel
-    int64_t parts;
+    StreamPlan stream;
+    int64_t parts;  // 0: row_bwd_once_kernel
 };
 BwdPlan pick_bwd_plan(int64_t T, int64_t D) {
     BwdPlan b{pick_row_plan(D), pick_stream_plan(D, 6 * D, true, true), 0};
-    if (b.stream.nv > 4 || T < 2 * 148 * (int64_t)b.stream.per_sm * b.stream.rows) b.stream.stages = 0;
-    const int64_t per_sm = b.stream.stages ? b.stream.per_sm : 1536 / b.row.threads < 1 ? 1 : 1536 / b.row.threads > 4 ? 4 : 1536 / b.row.threads;
-    const int64_t blocks = b.row.warp ? (T + slope::ROW_WARPS - 1) / slope::ROW_WARPS : T;
-    b.parts = blocks < 148 * per_sm ? blocks : 148 * per_sm;
+    if (T <= BWD_ONCE_ROWS || b.stream.nv > 4 || b.stream.stages == 0) return b;
+    const int64_t blocks = (T + b.stream.rows - 1) / b.stream.rows, most = 148 * (int64_t)b.stream.per_sm;
+    b.parts = blocks < most ? blocks : most;
     return b;
+}
+
+template <int NV, bool WARP>
+int row_bwd_once_launch(const slope::RowBwdParams &p, const RowPlan &r, cudaStream_t st, const char *what) {
+    const int threads = WARP ? 64 * slope::ROW_WARPS : r.threads < 256 ? 256 : r.threads;
+    const int64_t rows = WARP ? threads / 32 : 1;  // of a CTA
+    const int64_t row_ctas = (p.T + rows - 1) / rows, col_ctas = (p.D + slope::BWD_COLS - 1) / slope::BWD_COLS;
+    return launch_pdl(slope::row_bwd_once_kernel<NV, WARP>, dim3((unsigned)(row_ctas + col_ctas)), dim3((unsigned)threads), 0, st,
+                      what, p, (int)row_ctas);
 }
 
 template <int NV, bool WARP>
@@ -1757,39 +1768,43 @@ int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, 
     CHECK_PTR(rstd);
     CHECK_PTR(dH);
     CHECK_PTR(dw);
-    CHECK_PTR(ws);
     CHECK_OPT(dres);
     if (int rc = check_tokens(T)) return rc;
     if (int rc = check_width(D, NORM_MAX_D, "D")) return rc;
+    // some CTAs read dY and H for dw while others write dH
+    const uintptr_t n = (uintptr_t)T * (uintptr_t)D * 2, o = reinterpret_cast<uintptr_t>(dH);
+    const uintptr_t in[2] = {reinterpret_cast<uintptr_t>(dY), reinterpret_cast<uintptr_t>(H)};
+    for (uintptr_t i : in)
+        if (o < i + n && i < o + n) return fail(SLOPE_ERR_ARG, "rmsnorm_bwd: dH overlaps dY or H");
     const BwdPlan plan = pick_bwd_plan(T, D);
     const int64_t parts = plan.parts;
-    if (ws_floats < parts * D)
-        return fail(SLOPE_ERR_SHAPE, "rmsnorm_bwd: ws holds %lld floats, %lld are needed (slope_rmsnorm_bwd_ws)",
-                    (long long)ws_floats, (long long)(parts * D));
+    if (parts > 0) {
+        CHECK_PTR(ws);
+        if (ws_floats < parts * D)
+            return fail(SLOPE_ERR_SHAPE, "rmsnorm_bwd: ws holds %lld floats, %lld are needed (slope_rmsnorm_bwd_ws)",
+                        (long long)ws_floats, (long long)(parts * D));
+    }
     DevInfo d;
     if (int rc = device_info(d)) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    slope::RowBwdParams p{dY, H, w, rstd, dres, dH, ws, T, (int)D, (int)parts};
-    const RowPlan r = plan.row;
-    const dim3 grid((unsigned)parts), block((unsigned)r.threads);
+    slope::RowBwdParams p{dY, H, w, rstd, dres, dH, dw, ws, T, (int)D, (int)parts};
     const char *what = "rmsnorm_bwd launch";
-    const int smem = r.warp ? (int)(slope::ROW_WARPS * D * sizeof(float)) : 0;
-    int rc;
-    if (plan.stream.stages > 0)
-        rc = plan.stream.warp ? (plan.stream.nv == 1   ? row_bwd_stream_launch<1, true>(p, plan.stream, st, what)
-                                 : plan.stream.nv == 2 ? row_bwd_stream_launch<2, true>(p, plan.stream, st, what)
-                                                       : row_bwd_stream_launch<4, true>(p, plan.stream, st, what))
-             : plan.stream.nv == 1 ? row_bwd_stream_launch<1, false>(p, plan.stream, st, what)
-             : plan.stream.nv == 2 ? row_bwd_stream_launch<2, false>(p, plan.stream, st, what)
-             : plan.stream.nv == 3 ? row_bwd_stream_launch<3, false>(p, plan.stream, st, what)
-                                   : row_bwd_stream_launch<4, false>(p, plan.stream, st, what);
-    else if (r.warp)
-        rc = r.nv == 1   ? launch_pdl(slope::row_bwd_kernel<1, true, true>, grid, block, smem, st, what, p)
-             : r.nv == 2 ? launch_pdl(slope::row_bwd_kernel<2, true, true>, grid, block, smem, st, what, p)
-                         : launch_pdl(slope::row_bwd_kernel<4, true, true>, grid, block, smem, st, what, p);
-    else
-        rc = r.nv == 2 ? launch_pdl(slope::row_bwd_kernel<2, false, true>, grid, block, smem, st, what, p)
-                       : launch_pdl(slope::row_bwd_kernel<4, false, false>, grid, block, smem, st, what, p);
+    if (parts == 0) {
+        const RowPlan r = plan.row;
+        if (r.warp)
+            return r.nv == 1   ? row_bwd_once_launch<1, true>(p, r, st, what)
+                   : r.nv == 2 ? row_bwd_once_launch<2, true>(p, r, st, what)
+                               : row_bwd_once_launch<4, true>(p, r, st, what);
+        return r.nv == 2 ? row_bwd_once_launch<2, false>(p, r, st, what) : row_bwd_once_launch<4, false>(p, r, st, what);
+    }
+    const StreamPlan &sp = plan.stream;
+    const int rc = sp.warp ? (sp.nv == 1   ? row_bwd_stream_launch<1, true>(p, sp, st, what)
+                              : sp.nv == 2 ? row_bwd_stream_launch<2, true>(p, sp, st, what)
+                                           : row_bwd_stream_launch<4, true>(p, sp, st, what))
+                   : sp.nv == 1 ? row_bwd_stream_launch<1, false>(p, sp, st, what)
+                   : sp.nv == 2 ? row_bwd_stream_launch<2, false>(p, sp, st, what)
+                   : sp.nv == 3 ? row_bwd_stream_launch<3, false>(p, sp, st, what)
+                                : row_bwd_stream_launch<4, false>(p, sp, st, what);
     if (rc) return rc;
     return launch_pdl(slope::dw_sum_kernel, dim3((unsigned)((D + 31) / 32)), dim3(256), 0, st, "rmsnorm_bwd dw launch",
                       (const float *)ws, (int)parts, (int)D, dw);

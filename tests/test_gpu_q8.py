@@ -190,7 +190,8 @@ def test_rmsnorm_in_place(T, D):
 
 
 # ------------------------------------------------------------------ gradients of the norm
-@pytest.mark.parametrize("T,D", NORM_SHAPES + [(2500, 256), (1500, 2048)])
+@pytest.mark.parametrize("T,D", NORM_SHAPES + [(2500, 256), (1500, 2048), (1024, 264), (1025, 264), (1024, 5128), (1026, 12288), (1500, 12296),
+                                                 (777, 1000), (64, 1032), (300, 20000)])
 @pytest.mark.parametrize("dres", [False, True])
 def test_rmsnorm_bwd(T, D, dres):
     H, dY = P.random_bf16((T, D), 2.0, 11), P.random_bf16((T, D), 1e-2, 12)
@@ -201,8 +202,9 @@ def test_rmsnorm_bwd(T, D, dres):
     dh, dwr, mag, dwmag = P.norm_bwd(dY, H, w, rstd, e)
     rel = (depth(D) + 10) * P.F32  # the mean's sum, and the ten operations around it
     within(dH, dh, P.BF16 * (dh.abs() + rel * mag) + rel * mag, "dH")
-    # dw: rows per CTA in turn, up to four warps, the parts in eight chains, eight sums; and two products
-    chain = -(-T // 148) + 4 + 592 // 8 + 8 + 2
+    # dw: a thread's rows in turn, up to eight warps, the parts in eight chains, eight sums, and two products (in one
+    # launch: a thread's rows, three shuffles, up to 32 warps, two products)
+    chain = -(-T // 64) + 8 + 592 // 8 + 8 + 2
     within(dw, dwr, chain * P.F32 * dwmag, "dw")
     dH2, dw2 = ops.rmsnorm_bwd(dY, H, w, rstd, dres=e)
     assert torch.equal(dH, dH2) and torch.equal(dw, dw2)

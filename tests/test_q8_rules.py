@@ -43,12 +43,16 @@ def test_rmsnorm_bwd_refusals_and_scratch(buf):
     assert lib.slope_rmsnorm_bwd_ws(4, 64, None) == 1
     assert lib.slope_rmsnorm_bwd_ws(0, 64, ctypes.byref(n)) == 1
     assert lib.slope_rmsnorm_bwd_ws(4, 60, ctypes.byref(n)) == 2
-    for T, D in ((1, 8), (4, 64), (8192, 5120), (1 << 30, 32768)):
+    for T, D in ((1, 8), (4, 64), (1024, 5120), (8192, 32768)):
+        assert lib.slope_rmsnorm_bwd_ws(T, D, ctypes.byref(n)) == 0 and n.value == 0
+    for T, D in ((1025, 8), (8192, 5120), (1 << 30, 12288)):
         assert lib.slope_rmsnorm_bwd_ws(T, D, ctypes.byref(n)) == 0 and n.value >= D and n.value % D == 0
 
-    def call(dY=b, H=b, w=b, rstd=b, dres=None, T=4, D=64, dH=b, dw=b, ws=b, floats=1 << 20):
+    far = b + (1 << 32)  # never read: every call here is refused
+
+    def call(dY=b, H=b, w=b, rstd=b, dres=None, T=2000, D=64, dH=far, dw=b, ws=b, floats=1 << 20):
         return lib.slope_rmsnorm_bwd(dY, H, w, rstd, dres, T, D, dH, dw, ws, floats, None)
-    assert lib.slope_rmsnorm_bwd_ws(4, 64, ctypes.byref(n)) == 0
+    assert lib.slope_rmsnorm_bwd_ws(2000, 64, ctypes.byref(n)) == 0
     assert call(floats=n.value - 1) == 2
     for name in ("dY", "H", "w", "rstd", "dH", "dw", "ws"):
         assert call(**{name: None}) == 1
@@ -56,6 +60,11 @@ def test_rmsnorm_bwd_refusals_and_scratch(buf):
     assert call(dres=b + 8) == 3
     assert call(T=0) == 1
     assert call(D=20) == 2
+    for T in (4, 2000):  # dH over dY or H, wholly or by its last row
+        assert call(T=T, dH=b) == 1
+        assert call(T=T, H=far, dH=far) == 1
+        assert call(T=T, dH=b + 128 * (T - 1)) == 1
+        assert call(T=T, dY=far + 128 * (T - 1)) == 1
 
 
 @pytest.mark.parametrize("rows,K,code", [(0, 64, 1), (4, 0, 1), (4, 20, 2), (4, 65544, 2), ((1 << 30) + 1, 8, 2)])

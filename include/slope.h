@@ -370,9 +370,9 @@ int slope_quant_rows(const uint16_t *A, int64_t rows, int64_t K, int8_t *Q, floa
  * adapter, both may be NULL); Y [T x out] bf16.  The int8 sums are exact in
  * 32-bit integers (so in is at most 131072, SLOPE_ERR_SHAPE), the adapter's
  * are fp32, and the two are joined and rounded once.  A NaN or infinite scale
- * reaches every output of its token or channel.  No workspace: calls may
- * overlap on any streams; bit-reproducible.  One launch (slope_q8_plan says of
- * which form; with out = 64 one for every 65535 blocks of tokens).
+ * reaches every output of its token or channel.  One launch (slope_q8_plan
+ * says of which form) and no workspace: calls may overlap on any streams;
+ * bit-reproducible.
  */
 int slope_fwd_q8(const int8_t *Xq, const float *xscale, const int8_t *vals_q, const float *wscale, const uint16_t *meta,
                  const uint16_t *XL, const uint16_t *R, int64_t T, int64_t in, int64_t out, int64_t r, uint16_t *Y,

@@ -13,8 +13,8 @@
 // neither scale could do inside one accumulator.
 //
 // Roles (224 threads): warp 0 operand producer, warp 1 TMEM owner and MMA
-// issuer, warps 2..5 epilogue, warp 6 loads the codes where TMA cannot (rows
-// of K/8 bytes that are not a multiple of 16).
+// issuer, warps 2..5 epilogue, warp 6 loads the codes where TMA cannot
+// (q8_copy_codes).
 //
 // Persistent clusters of `splits` CTAs; the CTAs of a cluster share each
 // tile's sum over K, so that tiles can be handed out evenly whatever their
@@ -26,8 +26,9 @@
 // workspace and no atomics, and launches can overlap; integer sums do not
 // depend on the split.  The integer accumulator is double-buffered: the next
 // tile's MMAs run beside the epilogue.  Row tiles past the end start at
-// M - 128 instead, so that every code the MMA reads is a legal one; K ends
-// inside a k-tile after whole MMAs.
+// M - 128 instead, so that every code the MMA reads is a legal one (a layer of
+// 64 channels gets its codes from warp 6); K ends inside a k-tile after whole
+// MMAs.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -86,8 +87,9 @@ __device__ __forceinline__ void q8_store(const float (&v)[W], const Q8Params &p,
 
 // A 128 x 32-byte code tile (rows from m0, k-tile kt) into `e` in the 32-byte
 // swizzle, as 8-byte copies of one warp: for code rows of K/8 bytes that are
-// not a multiple of 16, which TMA cannot address.  Words past the row are
-// zeros that no MMA reads.
+// not a multiple of 16, which TMA cannot address, and for layers of 64
+// channels, whose missing rows take positions 0 and 1 (of kept values that TMA
+// reads as zero).  Words past the row are zeros that no MMA reads.
 __device__ __forceinline__ void q8_copy_codes(uint8_t *e, const uint16_t *meta, int M, int K, int m0, int kt, int lane) {
     const int words = K >> 4;  // a multiple of 4
 #pragma unroll
@@ -96,8 +98,13 @@ __device__ __forceinline__ void q8_copy_codes(uint8_t *e, const uint16_t *meta, 
         const int64_t at = (int64_t)(m0 + row) * words + kt * 16;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+            uint8_t *dst = e + row * 32 + 16 * ((c >> 1) ^ x) + 8 * (c & 1);
+            if (m0 + row >= M) {
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(0x44444444u, 0x44444444u);
+                continue;
+            }
             const bool in = kt * 16 + 4 * c < words && in_bounds(at + 4 * c, 4, (int64_t)M * words);
-            cp_async8(e + row * 32 + 16 * ((c >> 1) ^ x) + 8 * (c & 1), in ? meta + at + 4 * c : meta, in ? 8u : 0u);
+            cp_async8(dst, in ? meta + at + 4 * c : meta, in ? 8u : 0u);
         }
     }
 }
@@ -165,7 +172,7 @@ __global__ void __launch_bounds__(224, 1)
     if (warp == 6 && lane == 0 && p.meta_tma) {
         // the first stages' weights on their way to L2 beside the tail of the kernel before (3% at one to sixteen
         // tokens; nothing is read from them before the wait)
-        const int pm0 = min(cluster % p.m_tiles * 128, p.M - 128);
+        const int pm0 = max(0, min(cluster % p.m_tiles * 128, p.M - 128));
         for (int kt = k0; kt < min(k1, k0 + NS); ++kt) {
             tma_prefetch_2d(&tmA, kt * 128, pm0);
             tma_prefetch_2d(&tmE, kt * 16, pm0);
@@ -181,7 +188,7 @@ __global__ void __launch_bounds__(224, 1)
             uint32_t ph = 0;
             for (int w = cluster; w < p.num_work; w += num_clusters) {
                 const int mt = w % p.m_tiles, nt = w / p.m_tiles;
-                const int m0 = min(mt * 128, p.M - 128), n0 = nt * BN;  // M >= 128
+                const int m0 = max(0, min(mt * 128, p.M - 128)), n0 = nt * BN;
                 for (int kt = k0; kt < k1 + adp_kts; ++kt) {
                     if (!mbar_wait(&empty[s], ph ^ 1, abort_flag)) goto done;
                     uint8_t *a = smem + s * C::STAGE_BYTES;
@@ -261,11 +268,11 @@ __global__ void __launch_bounds__(224, 1)
         int it = 0;
         for (int w = cluster; w < p.num_work; w += num_clusters, ++it) {
             const int mt = w % p.m_tiles, nt = w / p.m_tiles;
-            const int m0 = min(mt * 128, p.M - 128), n0 = nt * BN;
+            const int m0 = max(0, min(mt * 128, p.M - 128)), n0 = nt * BN;
             const int cols = min(BN, (p.T - n0 + 1) & ~1);  // columns with tokens
             const int f = m0 + 32 * q + lane;               // this lane's channel
-            const bool row_ok = f >= mt * 128;              // rows the tile before owns are not stored again
-            const float ws = in_bounds(f, 1, p.M) ? __ldg(p.wscale + f) : 0.0f;
+            const bool row_ok = f >= mt * 128 && f < p.M;   // rows the tile before owns are not stored again
+            const float ws = f < p.M && in_bounds(f, 1, p.M) ? __ldg(p.wscale + f) : 0.0f;
             // every warp writes the scales that it reads itself (the four write the same values)
             float *xs = xs_buf + (it & 1) * BN;
             for (int c = lane; c < BN; c += 32) xs[c] = n0 + c < p.T && in_bounds(n0 + c, 1, p.T) ? __ldg(p.xscale + n0 + c) : 0.0f;
@@ -348,7 +355,7 @@ __global__ void __launch_bounds__(224, 1)
             ++published;
         };
         for (int w = cluster; w < p.num_work; w += num_clusters) {
-            const int m0 = min(w % p.m_tiles * 128, p.M - 128);
+            const int m0 = max(0, min(w % p.m_tiles * 128, p.M - 128));
             for (int kt = k0; kt < k1 + adp_kts; ++kt) {
                 if (!mbar_wait_warp(&empty[s], ph ^ 1, abort_flag)) {
                     cp_async_wait<0>();

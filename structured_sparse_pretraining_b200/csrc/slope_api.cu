@@ -1596,8 +1596,8 @@ RowPlan pick_row_plan(int64_t D) {
     return RowPlan{false, nv, (chunks + 32 * nv - 1) / (32 * nv) * 32};
 }
 
-// Rings of rows for many rows (row_stream_kernel and row_bwd_stream_kernel): a
-// warp's or a CTA's, nv 16-byte chunks per thread, CTAs per SM, and as many
+// Rings of rows for many rows (row_stream_kernel and row_bwd_stream_kernel), a
+// warp's or a CTA's: nv 16-byte chunks per thread, CTAs per SM, and as many
 // stages as shared memory holds; stages = 0 where not two rows of `row_bytes`
 // fit.
 struct StreamPlan {
@@ -1614,6 +1614,7 @@ StreamPlan pick_stream_plan(int64_t D, int64_t row_bytes, bool norm, bool backwa
     s.threads = s.warp ? 32 * slope::STREAM_WARPS : (chunks + 32 * s.nv - 1) / (32 * s.nv) * 32;
     s.rows = s.warp ? slope::STREAM_WARPS : 1;
     s.per_sm = backward ? slope::stream_bwd_ctas(s.nv, s.warp) : slope::stream_ctas(s.nv, norm, s.warp);
+    if (!s.warp && s.nv <= most_nv) s.per_sm = s.per_sm * 384 / s.threads;  // the registers of CTAs of 384 threads
     for (; s.per_sm >= 1; --s.per_sm) {
         const int64_t fit = (STREAM_SMEM / s.per_sm - 2048) / (row_bytes * s.rows);
         s.stages = (int)(fit > slope::STREAM_MAX_STAGES ? slope::STREAM_MAX_STAGES : fit);
@@ -1846,41 +1847,39 @@ Q8Plan pick_q8_plan(int64_t M, int64_t T, int64_t K, int64_t r, int sms) {
     const int64_t kts = (K + 255) / 256, adp = (r + 63) / 64;
     Q8Plan best{0, 1, 0, false};
     double best_us = 1e300;
-    if (M >= 128) {
-        const int bns[4] = {16, 32, 64, 128};
-        for (int bn : bns) {
-            if (bn > 16 && T <= bn / 2) break;  // half the columns would be empty
-            const int64_t tiles = (M + 127) / 128 * ((T + bn - 1) / bn);
-            double us = 4.5;
-            for (int s = 1; s <= 8 && s <= kts; s *= 2, us += 0.5) {
-                const int64_t clusters = sms / s > 0 ? sms / s : 1;
-                const double main_us = (double)((kts + s - 1) / s + adp) * (bn == 128 ? 0.62 : 0.48);
-                const double drain_us = 0.6 + 0.027 * bn / s;
-                const double t = us + (double)((tiles + clusters - 1) / clusters) * (main_us > drain_us ? main_us : drain_us);
-                if (t < best_us) {
-                    best_us = t;
-                    best = Q8Plan{bn, s, 0, false};
-                }
-            }
-        }
-        const int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
-        if (T > 64) {
-            const int64_t tiles = (M + 255) / 256 * ((T + 255) / 256);
-            const double t = 6.0 + (double)((tiles + pairs - 1) / pairs) * ((double)(kts + adp) + 3.5) * 0.55;
+    const int bns[4] = {16, 32, 64, 128};
+    for (int bn : bns) {
+        if (bn > 16 && T <= bn / 2) break;  // half the columns would be empty
+        const int64_t tiles = (M + 127) / 128 * ((T + bn - 1) / bn);
+        double us = 4.5;
+        for (int s = 1; s <= 8 && s <= kts; s *= 2, us += 0.5) {
+            const int64_t clusters = sms / s > 0 ? sms / s : 1;
+            const double main_us = (double)((kts + s - 1) / s + adp) * (bn == 128 ? 0.62 : 0.48);
+            const double drain_us = 0.6 + 0.027 * bn / s;
+            const double t = us + (double)((tiles + clusters - 1) / clusters) * (main_us > drain_us ? main_us : drain_us);
             if (t < best_us) {
                 best_us = t;
-                best = Q8Plan{256, 1, 0, false};
-            }
-            const int64_t wide_tiles = (M + 511) / 512 * ((T + 223) / 224);
-            const double t_wide = 7.0 + (double)((wide_tiles + pairs - 1) / pairs) * ((double)kts + 4.5) * 0.82;
-            if (t_wide < best_us) {
-                best_us = t_wide;
-                best = Q8Plan{224, 1, 0, true};
+                best = Q8Plan{bn, s, 0, false};
             }
         }
     }
+    const int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
+    if (T > 64 && M >= 128) {
+        const int64_t tiles = (M + 255) / 256 * ((T + 255) / 256);
+        const double t = 6.0 + (double)((tiles + pairs - 1) / pairs) * ((double)(kts + adp) + 3.5) * 0.55;
+        if (t < best_us) {
+            best_us = t;
+            best = Q8Plan{256, 1, 0, false};
+        }
+        const int64_t wide_tiles = (M + 511) / 512 * ((T + 223) / 224);
+        const double t_wide = 7.0 + (double)((wide_tiles + pairs - 1) / pairs) * ((double)kts + 4.5) * 0.82;
+        if (t_wide < best_us) {
+            best_us = t_wide;
+            best = Q8Plan{224, 1, 0, true};
+        }
+    }
     const double mb = (double)M * (double)K * 0.625e-6;
-    if (M < 128 || (T <= 4 && 3.0 + mb * 0.3 * (1.0 + 0.35 * (double)(T - 1)) < best_us)) {
+    if (T <= 4 && 3.0 + mb * 0.3 * (1.0 + 0.35 * (double)(T - 1)) < best_us) {
         const int64_t row = (K + 1023) / 1024 * 1024;
         int tb = T >= 3 ? 4 : (int)T;
         while (tb > 1 && tb * row > 200 * 1024) tb /= 2;
@@ -1921,18 +1920,10 @@ int q8_product(const int8_t *X, const float *xscale, const int8_t *W, const floa
     if (int rc = device_info(d)) return rc;
     const Q8Plan plan = pick_q8_plan(M, T, K, r, d.sms);
     if (plan.bn == 0) {
-        // the grid's second dimension counts blocks of tb tokens
-        for (int64_t t0 = 0; t0 < T;) {
-            const int64_t n = T - t0 < 65535 * (int64_t)plan.tb ? T - t0 : 65535 * (int64_t)plan.tb;
-            slope::SkinnyQ8Params p{X + t0 * K, xscale + t0, W, wscale, meta, XL ? XL + t0 * r : nullptr, R, Y + t0 * M,
-                                    (int)n, (int)K, (int)M, (int)r, plan.splits};
-            const int rc = plan.tb == 4   ? launch_skinny_q8<4>(p, d.sms, st)
-                           : plan.tb == 2 ? launch_skinny_q8<2>(p, d.sms, st)
-                                          : launch_skinny_q8<1>(p, d.sms, st);
-            if (rc) return rc;
-            t0 += n;
-        }
-        return SLOPE_OK;
+        slope::SkinnyQ8Params p{X, xscale, W, wscale, meta, XL, R, Y, (int)T, (int)K, (int)M, (int)r, plan.splits};
+        return plan.tb == 4   ? launch_skinny_q8<4>(p, d.sms, st)
+               : plan.tb == 2 ? launch_skinny_q8<2>(p, d.sms, st)
+                              : launch_skinny_q8<1>(p, d.sms, st);
     }
     CUtensorMap a, b, e, r2, xl;
     slope::Q8Params p{};
@@ -1943,7 +1934,7 @@ int q8_product(const int8_t *X, const float *xscale, const int8_t *W, const floa
     p.m_tiles = (int)((M + 127) / 128);
     p.num_work = plan.wide || plan.bn == 256 ? 0 : (int)(p.m_tiles * ((T + plan.bn - 1) / plan.bn));
     p.splits = plan.splits;
-    p.meta_tma = K % 128 == 0;
+    p.meta_tma = K % 128 == 0 && M >= 128;
     p.meta = meta;
     p.xscale = xscale;
     p.wscale = wscale;

@@ -254,8 +254,8 @@ PRODUCT = [
     # a few tokens: CUDA cores
     (1, 64, 64, 8), (1, 64, 128, 0), (2, 128, 64, 8), (3, 1024, 192, 24), (4, 1088, 448, 96), (1, 9216, 512, 96), (4, 2112, 9536, 16),
     (2, 36864, 128, 0), (4, 65536, 128, 8), (1, 131072, 64, 8), (1, 1024, 20032, 256),
-    # 64 channels at any token count
-    (5, 192, 64, 8), (37, 4096, 64, 200), (1000, 64, 64, 0),
+    # 64 channels: half a tile of them
+    (5, 192, 64, 8), (37, 4096, 64, 200), (1000, 64, 64, 0), (300, 17024, 64, 256), (16, 256, 64, 16), (3000, 1024, 64, 8), (6, 131072, 64, 24),
     # tensor cores: token tiles of 16, 32, 64, 128, ragged ends in tokens, channels and the sum
     (5, 64, 128, 8), (16, 256, 128, 0), (13, 4096, 192, 96), (17, 512, 320, 16), (32, 1024, 256, 256), (33, 384, 512, 40), (64, 2048, 640, 64),
     (65, 128, 192, 8), (128, 512, 128, 0), (200, 640, 1088, 24), (129, 9216, 256, 96), (1000, 768, 832, 64),
@@ -281,6 +281,7 @@ def test_the_cases_cover_every_form():
     assert {f[1:] for f in forms if f[0] == 128} == {(bn, s) for bn in (16, 32, 64, 128) for s in (1, 2, 4, 8)}
     odd = {ops.q8_plan(M, T, K, r)[0] for T, K, M, r in PRODUCT if K % 128}
     assert odd == {0, 128, 256, 512}
+    assert {ops.q8_plan(M, T, K, r)[0] for T, K, M, r in PRODUCT if M == 64} == {0, 128}
 
 
 @pytest.mark.parametrize("T,K,M,r", PRODUCT)

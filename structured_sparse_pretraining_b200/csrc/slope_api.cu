@@ -1609,7 +1609,7 @@ StreamPlan pick_stream_plan(int64_t D, int64_t row_bytes, bool norm, bool backwa
     const int chunks = (int)(D / 8);
     StreamPlan s{};
     s.warp = chunks <= 128;
-    const int most_nv = norm && !backward ? 6 : 4;  // with 384 threads; longer rows take 8
+    const int most_nv = norm ? 6 : 4;  // with 384 threads; longer rows take 8
     s.nv = s.warp ? (chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4) : chunks <= most_nv * 384 ? (chunks + 383) / 384 : 8;
     s.threads = s.warp ? 32 * slope::STREAM_WARPS : (chunks + 32 * s.nv - 1) / (32 * s.nv) * 32;
     s.rows = s.warp ? slope::STREAM_WARPS : 1;
@@ -1692,7 +1692,7 @@ struct BwdPlan {
 };
 BwdPlan pick_bwd_plan(int64_t T, int64_t D) {
     BwdPlan b{pick_row_plan(D), pick_stream_plan(D, 6 * D, true, true), 0};
-    if (T <= BWD_ONCE_ROWS || b.stream.nv > 4 || b.stream.stages == 0) return b;
+    if (T <= BWD_ONCE_ROWS || b.stream.nv > 6 || b.stream.stages == 0) return b;
     const int64_t blocks = (T + b.stream.rows - 1) / b.stream.rows, most = 148 * (int64_t)b.stream.per_sm;
     b.parts = blocks < most ? blocks : most;
     return b;
@@ -1805,7 +1805,9 @@ int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, 
                    : sp.nv == 1 ? row_bwd_stream_launch<1, false>(p, sp, st, what)
                    : sp.nv == 2 ? row_bwd_stream_launch<2, false>(p, sp, st, what)
                    : sp.nv == 3 ? row_bwd_stream_launch<3, false>(p, sp, st, what)
-                                : row_bwd_stream_launch<4, false>(p, sp, st, what);
+                   : sp.nv == 4 ? row_bwd_stream_launch<4, false>(p, sp, st, what)
+                   : sp.nv == 5 ? row_bwd_stream_launch<5, false>(p, sp, st, what)
+                                : row_bwd_stream_launch<6, false>(p, sp, st, what);
     if (rc) return rc;
     return launch_pdl(slope::dw_sum_kernel, dim3((unsigned)((D + 31) / 32)), dim3(256), 0, st, "rmsnorm_bwd dw launch",
                       (const float *)ws, (int)parts, (int)D, dw);

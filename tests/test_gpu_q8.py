@@ -190,7 +190,7 @@ def test_rmsnorm_in_place(T, D):
 
 
 # ------------------------------------------------------------------ gradients of the norm
-@pytest.mark.parametrize("T,D", NORM_SHAPES + [(2500, 256), (1500, 2048), (1024, 264), (1025, 264), (1024, 5128), (1026, 12288), (1500, 12296),
+@pytest.mark.parametrize("T,D", NORM_SHAPES + [(2500, 256), (1500, 2048), (1024, 264), (1025, 264), (1024, 5128), (1026, 12288), (1500, 12296), (1100, 18432), (1030, 16384), (1030, 18440),
                                                  (777, 1000), (64, 1032), (300, 20000)])
 @pytest.mark.parametrize("dres", [False, True])
 def test_rmsnorm_bwd(T, D, dres):

@@ -1609,12 +1609,13 @@ StreamPlan pick_stream_plan(int64_t D, int64_t row_bytes, bool norm, bool backwa
     const int chunks = (int)(D / 8);
     StreamPlan s{};
     s.warp = chunks <= 128;
-    const int most_nv = norm ? 6 : 4;  // with 384 threads; longer rows take 8
+    const int most_nv = 6;  // with 384 threads; longer rows take 8
     s.nv = s.warp ? (chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4) : chunks <= most_nv * 384 ? (chunks + 383) / 384 : 8;
     s.threads = s.warp ? 32 * slope::STREAM_WARPS : (chunks + 32 * s.nv - 1) / (32 * s.nv) * 32;
     s.rows = s.warp ? slope::STREAM_WARPS : 1;
     s.per_sm = backward ? slope::stream_bwd_ctas(s.nv, s.warp) : slope::stream_ctas(s.nv, norm, s.warp);
-    if (!s.warp && s.nv <= most_nv) s.per_sm = s.per_sm * 384 / s.threads;  // the registers of CTAs of 384 threads
+    // as many CTAs as the registers of those with the most threads hold
+    if (!s.warp) s.per_sm = s.per_sm * slope::stream_threads(s.nv, norm, false) / s.threads;
     for (; s.per_sm >= 1; --s.per_sm) {
         const int64_t fit = (STREAM_SMEM / s.per_sm - 2048) / (row_bytes * s.rows);
         s.stages = (int)(fit > slope::STREAM_MAX_STAGES ? slope::STREAM_MAX_STAGES : fit);
@@ -1661,10 +1662,8 @@ int row_launch(const slope::RowParams &p, int sms, cudaStream_t st, const char *
         if (s.nv == 2) return row_stream_launch<2, NORM, false>(p, s, sms, st, what);
         if (s.nv == 3) return row_stream_launch<3, NORM, false>(p, s, sms, st, what);
         if (s.nv == 4) return row_stream_launch<4, NORM, false>(p, s, sms, st, what);
-        if constexpr (NORM) {
-            if (s.nv == 5) return row_stream_launch<5, NORM, false>(p, s, sms, st, what);
-            if (s.nv == 6) return row_stream_launch<6, NORM, false>(p, s, sms, st, what);
-        }
+        if (s.nv == 5) return row_stream_launch<5, NORM, false>(p, s, sms, st, what);
+        if (s.nv == 6) return row_stream_launch<6, NORM, false>(p, s, sms, st, what);
         return row_stream_launch<8, NORM, false>(p, s, sms, st, what);
     }
     const int64_t blocks = r.warp ? (p.T + slope::ROW_WARPS - 1) / slope::ROW_WARPS : p.T;
@@ -1777,6 +1776,8 @@ int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, 
     const uintptr_t in[2] = {reinterpret_cast<uintptr_t>(dY), reinterpret_cast<uintptr_t>(H)};
     for (uintptr_t i : in)
         if (o < i + n && i < o + n) return fail(SLOPE_ERR_ARG, "rmsnorm_bwd: dH overlaps dY or H");
+    const uintptr_t e = reinterpret_cast<uintptr_t>(dres);
+    if (dres && e != o && o < e + n && e < o + n) return fail(SLOPE_ERR_ARG, "rmsnorm_bwd: dH overlaps a part of dres");
     const BwdPlan plan = pick_bwd_plan(T, D);
     const int64_t parts = plan.parts;
     if (parts > 0) {

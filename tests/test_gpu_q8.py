@@ -38,7 +38,8 @@ def depth(D):
 # ------------------------------------------------------------------ quantiser
 @pytest.mark.parametrize("rows,K", [(1, 8), (3, 16), (5, 64), (130, 264), (33, 512), (7, 520), (4, 1000), (9, 1024), (6, 1032),
                                     (3, 4608), (2, 16384), (2, 16392), (2, 36864), (1, 65536), (2000, 96),
-                                    (10000, 72), (9600, 512), (7201, 1000), (1000, 1032), (2049, 4608), (900, 8200), (700, 12288), (333, 36864), (300, 65536)])
+                                    (10000, 72), (9600, 512), (7201, 1000), (1000, 1032), (2049, 4608), (900, 8200), (700, 12288), (333, 36864), (300, 65536),
+                                    (800, 12296), (700, 16384), (600, 18432), (500, 18440)])
 def test_quant_rows(rows, K):
     A = P.random_bf16((rows, K), 0.02, 1)
     if rows > 2:
@@ -428,6 +429,41 @@ def test_calls_on_several_streams_overlap_safely(T, K, M):
     ops.status_sync()
     for i, y in enumerate(got):
         assert torch.equal(y, want[i % 4])
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values in every operand: the last rows are the right ones (the first ones' neighbours would be
+    overwritten by an offset that wrapped)."""
+    rows, K = 262200, 8208
+    tail = 3
+    A = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    A[-tail:] = P.random_bf16((tail, K), 1.0, 41)
+    Q, scale = ops.quant_rows(A)
+    q, top = P.quantise(A[-tail:].double())
+    assert torch.equal(Q[-tail:], q) and not Q[:5].any() and not scale[:-tail].any()
+    w = (1 + P.random_bf16((K,), 0.2, 42).float()).to(torch.bfloat16)
+    Q, _, Y, H, rstd = ops.rmsnorm_q8(A, w, EPS, res=A, with_y=True, with_rstd=True)
+    h, y, _, q, _ = P.norm(A[-tail:], w, EPS, A[-tail:])
+    assert torch.equal(H[-tail:], h) and torch.equal(Q[-tail:], q) and not Y[:5].any()
+    within(Y[-tail:], y, P.BF16 * 1.01 * y.abs(), "Y")
+    del Q, Y
+    dH, dw = ops.rmsnorm_bwd(A, H, w, rstd)
+    dh, dwr, mag, dwmag = P.norm_bwd(A[-tail:], h, w, rstd[-tail:])
+    within(dH[-tail:], dh, P.BF16 * dh.abs() + 2.0 ** -17 * mag, "dH")
+    within(dw, dwr, 8 * P.F32 * dwmag, "dw")  # every other row adds zeros
+    del A, H, dH
+    for T, K, M in ((1 << 15, 128, 65600), (1 << 15, 64, 65600)):  # Y has 2^31 values and some
+        Xq, xs, Wq, ws, meta, XL, R = product_case(8, K, M, 8)
+        X = torch.zeros(T, K, dtype=torch.int8, device="cuda")
+        X[-8:] = Xq
+        s = torch.zeros(T, device="cuda")
+        s[-8:] = xs
+        L = torch.zeros(T, 8, dtype=torch.bfloat16, device="cuda")
+        L[-8:] = XL
+        Y = ops.fwd_q8(X, s, Wq, ws, meta, L, R, M)
+        want, tol = P.product(Xq, xs, Wq, ws, meta, XL, R)
+        within(Y[-8:], want, tol, "Y")
+        assert not Y[:40].any()
 
 
 def test_captured_before_any_call():

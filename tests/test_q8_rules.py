@@ -65,6 +65,7 @@ def test_rmsnorm_bwd_refusals_and_scratch(buf):
         assert call(T=T, H=far, dH=far) == 1
         assert call(T=T, dH=b + 128 * (T - 1)) == 1
         assert call(T=T, dY=far + 128 * (T - 1)) == 1
+        assert call(T=T, dres=far + 128) == 1
 
 
 @pytest.mark.parametrize("rows,K,code", [(0, 64, 1), (4, 0, 1), (4, 20, 2), (4, 65544, 2), ((1 << 30) + 1, 8, 2)])

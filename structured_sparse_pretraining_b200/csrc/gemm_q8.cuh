@@ -48,14 +48,28 @@ struct Q8Params {
     uint16_t *Y;           // [T x M]
 };
 
+// The columns of a BN-wide tile that the CTAs of a cluster of S finish: CTA u
+// takes [first(u), first(u + 1)), in steps of 8, or of 2 where there are fewer
+// than S steps of 8.
+struct Q8Shares {
+    int step, steps, S;
+    __host__ __device__ Q8Shares(int bn, int splits) : step(bn >= 8 * splits ? 8 : 2), steps(bn / step), S(splits) {}
+    __host__ __device__ int first(int u) const { return steps * u / S * step; }
+    __host__ __device__ int most() const { return (steps + S - 1) / S * step; }
+};
+
+// Shared memory of a tile kernel for the partials of the other CTAs of its
+// cluster: enough for clusters of 1, 2, 3, 4 and 8 (five to seven CTAs were
+// measured slower than three or four on every layer tried).
+constexpr int q8_red_bytes(int bn) { return bn == 128 ? 57344 : bn == 64 ? 28672 : bn == 32 ? 16384 : 7168; }
+
 template <int BN>
 struct Q8Cfg {
     static constexpr int A_BYTES = 16384;     // 128 rows x 128 stored int8
     static constexpr int B_PANEL = BN * 128;  // BN rows x 128 dense int8, 128-byte swizzle
     static constexpr int E_BYTES = 4096;      // 128 rows x 32 bytes of codes, 32-byte swizzle
     static constexpr int STAGE_BYTES = A_BYTES + 2 * B_PANEL + E_BYTES;
-    static constexpr int MAX_SPLITS = 8;
-    static constexpr int RED_BYTES = BN * 128 * 4 / MAX_SPLITS * (MAX_SPLITS - 1);  // partials of the other CTAs
+    static constexpr int RED_BYTES = q8_red_bytes(BN);
     static constexpr int XS_BYTES = BN * 4;   // a tile's token scales
     static constexpr int BAR_BYTES = 256;
     static constexpr int NS_RAW = (232448 - 1024 - BAR_BYTES - 2 * XS_BYTES - RED_BYTES) / STAGE_BYTES;
@@ -264,7 +278,8 @@ __global__ void __launch_bounds__(224, 1)
     } else if (warp < 6) {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;
-        const int share = BN / S;
+        const Q8Shares shares(BN, S);
+        const int c_own = shares.first(rank), own = shares.first(rank + 1) - c_own;  // this CTA's columns
         int it = 0;
         for (int w = cluster; w < p.num_work; w += num_clusters, ++it) {
             const int mt = w % p.m_tiles, nt = w / p.m_tiles;
@@ -296,7 +311,7 @@ __global__ void __launch_bounds__(224, 1)
                 if (p.r > 0) tmem_ld_32x32_n(tadp + c, af);
                 tmem_ld_wait();
                 for (int u = 0; u < S - 1; ++u) {
-                    const uint32_t *src = red + (u * share + c - rank * share) * 128 + 32 * q + lane;
+                    const uint32_t *src = red + (u * own + c - c_own) * 128 + 32 * q + lane;
 #pragma unroll
                     for (int j = 0; j < W; ++j) ai[j] += src[j * 128];
                 }
@@ -311,28 +326,29 @@ __global__ void __launch_bounds__(224, 1)
             if (S > 1) {
                 if (it > 0 && !__all_sync(0xffffffffu, mbar_wait_cluster(red_empty, (it - 1) & 1, abort_flag))) break;
                 for (int i = 1; i < S; ++i) {
-                    const int u = (rank + i) % S;  // the CTA that finishes columns [u share, (u + 1) share)
-                    const uint32_t dst = cluster_addr(red + (rank - (rank > u)) * share * 128 + 32 * q + lane, u);
-                    const int c_end = min((u + 1) * share, cols);
-                    if (share % 8 == 0) {
+                    const int u = (rank + i) % S;  // the CTA that finishes columns [c0, c0 + n)
+                    const int c0 = shares.first(u), n = shares.first(u + 1) - c0;
+                    const uint32_t dst = cluster_addr(red + (rank - (rank > u)) * n * 128 + 32 * q + lane, u);
+                    const int c_end = min(c0 + n, cols);
+                    if (shares.step == 8) {
 #pragma unroll 1
-                        for (int c = u * share; c < c_end; c += 8) push(W8{}, c, dst + (c - u * share) * 512);
+                        for (int c = c0; c < c_end; c += 8) push(W8{}, c, dst + (c - c0) * 512);
                     } else {
 #pragma unroll 1
-                        for (int c = u * share; c < c_end; c += 2) push(W2{}, c, dst + (c - u * share) * 512);
+                        for (int c = c0; c < c_end; c += 2) push(W2{}, c, dst + (c - c0) * 512);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster_rel(cluster_addr(red_full, u));
                 }
                 if (!__all_sync(0xffffffffu, mbar_wait_cluster(red_full, it & 1, abort_flag))) break;
             }
-            const int c_end = min((rank + 1) * share, cols);
-            if (share % 8 == 0) {
+            const int c_end = min(c_own + own, cols);
+            if (shares.step == 8) {
 #pragma unroll 1
-                for (int c = rank * share; c < c_end; c += 8) finish(W8{}, c);
+                for (int c = c_own; c < c_end; c += 8) finish(W8{}, c);
             } else {
 #pragma unroll 1
-                for (int c = rank * share; c < c_end; c += 2) finish(W2{}, c);
+                for (int c = c_own; c < c_end; c += 2) finish(W2{}, c);
             }
             tc_fence_before();
             __syncwarp();

@@ -235,8 +235,8 @@ int launch_gemm(const CUtensorMap &a, const CUtensorMap &b, const slope::GemmPar
 template <typename Kern, typename... Args>
 int launch_clusters(Kern kern, int slot, int csize, int threads, int smem_bytes, int num_work, int sms,
                     cudaStream_t st, Args... args) {
-    static std::atomic<uint64_t> attr_set_mask[64];
-    static std::atomic<int> max_clusters[64][64];
+    static std::atomic<uint64_t> attr_set_mask[96];
+    static std::atomic<int> max_clusters[96][64];
     int dev = 0;
     cudaGetDevice(&dev);
     cudaLaunchConfig_t cfg = {};
@@ -1818,7 +1818,7 @@ int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, 
 
 namespace {
 // ------------------------------------------------------------------ int8 sparse product
-constexpr int Q8_WIDE_SLOT = 42, Q8_TILE_SLOT = 44, Q8_PAIR_SLOT = 60;  // entries in launch_clusters' table (the tiles': 16)
+constexpr int Q8_WIDE_SLOT = 42, Q8_PAIR_SLOT = 43, Q8_TILE_SLOT = 44;  // entries in launch_clusters' table (the tiles': 32)
 constexpr int64_t Q8_MAX_K = 131072;  // 128 * 128 * K / 2 stays below 2^31
 
 struct Q8Plan {
@@ -1835,7 +1835,9 @@ struct Q8Plan {
 //    clusters costs its k-tiles (a split's share of K, and the adapter's) at
 //    0.48 us each, 0.62 at bn = 128 (the ring then holds three stages), or its
 //    epilogue where that is longer, after 4.5 us and half a microsecond for
-//    each doubling of the split.
+//    each doubling of the split, and half a microsecond a round for each CTA
+//    that joins (16 tokens: 20480 -> 5120 34, 22, 19 and 24 us with one to four
+//    CTAs, 9216 -> 27648 37, 32, 42 and 54).
 //  * 256 x 256 pair tiles: 0.55 us a k-tile of a round, about 2 us for its
 //    drain, and 6 us (9216 -> 27648 at 256 tokens: 49 us against 75 with 128 x
 //    128 tiles and 65 with 512 x 224 ones; at 128 tokens 45 against 43 and 44).
@@ -1851,15 +1853,20 @@ Q8Plan pick_q8_plan(int64_t M, int64_t T, int64_t K, int64_t r, int sms) {
     Q8Plan best{0, 1, 0, false};
     double best_us = 1e300;
     const int bns[4] = {16, 32, 64, 128};
+    // clusters of 1 to 8 CTAs, one to an SM, that 148 SMs hold at once (by the occupancy query: they do not straddle
+    // the SMs' groups)
+    constexpr int max_resident[8] = {148, 74, 45, 33, 26, 22, 15, 15};
     for (int bn : bns) {
         if (bn > 16 && T <= bn / 2) break;  // half the columns would be empty
         const int64_t tiles = (M + 127) / 128 * ((T + bn - 1) / bn);
-        double us = 4.5;
-        for (int s = 1; s <= 8 && s <= kts; s *= 2, us += 0.5) {
-            const int64_t clusters = sms / s > 0 ? sms / s : 1;
+        for (int s = 1; s <= 8 && s <= kts; ++s) {
+            if (s > 4 && s < 8) continue;
+            const double us = 4.5 + 0.5 * std::log2((double)s);
+            const int64_t fit = (int64_t)sms * max_resident[s - 1] / 148, clusters = fit > 0 ? fit : 1;
             const double main_us = (double)((kts + s - 1) / s + adp) * (bn == 128 ? 0.62 : 0.48);
             const double drain_us = 0.6 + 0.027 * bn / s;
-            const double t = us + (double)((tiles + clusters - 1) / clusters) * (main_us > drain_us ? main_us : drain_us);
+            const double round_us = (main_us > drain_us ? main_us : drain_us) + 0.5 * (s - 1);
+            const double t = us + (double)((tiles + clusters - 1) / clusters) * round_us;
             if (t < best_us) {
                 best_us = t;
                 best = Q8Plan{bn, s, 0, false};
@@ -1911,8 +1918,10 @@ template <int BN>
 int launch_q8_tile(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &e, const CUtensorMap &r2,
                    const CUtensorMap &xl, const slope::Q8Params &p, int sms, cudaStream_t st) {
     // an entry of launch_clusters' table for each width and cluster size
-    const int slot = Q8_TILE_SLOT + 4 * (BN == 16 ? 0 : BN == 32 ? 1 : BN == 64 ? 2 : 3) +
-                     (p.splits == 1 ? 0 : p.splits == 2 ? 1 : p.splits == 4 ? 2 : 3);
+    const slope::Q8Shares shares(BN, p.splits);
+    if (p.splits > 8 || (p.splits - 1) * shares.most() * 512 > slope::Q8Cfg<BN>::RED_BYTES)
+        return fail(SLOPE_ERR_SHAPE, "int8 product: no room for the partials of a cluster of %d", p.splits);
+    const int slot = Q8_TILE_SLOT + 8 * (BN == 16 ? 0 : BN == 32 ? 1 : BN == 64 ? 2 : 3) + p.splits - 1;
     return launch_clusters(slope::q8_tile_kernel<BN>, slot, p.splits, 224, slope::Q8Cfg<BN>::SMEM_BYTES, p.num_work, sms, st, a,
                            b, e, r2, xl, p);
 }

@@ -273,13 +273,15 @@ PRODUCT = [
     # every width at every split
     (500, 1024, 320, 64), (300, 2048, 192, 64), (151, 4096, 192, 64), (501, 1024, 640, 64), (500, 2048, 320, 64), (299, 4096, 192, 64),
     (1000, 1536, 640, 64), (503, 2048, 640, 64), (500, 4096, 320, 64),
+    (250, 3328, 320, 64), (499, 3328, 320, 64), (250, 16384, 192, 64), (1000, 2048, 640, 64), (1000, 5120, 320, 64), (500, 16384, 192, 64),
+    (1000, 3328, 640, 64), (11, 3392, 192, 40), (13, 5120, 5120, 64),
 ]
 
 
 def test_the_cases_cover_every_form():
     forms = {ops.q8_plan(M, T, K, r) for T, K, M, r in PRODUCT}
     assert {f[:2] for f in forms} >= {(0, 1), (0, 2), (0, 4), (128, 16), (128, 32), (128, 64), (128, 128), (256, 256), (512, 224)}
-    assert {f[1:] for f in forms if f[0] == 128} == {(bn, s) for bn in (16, 32, 64, 128) for s in (1, 2, 4, 8)}
+    assert {f[1:] for f in forms if f[0] == 128} == {(bn, s) for bn in (16, 32, 64, 128) for s in (1, 2, 3, 4, 8)}
     odd = {ops.q8_plan(M, T, K, r)[0] for T, K, M, r in PRODUCT if K % 128}
     assert odd == {0, 128, 256, 512}
     assert {ops.q8_plan(M, T, K, r)[0] for T, K, M, r in PRODUCT if M == 64} == {0, 128}

@@ -113,7 +113,7 @@ def test_q8_plan_is_well_formed(M, T, K, r):
         assert T <= 4 and bn in (1, 2, 4) and splits in (1, 2, 4, 8, 16)
         assert bn * -(-K // 1024) * 1024 <= 200 * 1024, "the tokens' rows fit shared memory"
     elif rows == 128:
-        assert bn in (16, 32, 64, 128) and splits in (1, 2, 4, 8) and splits <= kts
+        assert bn in (16, 32, 64, 128) and splits in (1, 2, 3, 4, 8) and splits <= kts
     else:
         assert (rows, bn) in ((256, 256), (512, 224)) and M >= 128 and splits == 1
 

@@ -29,6 +29,11 @@
 // M - 128 instead, so that every code the MMA reads is a legal one (a layer of
 // 64 channels gets its codes from warp 6); K ends inside a k-tile after whole
 // MMAs.
+//
+// Measured, with adapters: one token on 9216 -> 27648 31 us (80% of the copy
+// rate), sixteen on 36864 -> 9216 39.5; sixteen on 20480 -> 5120 19 us with
+// clusters of three, 22 with two.  Splits of 1, 2, 3, 4 and 8 are offered:
+// resident clusters of 5, 6 and 7 fill 130, 132 and 105 SMs, those of 4 fill 132.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -70,14 +75,14 @@ struct Q8Cfg {
     static constexpr int E_BYTES = 4096;      // 128 rows x 32 bytes of codes, 32-byte swizzle
     static constexpr int STAGE_BYTES = A_BYTES + 2 * B_PANEL + E_BYTES;
     static constexpr int RED_BYTES = q8_red_bytes(BN);
-    static constexpr int XS_BYTES = BN * 4;   // a tile's token scales
+    static constexpr int XS_BYTES = 3 * BN * 4;  // token scales of three tiles
     static constexpr int BAR_BYTES = 256;
-    static constexpr int NS_RAW = (232448 - 1024 - BAR_BYTES - 2 * XS_BYTES - RED_BYTES) / STAGE_BYTES;
+    static constexpr int NS_RAW = (232448 - 1024 - BAR_BYTES - XS_BYTES - RED_BYTES) / STAGE_BYTES;
     static constexpr int NS = NS_RAW > 8 ? 8 : NS_RAW;
     static constexpr int ADP_COL = 2 * BN;    // fp32 adapter accumulator, after the two integer ones
     static constexpr int E_COL = 3 * BN;      // 8 columns per stage
     static constexpr int TMEM_COLS = BN == 128 ? 512 : BN >= 32 ? 256 : 128;
-    static constexpr int SMEM_BYTES = NS * STAGE_BYTES + RED_BYTES + 2 * XS_BYTES + BAR_BYTES + 1024;
+    static constexpr int SMEM_BYTES = NS * STAGE_BYTES + RED_BYTES + XS_BYTES + BAR_BYTES + 1024;
     static_assert(E_COL + 8 * NS <= TMEM_COLS, "TMEM budget");
     static_assert(BAR_BYTES >= 8 * (2 * NS + 6) + 8, "barrier area");
     static_assert(B_PANEL % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzle-atom alignment");
@@ -133,8 +138,8 @@ __global__ void __launch_bounds__(224, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint32_t *red = reinterpret_cast<uint32_t *>(smem + NS * C::STAGE_BYTES);  // [source][token of the share][128 channels]
-    float *xs_buf = reinterpret_cast<float *>(smem + NS * C::STAGE_BYTES + C::RED_BYTES);  // [2][BN]
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + NS * C::STAGE_BYTES + C::RED_BYTES + 2 * C::XS_BYTES);
+    float *xs_buf = reinterpret_cast<float *>(smem + NS * C::STAGE_BYTES + C::RED_BYTES);  // [3][BN]
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + NS * C::STAGE_BYTES + C::RED_BYTES + C::XS_BYTES);
     uint64_t *empty = full + NS;
     uint64_t *acc_full = empty + NS;     // [2]
     uint64_t *acc_empty = acc_full + 2;  // [2], 4 arrivals
@@ -288,8 +293,10 @@ __global__ void __launch_bounds__(224, 1)
             const int f = m0 + 32 * q + lane;               // this lane's channel
             const bool row_ok = f >= mt * 128 && f < p.M;   // rows the tile before owns are not stored again
             const float ws = f < p.M && in_bounds(f, 1, p.M) ? __ldg(p.wscale + f) : 0.0f;
-            // every warp writes the scales that it reads itself (the four write the same values)
-            float *xs = xs_buf + (it & 1) * BN;
+            // Every warp writes the scales that it reads itself (the four write the same values).  A warp may be here
+            // while another is still in the tile before the last: that one's sums must be released before the
+            // wait below ends, so three buffers keep them apart.
+            float *xs = xs_buf + it % 3 * BN;
             for (int c = lane; c < BN; c += 32) xs[c] = n0 + c < p.T && in_bounds(n0 + c, 1, p.T) ? __ldg(p.xscale + n0 + c) : 0.0f;
             __syncwarp();
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + (it & 1) * BN;

@@ -4,7 +4,7 @@
 //
 // Norm.  For a token row x (and the residual stream's row e, when there is
 // one):  h = bf16(x + e),  rstd = (mean h^2 + eps)^(-1/2),
-//        y = bf16(h rstd w),  and in int8  y ~ q s  with
+//        y = bf16((h w) rstd),  and in int8  y ~ q s  with
 //        p = h w,  q = round(127 p / max|p|),  s = rstd max|p| / 127.
 // The factor rstd cancels in q: p is the product of two bf16 numbers and so
 // exact in binary32, and q is decided exactly (quant_exact), so that q does
@@ -427,6 +427,7 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM, WARP), stream_ctas(NV
                 rstd = row_rstd(s2, inv_d, 0.0f) * 0x1p-80f;
             }
         }
+        if (WARP) __syncwarp();
         if (gi == 0) {
             // every thread of the group has read the stage
             fetch(row + stages * step, s);
@@ -469,7 +470,8 @@ struct RowBwdParams {
 // statistics but rstd, which is given, so the launch's last CTAs compute it
 // from columns while the others compute dH from rows.  They read dY and H once
 // more (from L2, where few rows leave them), which costs less than a second
-// launch and its scratch up to about a thousand rows.
+// launch and its scratch up to about a thousand rows: 4.6 against 6.1 us at
+// 777 x 1000, but 10.1 against 7.9 at 2048 x 1024.
 //
 // Row CTAs: one row (a warp's each where they are short) held in registers.
 // Column CTAs: 32 columns, 16 bytes to a thread, the rows spread over the
@@ -585,7 +587,8 @@ __global__ void __launch_bounds__(WARP ? 64 * ROW_WARPS : 1024) row_bwd_once_ker
 // of `part`, and dw_sum_kernel adds those rows in a fixed order.  The second
 // pass reads the row again from shared memory, so registers hold only the sums
 // and the weight.  A warp refills a stage after its own second pass, a CTA
-// after the next row's barrier, when every thread is done with it.
+// after the next row's barrier, when every thread is done with it.  8192 x 5120
+// with dres (8 bytes a value): 60 us, 85% of the copy rate.
 template <int NV, bool WARP>
 __global__ void __launch_bounds__(stream_threads(NV, true, WARP), stream_bwd_ctas(NV, WARP))
     row_bwd_stream_kernel(const __grid_constant__ RowBwdParams p, int stages) {

@@ -1888,7 +1888,7 @@ Q8Plan pick_q8_plan(int64_t M, int64_t T, int64_t K, int64_t r, int sms) {
             best = Q8Plan{224, 1, 0, true};
         }
     }
-    const double mb = (double)M * (double)K * 0.625e-6;
+    const double mb = (double)M * (double)((K + 1023) / 1024 * 1024) * 0.625e-6;  // lanes past a short row idle
     if (T <= 4 && 3.0 + mb * 0.3 * (1.0 + 0.35 * (double)(T - 1)) < best_us) {
         const int64_t row = (K + 1023) / 1024 * 1024;
         int tb = T >= 3 ? 4 : (int)T;

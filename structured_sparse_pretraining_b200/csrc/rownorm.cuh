@@ -56,14 +56,15 @@ __device__ __forceinline__ QuantRow quant_row(float pmax) {
     return q;
 }
 
-__device__ __forceinline__ uint2 pack_codes(const float (&m)[8]) {  // the low bytes
+__device__ __forceinline__ uint2 pack_codes(const float2 (&m)[4]) {  // the low bytes
     uint2 r;
-    r.x = __byte_perm(__byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0040),
-                      __byte_perm(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0040), 0x5410);
-    r.y = __byte_perm(__byte_perm(__float_as_uint(m[4]), __float_as_uint(m[5]), 0x0040),
-                      __byte_perm(__float_as_uint(m[6]), __float_as_uint(m[7]), 0x0040), 0x5410);
+    r.x = __byte_perm(__byte_perm(__float_as_uint(m[0].x), __float_as_uint(m[0].y), 0x0040),
+                      __byte_perm(__float_as_uint(m[1].x), __float_as_uint(m[1].y), 0x0040), 0x5410);
+    r.y = __byte_perm(__byte_perm(__float_as_uint(m[2].x), __float_as_uint(m[2].y), 0x0040),
+                      __byte_perm(__float_as_uint(m[3].x), __float_as_uint(m[3].y), 0x0040), 0x5410);
     return r;
 }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 constexpr float ROUND_MAGIC = 12582912.0f;  // 1.5 2^23: adding it rounds to an integer in the float's low bits
 
 // The largest of |a|, |b|, |c|, or NaN if one is.
@@ -84,45 +85,57 @@ __device__ __forceinline__ float quant_exact(float t, float k, float pm) {
     return (a > half || (a == half && odd)) ? k + copysignf(1.0f, d) : k;
 }
 
-// Eight products of two bf16 numbers to int8 codes.  The quotient p inv is off
-// by at most 2^-14 (four units of 2^-24 at 127, p f inv two roundings and inv
-// two units); one within 2^-13 of a border (2.4 in 10^4 of them) is decided
-// again by quant_exact.
-__device__ __forceinline__ uint2 quant8(float (&p)[8], const QuantRow &q) {
+// Eight products of two bf16 numbers to int8 codes.  The fused p inv is off by
+// at most 2^-14 (inv two units of 2^-23 of 127, the difference below half of
+// 2^-24); one within 2^-13 of a border (2.4 in 10^4 of them) is decided again
+// by quant_exact.
+__device__ __forceinline__ uint2 quant8(float2 (&p)[4], const QuantRow &q) {
     if (q.f != 1.0f) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] *= q.f;
+        for (int k = 0; k < 4; ++k) p[k] = __fmul2_rn(p[k], both(q.f));
     }
-    float m[8], worst = 0.0f;
+    float2 m[4];
+    float worst = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-        const float t0 = p[j] * q.inv, t1 = p[j + 1] * q.inv;
-        m[j] = t0 + ROUND_MAGIC;
-        m[j + 1] = t1 + ROUND_MAGIC;
-        worst = max_abs3(worst, t0 - (m[j] - ROUND_MAGIC), t1 - (m[j + 1] - ROUND_MAGIC));
+    for (int k = 0; k < 4; ++k) {
+        m[k] = __ffma2_rn(p[k], both(q.inv), both(ROUND_MAGIC));
+        const float2 neg = __ffma2_rn(m[k], both(-1.0f), both(ROUND_MAGIC));  // minus the rounded value
+        const float2 d = __ffma2_rn(p[k], both(q.inv), neg);
+        worst = max_abs3(worst, d.x, d.y);
     }
     if (worst > 0.5f - 0x1p-13f) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = quant_exact(p[j], m[j] - ROUND_MAGIC, q.pm) + ROUND_MAGIC;
+        for (int k = 0; k < 4; ++k) {
+            m[k].x = quant_exact(p[k].x, m[k].x - ROUND_MAGIC, q.pm) + ROUND_MAGIC;
+            m[k].y = quant_exact(p[k].y, m[k].y - ROUND_MAGIC, q.pm) + ROUND_MAGIC;
+        }
     }
     return pack_codes(m);
 }
 
 // Eight bf16 values to int8 codes.  With eight significant bits on either
 // side, a quotient t = 127 a / max|a| that is not a border k + 1/2 is further
-// than t / (254 255) = 1.5 10^-5 t from it, and the computed one is off by at
-// most 3 10^-7 t: rounding it to 18 bits after the leading one (steps of 2^-18,
-// at most 3.8 10^-6 of it) leaves every border exact and moves nothing else
+// than t / (254 255) = 1.5 10^-5 t from it, and a inv is off by at most
+// 3 10^-7 t: rounding it to 18 bits after the leading one (steps of 2^-18, at
+// most 3.8 10^-6 of it) leaves every border exact and moves nothing else
 // onto one or across it, and the rounding to an integer then breaks ties to even.
-__device__ __forceinline__ uint2 quant8_rows(float (&a)[8], const QuantRow &q) {
+// The rounding is Dekker's split: a inv - g with g about 33 a inv has the last
+// place of 32 a inv, which is 2^-18 of a inv's leading one, g is a multiple of
+// it, and so g plus the difference is exact.
+__device__ __forceinline__ uint2 quant8_rows(float2 (&a)[4], const QuantRow &q) {
     if (q.f != 1.0f) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] *= q.f;
+        for (int k = 0; k < 4; ++k) a[k] = __fmul2_rn(a[k], both(q.f));
     }
-    float m[8];
+    const float inv33 = q.inv * 33.0f;
+    float2 m[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        m[j] = __uint_as_float((__float_as_uint(a[j] * q.inv) + 16u) & ~31u) + ROUND_MAGIC;
+    for (int k = 0; k < 4; ++k) {
+        const float2 neg = __fmul2_rn(a[k], both(-inv33));               // -g
+        const float2 d = __ffma2_rn(a[k], both(q.inv), neg);             // a inv - g
+        const float2 t = __ffma2_rn(neg, both(-1.0f), d);                // a inv, split
+        m[k] = __fadd2_rn(t, both(ROUND_MAGIC));
+    }
     return pack_codes(m);
 }
 
@@ -153,25 +166,21 @@ __device__ __forceinline__ uint4 add_bf16x8(uint4 x, uint4 e) {
 }
 
 // Eight values' p = h w (the quantiser: a), and their share of a row's
-// statistics.  The norm: the sum of squares and the largest |p| as a float's
+// statistics.  The norm: the sums of the even and of the odd squares and the largest |p| as a float's
 // bits (NaN, larger than any number, if one is).  The quantiser: the largest
 // |a| of the even and of the odd values, as two bf16 patterns (an infinity's
 // or a NaN's is larger than any number's).
 template <bool NORM>
-__device__ __forceinline__ void row_stats(uint4 h, uint4 w, float (&v)[8], float &ss, uint32_t &mx) {
+__device__ __forceinline__ void row_stats(uint4 h, uint4 w, float2 (&v)[4], float2 &ss, uint32_t &mx) {
     const uint32_t a[4] = {h.x, h.y, h.z, h.w}, b[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const float2 u = bf16x2_to_float2(a[k]);
+        v[k] = bf16x2_to_float2(a[k]);
         if (NORM) {
-            const float2 g = bf16x2_to_float2(b[k]);
-            ss = fmaf(u.x, u.x, fmaf(u.y, u.y, ss));
-            v[2 * k] = u.x * g.x;
-            v[2 * k + 1] = u.y * g.y;
-            mx = __float_as_uint(max_abs3(__uint_as_float(mx), v[2 * k], v[2 * k + 1]));
+            ss = __ffma2_rn(v[k], v[k], ss);
+            v[k] = __fmul2_rn(v[k], bf16x2_to_float2(b[k]));
+            mx = __float_as_uint(max_abs3(__uint_as_float(mx), v[k].x, v[k].y));
         } else {
-            v[2 * k] = u.x;
-            v[2 * k + 1] = u.y;
             mx = __vmaxu2(mx, a[k] & 0x7FFF7FFFu);
         }
     }
@@ -195,12 +204,17 @@ __device__ __forceinline__ float scaled_squares(uint4 h, float s2) {
 
 // Eight outputs of a row from its p (h w, or the quantiser's values): y = p rstd and the codes of p.
 template <bool NORM>
-__device__ __forceinline__ void row_outputs(const RowParams &p, int64_t at, float (&v)[8], float rstd, const QuantRow &q,
+__device__ __forceinline__ void row_outputs(const RowParams &p, int64_t at, float2 (&v)[4], float rstd, const QuantRow &q,
                                             bool finite) {
-    if (NORM && p.Y)
-        *reinterpret_cast<uint4 *>(p.Y + at) =
-            make_uint4(pack_bf16x2(v[0] * rstd, v[1] * rstd), pack_bf16x2(v[2] * rstd, v[3] * rstd),
-                       pack_bf16x2(v[4] * rstd, v[5] * rstd), pack_bf16x2(v[6] * rstd, v[7] * rstd));
+    if (NORM && p.Y) {
+        uint32_t y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 t = __fmul2_rn(v[k], both(rstd));
+            y[k] = pack_bf16x2(t.x, t.y);
+        }
+        *reinterpret_cast<uint4 *>(p.Y + at) = make_uint4(y[0], y[1], y[2], y[3]);
+    }
     if (p.Q) *reinterpret_cast<uint2 *>(p.Q + at) = !finite ? make_uint2(0, 0) : NORM ? quant8(v, q) : quant8_rows(v, q);
 }
 
@@ -246,14 +260,14 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
         return NORM && c < nchunk && in_bounds(8 * c, 8, p.D) ? __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c))
                                                               : make_uint4(0, 0, 0, 0);
     };
-    float ss = 0.0f;
+    float2 ss2 = make_float2(0.0f, 0.0f);
     uint32_t mx = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        float v[8];
-        row_stats<NORM>(h[i], weight(gi + i * gsize), v, ss, mx);
+        float2 v[4];
+        row_stats<NORM>(h[i], weight(gi + i * gsize), v, ss2, mx);
     }
-    if (NORM) ss = warp_sum(ss);
+    float ss = NORM ? warp_sum(ss2.x + ss2.y) : 0.0f;
     mx = __reduce_max_sync(0xffffffffu, row_max_bits<NORM>(mx));
     if (!WARP) {
         if (lane == 0) {
@@ -296,7 +310,7 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
     for (int i = 0; i < NV; ++i) {
         const int c = gi + i * gsize;
         if (c < nchunk && in_bounds(base + 8 * c, 8, total)) {
-            float v[8], s_unused = 0.0f;
+            float2 v[4], s_unused = make_float2(0.0f, 0.0f);
             uint32_t m_unused = 0;
             row_stats<NORM>(h[i], weight(c), v, s_unused, m_unused);
             row_outputs<NORM>(p, base + 8 * c, v, rstd, q, finite);
@@ -304,65 +318,64 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
     }
 }
 
-// The same for many rows: persistent groups of threads (a warp up to 1024
-// values, a CTA above), each with a ring of `stages` rows (X, and res beside
-// it) that bulk copies keep filled, so that the loads of the next rows run
-// beside the arithmetic and the stores of this one.  The row and the
-// weight stay in registers between the statistics and the outputs.  With one row per
-// CTA and nothing ahead the norm of 8192 x 9216 (9 bytes a value) took 150 us,
-// 69% of the measured copy rate; here 114 us, 91%.  A CTA's rows take one barrier each: when it
-// falls every thread has read its chunks, and the row's stage is refilled.
-constexpr int STREAM_MAX_STAGES = 4;
-constexpr int STREAM_WARPS = 8;  // rows in work at once in a CTA of the warp form
-// Threads at most and CTAs per SM of a form with NV chunks a thread, by
-// measurement at 8192 rows or more.  The norm wants one CTA and a deep ring
-// where a row is long (9216 with residual and both outputs: 114 us with one
-// CTA per SM, 119 with two, 129 with three, which spill) and three below
-// (5120 in bf16: 59 us with three, 62 with two; 2048: 60 with three, 85 with
-// four); the quantiser three (27648 x 4608: 69 us with three, 80 with two, 76
-// with four).  Few chunks to many threads beat more to fewer (16384: 102 us
-// with six, 196 with eight, which spill).
+// The same for many long rows: CTAs that take several rows each, with a ring of
+// two rows (X, and res beside it) that bulk copies keep filled, so that the
+// load of the next row runs beside the arithmetic and the stores of this one.
+// The row and the weight stay in registers between the statistics and the
+// outputs.  A CTA's rows take one barrier each: when it falls every thread has
+// read its chunks, and the row's stage is refilled.
+//
+// 8192 x 9216 in a row of calls: with residual and both outputs (9 bytes a
+// value) one row per CTA and nothing ahead takes 139 us, one CTA of this per
+// SM with four stages 115, with two 109 (fewer reads in flight disturb the
+// writes less), and eight rounds of two CTAs per SM 104, 100% of the measured
+// copy rate: SMs differ in speed, and rounds let the fast ones take more.
+// Without the residual there is less to load per barrier, and the instructions
+// (22 a value in int8, of which the reductions and the barrier are about five)
+// bound it: 53 us in bf16, 67 in int8.  The quantiser takes 36 (96%).
+constexpr int STREAM_STAGES = 2;
+constexpr int STREAM_WARPS = 8;  // rows in work at once in a CTA of the gradients' warp form
+// Threads at most and CTAs per SM of a form with NV chunks a thread.  Norm:
+// 12288 with everything 143 us with two CTAs per SM, 151 with one; 16384 99
+// us (4096 rows) with one, 127 with two, which spill.  Quantiser: 9216 36 us
+// with three, 38 with two.  Few chunks to many threads beat more to fewer
+// (16384: 99 us with six, 196 with eight, which spill).
 constexpr int stream_threads(int nv, bool norm, bool warp) { return warp ? 32 * STREAM_WARPS : nv <= 6 ? 384 : norm ? 512 : 1024; }
-constexpr int stream_ctas(int nv, bool norm, bool warp) {
-    return warp ? (nv <= 2 ? 4 : 3) : norm ? (nv <= 2 ? 3 : 1) : nv <= 2 ? 3 : nv <= 4 ? 2 : 1;
-}
+constexpr int stream_ctas(int nv, bool norm) { return norm ? (nv <= 2 ? 3 : nv <= 4 ? 2 : 1) : nv <= 4 ? 3 : nv <= 6 ? 2 : 1; }
 constexpr int stream_bwd_ctas(int nv, bool warp) { return warp ? (nv <= 2 ? 3 : 2) : nv <= 2 ? 3 : nv == 3 ? 2 : 1; }
-template <int NV, bool NORM, bool WARP>
-__global__ void __launch_bounds__(stream_threads(NV, NORM, WARP), stream_ctas(NV, NORM, WARP))
-    row_stream_kernel(const __grid_constant__ RowParams p, int stages) {
+template <int NV, bool NORM>
+__global__ void __launch_bounds__(stream_threads(NV, NORM, false), stream_ctas(NV, NORM))
+    row_stream_kernel(const __grid_constant__ RowParams p) {
     extern __shared__ __align__(16) uint8_t row_smem[];
-    constexpr int GROUPS = WARP ? STREAM_WARPS : 1;
-    __shared__ __align__(8) uint64_t s_full[GROUPS][STREAM_MAX_STAGES];
+    __shared__ __align__(8) uint64_t full[STREAM_STAGES];
     __shared__ float s_sum[2][32];
     __shared__ uint32_t s_max[2][32];
     __shared__ int abort_flag;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    const int gi = WARP ? lane : threadIdx.x, gsize = WARP ? 32 : blockDim.x, group = WARP ? warp : 0;
+    const int gi = threadIdx.x, gsize = blockDim.x;
     const int nchunk = p.D >> 3;
     const int64_t total = p.T * p.D;
     const uint32_t row_bytes = (uint32_t)p.D * 2;
     const bool has_res = NORM && p.res;
     const uint32_t stage_bytes = has_res ? 2 * row_bytes : row_bytes;
-    uint8_t *ring = row_smem + (uint32_t)(group * stages) * stage_bytes;
-    uint64_t *full = s_full[group];
     if (threadIdx.x == 0) {
-        for (int i = 0; i < GROUPS * STREAM_MAX_STAGES; ++i) mbar_init(&s_full[0][0] + i, 1);
+        for (int i = 0; i < STREAM_STAGES; ++i) mbar_init(&full[i], 1);
         abort_flag = 0;
         fence_barrier_init();
     }
     __syncthreads();
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t row0 = (int64_t)blockIdx.x * GROUPS + group, step = (int64_t)gridDim.x * GROUPS;
-    auto fetch = [&](int64_t row, int s) {  // one thread of the group
+    const int64_t row0 = blockIdx.x, step = gridDim.x;
+    auto fetch = [&](int64_t row, int s) {  // one thread
         if (row >= p.T || !in_bounds(row * p.D, p.D, total)) return;
-        uint8_t *dst = ring + s * stage_bytes;
+        uint8_t *dst = row_smem + s * stage_bytes;
         mbar_arrive_expect_tx(&full[s], stage_bytes);
         bulk_load(dst, p.X + row * p.D, row_bytes, &full[s]);
         if (has_res) bulk_load(dst + row_bytes, p.res + row * p.D, row_bytes, &full[s]);
     };
     if (gi == 0)
-        for (int s = 0; s < stages; ++s) fetch(row0 + s * step, s);
+        for (int s = 0; s < STREAM_STAGES; ++s) fetch(row0 + s * step, s);
     uint4 w[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -375,7 +388,7 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM, WARP), stream_ctas(NV
     uint32_t ph = 0;
     for (int64_t row = row0; row < p.T; row += step) {
         const int64_t base = row * p.D;
-        const uint8_t *src = ring + s * stage_bytes;
+        const uint8_t *src = row_smem + s * stage_bytes;
         auto load_h = [&](int c) {
             uint4 h = *reinterpret_cast<const uint4 *>(src + 16 * c);
             if (has_res) h = add_bf16x8(h, *reinterpret_cast<const uint4 *>(src + row_bytes + 16 * c));
@@ -385,8 +398,7 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM, WARP), stream_ctas(NV
         mbar_wait(&full[s], ph, &abort_flag);
         __syncwarp();
         uint4 held[NV];  // h, or the quantiser's row
-        float v[8];
-        float ss = 0.0f;
+        float2 v[4], ss2 = make_float2(0.0f, 0.0f);
         uint32_t mx = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -396,19 +408,23 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM, WARP), stream_ctas(NV
                 h = load_h(c);
                 if (has_res && p.H && in_bounds(base + 8 * c, 8, total)) *reinterpret_cast<uint4 *>(p.H + base + 8 * c) = h;
             }
-            row_stats<NORM>(h, w[i], v, ss, mx);
+            row_stats<NORM>(h, w[i], v, ss2, mx);
             held[i] = h;
         }
-        if (NORM) ss = warp_sum(ss);
+        float ss = NORM ? warp_sum(ss2.x + ss2.y) : 0.0f;
         mx = __reduce_max_sync(0xffffffffu, row_max_bits<NORM>(mx));
-        if (!WARP) {
-            if (lane == 0) {
-                s_sum[turn][warp] = ss;
-                s_max[turn][warp] = mx;
-            }
-            __syncthreads();
-            if (NORM) ss = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
-            mx = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[turn][lane] : 0u);
+        if (lane == 0) {
+            s_sum[turn][warp] = ss;
+            s_max[turn][warp] = mx;
+        }
+        __syncthreads();
+        if (NORM) ss = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
+        mx = __reduce_max_sync(0xffffffffu, lane < nw ? s_max[turn][lane] : 0u);
+        // without this the compiler keeps the row's p and the weight as floats across the barrier, twice the registers
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            asm volatile("" : "+r"(held[i].x), "+r"(held[i].y), "+r"(held[i].z), "+r"(held[i].w));
+            if (NORM) asm volatile("" : "+r"(w[i].x), "+r"(w[i].y), "+r"(w[i].z), "+r"(w[i].w));
         }
         float rstd = 1.0f;
         if (NORM) {
@@ -418,25 +434,20 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM, WARP), stream_ctas(NV
 #pragma unroll
                 for (int i = 0; i < NV; ++i) s2 = scaled_squares(held[i], s2);
                 s2 = warp_sum(s2);
-                if (!WARP) {
-                    __syncthreads();
-                    if (lane == 0) s_sum[turn][warp] = s2;
-                    __syncthreads();
-                    s2 = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
-                }
+                __syncthreads();
+                if (lane == 0) s_sum[turn][warp] = s2;
+                __syncthreads();
+                s2 = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
                 rstd = row_rstd(s2, inv_d, 0.0f) * 0x1p-80f;
             }
         }
-        if (WARP) __syncwarp();
         if (gi == 0) {
-            // every thread of the group has read the stage
-            fetch(row + stages * step, s);
+            // every thread has read the stage
+            fetch(row + STREAM_STAGES * step, s);
             if (NORM && p.rstd && in_bounds(row, 1, p.T)) p.rstd[row] = rstd;
         }
-        if (++s == stages) {
-            s = 0;
-            ph ^= 1;
-        }
+        ph ^= s;
+        s ^= 1;
         turn ^= 1;  // the next row's sums go beside this row's, which other warps may still read
         const bool finite = mx < kInfBits;
         const float pmax = __uint_as_float(mx);
@@ -447,7 +458,7 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM, WARP), stream_ctas(NV
         for (int i = 0; i < NV; ++i) {
             const int c = gi + i * gsize;
             if (c < nchunk && in_bounds(base + 8 * c, 8, total)) {
-                row_stats<NORM>(held[i], w[i], v, ss, mx);  // p again
+                row_stats<NORM>(held[i], w[i], v, ss2, mx);  // p again
                 row_outputs<NORM>(p, base + 8 * c, v, rstd, q, finite);
             }
         }
@@ -582,7 +593,8 @@ __global__ void __launch_bounds__(WARP ? 64 * ROW_WARPS : 1024) row_bwd_once_ker
     }
 }
 
-// Many rows: persistent groups with the rings of row_stream_kernel.  A group
+// Many rows: persistent groups (a warp up to 1024 values, a CTA above) with the
+// rings of row_stream_kernel.  A group
 // keeps its sum of dY n in registers, a CTA writes its groups' sum as one row
 // of `part`, and dw_sum_kernel adds those rows in a fixed order.  The second
 // pass reads the row again from shared memory, so registers hold only the sums
@@ -591,10 +603,10 @@ __global__ void __launch_bounds__(WARP ? 64 * ROW_WARPS : 1024) row_bwd_once_ker
 // with dres (8 bytes a value): 60 us, 85% of the copy rate.
 template <int NV, bool WARP>
 __global__ void __launch_bounds__(stream_threads(NV, true, WARP), stream_bwd_ctas(NV, WARP))
-    row_bwd_stream_kernel(const __grid_constant__ RowBwdParams p, int stages) {
+    row_bwd_stream_kernel(const __grid_constant__ RowBwdParams p) {
     extern __shared__ __align__(16) uint8_t row_smem[];
     constexpr int GROUPS = WARP ? STREAM_WARPS : 1;
-    __shared__ __align__(8) uint64_t s_full[GROUPS][STREAM_MAX_STAGES];
+    __shared__ __align__(8) uint64_t s_full[GROUPS][STREAM_STAGES];
     __shared__ float s_sum[2][32];
     __shared__ int abort_flag;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -603,10 +615,10 @@ __global__ void __launch_bounds__(stream_threads(NV, true, WARP), stream_bwd_cta
     const int64_t total = p.T * p.D;
     const uint32_t row_bytes = (uint32_t)p.D * 2;
     const uint32_t stage_bytes = (p.dres ? 3 : 2) * row_bytes;
-    uint8_t *ring = row_smem + (uint32_t)(group * stages) * stage_bytes;
+    uint8_t *ring = row_smem + (uint32_t)(group * STREAM_STAGES) * stage_bytes;
     uint64_t *full = s_full[group];
     if (threadIdx.x == 0) {
-        for (int i = 0; i < GROUPS * STREAM_MAX_STAGES; ++i) mbar_init(&s_full[0][0] + i, 1);
+        for (int i = 0; i < GROUPS * STREAM_STAGES; ++i) mbar_init(&s_full[0][0] + i, 1);
         abort_flag = 0;
         fence_barrier_init();
     }
@@ -623,7 +635,7 @@ __global__ void __launch_bounds__(stream_threads(NV, true, WARP), stream_bwd_cta
         if (p.dres) bulk_load(dst + 2 * row_bytes, p.dres + row * p.D, row_bytes, &full[s]);
     };
     if (gi == 0)
-        for (int s = 0; s < stages; ++s) fetch(row0 + s * step, s);
+        for (int s = 0; s < STREAM_STAGES; ++s) fetch(row0 + s * step, s);
     uint4 w[NV];
     float acc[NV][8];
 #pragma unroll
@@ -666,7 +678,7 @@ __global__ void __launch_bounds__(stream_threads(NV, true, WARP), stream_bwd_cta
             if (lane == 0) s_sum[turn][warp] = dot;
             __syncthreads();
             // the stage of the row before: every thread has left its second pass
-            if (gi == 0 && row > row0) fetch(row + (stages - 1) * step, s == 0 ? stages - 1 : s - 1);
+            if (gi == 0 && row > row0) fetch(row + step, s ^ 1);
             dot = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
             turn ^= 1;
         }
@@ -694,12 +706,10 @@ __global__ void __launch_bounds__(stream_threads(NV, true, WARP), stream_bwd_cta
         }
         if (WARP) {
             __syncwarp();
-            if (gi == 0) fetch(row + stages * step, s);
+            if (gi == 0) fetch(row + STREAM_STAGES * step, s);
         }
-        if (++s == stages) {
-            s = 0;
-            ph ^= 1;
-        }
+        ph ^= s;
+        s ^= 1;
     }
     // this CTA's partial row; the warps of the warp form add theirs in warp order, in the rings' memory
     const int64_t pbase = (int64_t)blockIdx.x * p.D, ptotal = (int64_t)p.parts * p.D;

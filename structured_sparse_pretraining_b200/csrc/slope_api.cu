@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -1596,33 +1597,31 @@ RowPlan pick_row_plan(int64_t D) {
     return RowPlan{false, nv, (chunks + 32 * nv - 1) / (32 * nv) * 32};
 }
 
-// Rings of rows for many rows (row_stream_kernel and row_bwd_stream_kernel), a
-// warp's or a CTA's: nv 16-byte chunks per thread, CTAs per SM, and as many
-// stages as shared memory holds; stages = 0 where not two rows of `row_bytes`
-// fit.
+// Rings of rows for many rows (row_stream_kernel and row_bwd_stream_kernel, the
+// latter also with a warp's): nv 16-byte chunks per thread and as many CTAs per
+// SM as its registers and shared memory hold; per_sm = 0 where one CTA's ring
+// of two rows of `row_bytes` does not fit.
 struct StreamPlan {
     bool warp;
-    int nv, threads, per_sm, stages, smem, rows;  // rows in work at once in a CTA
+    int nv, threads, per_sm, smem, rows;  // rows in work at once in a CTA
 };
 constexpr int STREAM_SMEM = 224 * 1024;  // of an SM, for its CTAs' rings
 StreamPlan pick_stream_plan(int64_t D, int64_t row_bytes, bool norm, bool backward) {
     const int chunks = (int)(D / 8);
     StreamPlan s{};
-    s.warp = chunks <= 128;
+    s.warp = backward && chunks <= 128;
     const int most_nv = 6;  // with 384 threads; longer rows take 8
     s.nv = s.warp ? (chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4) : chunks <= most_nv * 384 ? (chunks + 383) / 384 : 8;
+    // Two chunks at least, which share a row's reductions (8192 x 1280 in int8: 14 us against 17), but the gradients'
+    // sums of dw want the registers (8192 x 2048: 30 us with one chunk, 32 with two).
+    if (!backward && s.nv < 2) s.nv = 2;
     s.threads = s.warp ? 32 * slope::STREAM_WARPS : (chunks + 32 * s.nv - 1) / (32 * s.nv) * 32;
     s.rows = s.warp ? slope::STREAM_WARPS : 1;
-    s.per_sm = backward ? slope::stream_bwd_ctas(s.nv, s.warp) : slope::stream_ctas(s.nv, norm, s.warp);
+    s.per_sm = backward ? slope::stream_bwd_ctas(s.nv, s.warp) : slope::stream_ctas(s.nv, norm);
     // as many CTAs as the registers of those with the most threads hold
     if (!s.warp) s.per_sm = s.per_sm * slope::stream_threads(s.nv, norm, false) / s.threads;
-    for (; s.per_sm >= 1; --s.per_sm) {
-        const int64_t fit = (STREAM_SMEM / s.per_sm - 2048) / (row_bytes * s.rows);
-        s.stages = (int)(fit > slope::STREAM_MAX_STAGES ? slope::STREAM_MAX_STAGES : fit);
-        if (s.stages >= 2) break;
-    }
-    if (s.stages < 2) s.stages = 0;
-    s.smem = (int)(s.stages * s.rows * row_bytes);
+    s.smem = (int)(slope::STREAM_STAGES * s.rows * row_bytes);
+    while (s.per_sm > 0 && STREAM_SMEM / s.per_sm - 2048 < s.smem) --s.per_sm;
     return s;
 }
 
@@ -1638,33 +1637,36 @@ int allow_smem(Kern kern, int bytes, std::atomic<uint64_t> &done) {
     return SLOPE_OK;
 }
 
-template <int NV, bool NORM, bool WARP>
-int row_stream_launch(const slope::RowParams &p, const StreamPlan &s, int sms, cudaStream_t st, const char *what) {
+template <int NV, bool NORM>
+int row_stream_launch(const slope::RowParams &p, const StreamPlan &s, int64_t ctas, cudaStream_t st, const char *what) {
     static std::atomic<uint64_t> done{0};
-    if (int rc = allow_smem(slope::row_stream_kernel<NV, NORM, WARP>, STREAM_SMEM - 2048, done)) return rc;
-    const int64_t most = (int64_t)sms * s.per_sm;
-    return launch_pdl(slope::row_stream_kernel<NV, NORM, WARP>, dim3((unsigned)most), dim3((unsigned)s.threads), s.smem, st, what,
-                      p, s.stages);
+    if (int rc = allow_smem(slope::row_stream_kernel<NV, NORM>, STREAM_SMEM - 2048, done)) return rc;
+    return launch_pdl(slope::row_stream_kernel<NV, NORM>, dim3((unsigned)ctas), dim3((unsigned)s.threads), s.smem, st, what, p);
 }
 
 template <bool NORM>
 int row_launch(const slope::RowParams &p, int sms, cudaStream_t st, const char *what) {
     const RowPlan r = pick_row_plan(p.D);
-    const StreamPlan s = pick_stream_plan(p.D, p.D * (p.res ? 4 : 2), NORM, false);
-    // rings pay from two rows for each of their groups on
-    if (s.stages > 0 && p.T >= 2 * (int64_t)sms * s.per_sm * s.rows) {
-        if (s.warp) {
-            if (s.nv == 1) return row_stream_launch<1, NORM, true>(p, s, sms, st, what);
-            if (s.nv == 2) return row_stream_launch<2, NORM, true>(p, s, sms, st, what);
-            return row_stream_launch<4, NORM, true>(p, s, sms, st, what);
-        }
-        if (s.nv == 1) return row_stream_launch<1, NORM, false>(p, s, sms, st, what);
-        if (s.nv == 2) return row_stream_launch<2, NORM, false>(p, s, sms, st, what);
-        if (s.nv == 3) return row_stream_launch<3, NORM, false>(p, s, sms, st, what);
-        if (s.nv == 4) return row_stream_launch<4, NORM, false>(p, s, sms, st, what);
-        if (s.nv == 5) return row_stream_launch<5, NORM, false>(p, s, sms, st, what);
-        if (s.nv == 6) return row_stream_launch<6, NORM, false>(p, s, sms, st, what);
-        return row_stream_launch<8, NORM, false>(p, s, sms, st, what);
+    // Rings pay where a row is long and there are rows to take: with residual and both outputs 4800 x 5120 (20 KB a
+    // row) 37 us against 43 with a row to a CTA, 9600 x 2048 (8 KB) 35 against 33; the quantiser at 9600 x 9216 45
+    // against 50, at 9600 x 5120 26 on both sides, at 1200 x 9216 10.5 against 9.0.
+    const int64_t row_bytes = p.D * (p.res ? 4 : 2);
+    const StreamPlan s = pick_stream_plan(p.D, row_bytes, NORM, false);
+    const int64_t resident = (int64_t)sms * s.per_sm;
+    if (s.per_sm > 0 && row_bytes >= 12288 && p.T >= (NORM ? 2 : 4) * resident) {
+        // Rounds of CTAs, so that fast SMs take more of them: two, or eight with a residual, whose rows move more
+        // bytes; but each CTA starts with an empty ring, so it gets eight rows, or two where others run beside it
+        // and the residual's bytes hide that (4096 x 16384 with one CTA per SM: 99 us with four rounds, 107 with
+        // eight; 8192 x 5120: 52 us with eight, 54 with four, 60 with one).
+        const int64_t rows = p.res && s.per_sm > 1 ? 2 : 8;
+        const int64_t rounds = std::max<int64_t>(1, std::min<int64_t>(p.res ? 8 : 2, p.T / (resident * rows)));
+        const int64_t ctas = rounds * resident;
+        if (s.nv == 2) return row_stream_launch<2, NORM>(p, s, ctas, st, what);
+        if (s.nv == 3) return row_stream_launch<3, NORM>(p, s, ctas, st, what);
+        if (s.nv == 4) return row_stream_launch<4, NORM>(p, s, ctas, st, what);
+        if (s.nv == 5) return row_stream_launch<5, NORM>(p, s, ctas, st, what);
+        if (s.nv == 6) return row_stream_launch<6, NORM>(p, s, ctas, st, what);
+        return row_stream_launch<8, NORM>(p, s, ctas, st, what);
     }
     const int64_t blocks = r.warp ? (p.T + slope::ROW_WARPS - 1) / slope::ROW_WARPS : p.T;
     const dim3 grid((unsigned)blocks), block((unsigned)r.threads);
@@ -1691,7 +1693,7 @@ struct BwdPlan {
 };
 BwdPlan pick_bwd_plan(int64_t T, int64_t D) {
     BwdPlan b{pick_row_plan(D), pick_stream_plan(D, 6 * D, true, true), 0};
-    if (T <= BWD_ONCE_ROWS || b.stream.nv > 6 || b.stream.stages == 0) return b;
+    if (T <= BWD_ONCE_ROWS || b.stream.nv > 6 || b.stream.per_sm == 0) return b;
     const int64_t blocks = (T + b.stream.rows - 1) / b.stream.rows, most = 148 * (int64_t)b.stream.per_sm;
     b.parts = blocks < most ? blocks : most;
     return b;
@@ -1711,7 +1713,7 @@ int row_bwd_stream_launch(const slope::RowBwdParams &p, const StreamPlan &s, cud
     static std::atomic<uint64_t> done{0};
     if (int rc = allow_smem(slope::row_bwd_stream_kernel<NV, WARP>, STREAM_SMEM - 2048, done)) return rc;
     return launch_pdl(slope::row_bwd_stream_kernel<NV, WARP>, dim3((unsigned)p.parts), dim3((unsigned)s.threads), s.smem, st,
-                      what, p, s.stages);
+                      what, p);
 }
 }  // namespace
 

@@ -338,10 +338,10 @@ constexpr int STREAM_WARPS = 8;  // rows in work at once in a CTA of the gradien
 // Threads at most and CTAs per SM of a form with NV chunks a thread.  Norm:
 // 12288 with everything 143 us with two CTAs per SM, 151 with one; 16384 99
 // us (4096 rows) with one, 127 with two, which spill.  Quantiser: 9216 36 us
-// with three, 38 with two.  Few chunks to many threads beat more to fewer
+// with four, 38 with two; 12288 50 and 48.  Few chunks to many threads beat more to fewer
 // (16384: 99 us with six, 196 with eight, which spill).
 constexpr int stream_threads(int nv, bool norm, bool warp) { return warp ? 32 * STREAM_WARPS : nv <= 6 ? 384 : norm ? 512 : 1024; }
-constexpr int stream_ctas(int nv, bool norm) { return norm ? (nv <= 2 ? 3 : nv <= 4 ? 2 : 1) : nv <= 4 ? 3 : nv <= 6 ? 2 : 1; }
+constexpr int stream_ctas(int nv, bool norm) { return norm ? (nv <= 2 ? 3 : nv <= 4 ? 2 : 1) : nv <= 3 ? 4 : nv <= 6 ? 2 : 1; }
 constexpr int stream_bwd_ctas(int nv, bool warp) { return warp ? (nv <= 2 ? 3 : 2) : nv <= 2 ? 3 : nv == 3 ? 2 : 1; }
 template <int NV, bool NORM>
 __global__ void __launch_bounds__(stream_threads(NV, NORM, false), stream_ctas(NV, NORM))
@@ -736,7 +736,9 @@ __global__ void __launch_bounds__(stream_threads(NV, true, WARP), stream_bwd_cta
 }
 
 // dw[d] = sum over the `parts` rows of part[.][d], in a fixed order: 32
-// columns per CTA, 8 warps over the rows, their sums added in warp order.
+// columns per CTA, 8 warps over the rows, their sums added in warp order.  (32
+// warps with every load in flight were slower, 64 against 60 us at 8192 x 5120:
+// CTAs of that size do not fit beside the rings' and start after them.)
 __global__ void __launch_bounds__(256) dw_sum_kernel(const float *part, int parts, int D, float *dw) {
     __shared__ float s[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -1654,12 +1654,11 @@ int row_launch(const slope::RowParams &p, int sms, cudaStream_t st, const char *
     const StreamPlan s = pick_stream_plan(p.D, row_bytes, NORM, false);
     const int64_t resident = (int64_t)sms * s.per_sm;
     if (s.per_sm > 0 && row_bytes >= 12288 && p.T >= (NORM ? 2 : 4) * resident) {
-        // Rounds of CTAs, so that fast SMs take more of them: two, or eight with a residual, whose rows move more
-        // bytes; but each CTA starts with an empty ring, so it gets eight rows, or two where others run beside it
-        // and the residual's bytes hide that (4096 x 16384 with one CTA per SM: 99 us with four rounds, 107 with
-        // eight; 8192 x 5120: 52 us with eight, 54 with four, 60 with one).
-        const int64_t rows = p.res && s.per_sm > 1 ? 2 : 8;
-        const int64_t rounds = std::max<int64_t>(1, std::min<int64_t>(p.res ? 8 : 2, p.T / (resident * rows)));
+        // With a residual, whose rows move more bytes, rounds of CTAs, so that fast SMs take more of them.  Each CTA
+        // starts with an empty ring, so it gets two rows where others run beside it, else eight (4096 x 16384 with one
+        // CTA per SM: 99 us with four rounds, 107 with eight; 8192 x 5120: 52 us with eight, 54 with four, 60 with
+        // one; 8192 x 9216 without residual: 53 with one, 54 with two).
+        const int64_t rounds = p.res ? std::max<int64_t>(1, std::min<int64_t>(8, p.T / (resident * (s.per_sm > 1 ? 2 : 8)))) : 1;
         const int64_t ctas = rounds * resident;
         if (s.nv == 2) return row_stream_launch<2, NORM>(p, s, ctas, st, what);
         if (s.nv == 3) return row_stream_launch<3, NORM>(p, s, ctas, st, what);

@@ -84,5 +84,10 @@ def call(name, *args):
     lib = load()
     rc = getattr(lib, name)(*args)
     if rc != 0:
-        raise SlopeError(rc, lib.slope_last_error().decode())
+        raise error(rc)
     return rc
+
+
+def error(rc):
+    """SlopeError of a status that an entry point has just returned on this thread."""
+    return SlopeError(rc, load().slope_last_error().decode())

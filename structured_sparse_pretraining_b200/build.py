@@ -1,9 +1,11 @@
 """Build libslope.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a,
 and its debug build libslope_debug.so (-DSLOPE_DEBUG_BOUNDS: bounds checks on
-every plain global-memory access of the kernels, for tests)."""
+every plain global-memory access of the kernels, for tests), and with g++
+the Python module _calls.so (csrc/calls.cpp)."""
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -37,16 +39,40 @@ def _build_one(lib: str, extra, force: bool, verbose: bool) -> str:
     return lib
 
 
+def build_calls(force: bool = False) -> str:
+    """Build _calls.so: Python's and torch's headers, no device code."""
+    src, lib = os.path.join(HERE, "csrc", "calls.cpp"), os.path.join(HERE, "_calls.so")
+    deps = [src, os.path.join(ROOT, "include", "slope.h")]
+    if not force and os.path.exists(lib) and os.path.getmtime(lib) >= max(map(os.path.getmtime, deps)):
+        return lib
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    include = [sysconfig.get_paths()["include"], os.path.join(home, "include"),
+               os.path.join(home, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+           + [f"-isystem{d}" for d in include] + ["-o", lib, src, "-L" + os.path.join(home, "lib"),
+                                                  "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("g++ failed building _calls.so")
+    return lib
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = True) -> str:
-    """Build libslope.so (and, with debug=True, libslope_debug.so beside it,
-    in parallel); returns the release library's path."""
-    if not debug:
-        return _build_one(LIB, [], force, verbose)
+    """Build libslope.so and _calls.so (and, with debug=True, libslope_debug.so
+    beside them, in parallel); returns the release library's path."""
     from concurrent.futures import ThreadPoolExecutor
-    with ThreadPoolExecutor(2) as ex:
+    with ThreadPoolExecutor(3) as ex:
+        calls = ex.submit(build_calls, force)
+        if not debug:
+            calls.result()
+            return _build_one(LIB, [], force, verbose)
         rel = ex.submit(_build_one, LIB, [], force, verbose)
         dbg = ex.submit(_build_one, LIB_DEBUG, ["-DSLOPE_DEBUG_BOUNDS"], force, False)
         dbg.result()
+        calls.result()
         return rel.result()
 
 

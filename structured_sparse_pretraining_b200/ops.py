@@ -8,7 +8,6 @@ bf16 tensors are torch.bfloat16; the 16-bit position-code words ("meta") are
 torch.int16 tensors holding the uint16 patterns.
 """
 import ctypes
-import functools
 
 import torch
 
@@ -264,9 +263,35 @@ def bwd_dw_masked_noalloc(dY, X, meta, dW_vals):
     return dW_vals
 
 
-# The calls below may be a few microseconds of GPU work each, so their checks
-# take the short way when everything fits: one comparison chain per tensor, and
-# the long way, with its message, only for what does not.
+# The calls below may be a few microseconds of GPU work each, so they go through
+# the module _calls (csrc/calls.cpp) when everything fits: 4.5 us of host time
+# for fwd_q8 where the way from here takes 10.1.  What does not fit (another
+# device than the current one, a subclass, an error) goes the way from here,
+# with its messages.
+_calls = None
+
+
+def _bind():
+    """The module _calls, on the entry points of the loaded library."""
+    global _calls
+    try:
+        from . import _calls as calls
+    except ImportError as e:
+        raise RuntimeError(f"_calls.so not built or not loadable ({e}); run structured_sparse_pretraining_b200/build.py") from e
+    lib = _lib.load()
+    names = ("rmsnorm", "rmsnorm_bwd", "rmsnorm_bwd_ws", "quant_rows", "fwd_q8")
+    calls.bind(*(ctypes.cast(getattr(lib, "slope_" + n), ctypes.c_void_p).value for n in names))
+    _calls = calls
+    return calls
+
+
+def _done(out):
+    """The result of a call through _calls, or its status raised."""
+    if type(out) is int:
+        raise _lib.error(out)
+    return out
+
+
 def _fit(t, dtype, name, shape, dev):
     """t as a contiguous CUDA tensor of `dtype` and `shape` on device `dev`, or an error."""
     if t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
@@ -283,11 +308,6 @@ def _rows(t, dtype, name):
     raise ValueError(f"{name} has shape {tuple(t.shape)}, expected two dimensions")
 
 
-# torch's allocation for compiled code, on the current device: 0.8 us a tensor
-# where empty_like takes 1.3 and new_empty 2.0 to 2.5 (absent, new_empty serves)
-_new = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
-
-
 def _place(t):
     """(device index of a CUDA tensor, whether it is the current device)."""
     dev = t.get_device()
@@ -297,10 +317,7 @@ def _place(t):
 def _out(t, dtype, name, shape, like, place):
     """(output tensor, pointer): the given one, checked, or a new one."""
     if t is None:
-        if _new is not None and place[1]:
-            t = _new(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
-        else:
-            t = like.new_empty(shape, dtype=dtype)
+        t = like.new_empty(shape, dtype=dtype)
         return t, t.data_ptr()
     return t, _fit(t, dtype, name, shape, place[0])
 
@@ -315,7 +332,6 @@ def _call_on(place, name, *args):
         return _lib.call(name, *args, stream)
 
 
-@functools.lru_cache(maxsize=256)
 def _norm_bwd_floats(T, D):
     floats = ctypes.c_int64(0)
     _lib.call("slope_rmsnorm_bwd_ws", T, D, ctypes.byref(floats))
@@ -327,8 +343,7 @@ def rmsnorm(X, w, eps, res=None, with_rstd=False, H=None, Y=None, rstd=None):
     per token.  X, res [T, D] bf16, w [D] bf16.  H (h, the residual stream) is
     None without res; rstd [T] fp32 is written with with_rstd (rmsnorm_bwd
     needs it), else None."""
-    _, _, Y, H, rstd = _rmsnorm(X, w, eps, res, True, False, with_rstd, H, Y, None, None, rstd)
-    return Y, H, rstd
+    return _rmsnorm(X, w, eps, res, True, False, with_rstd, H, Y, None, None, rstd)[2:]
 
 
 def rmsnorm_q8(X, w, eps, res=None, with_y=False, with_rstd=False, H=None, Y=None, Q=None, qscale=None, rstd=None):
@@ -339,6 +354,9 @@ def rmsnorm_q8(X, w, eps, res=None, with_y=False, with_rstd=False, H=None, Y=Non
 
 
 def _rmsnorm(X, w, eps, res, with_y, with_q8, with_rstd, H, Y, Q, qscale, rstd):
+    out = (_calls or _bind()).rmsnorm(X, w, eps, res, with_y, with_q8, with_rstd, H, Y, Q, qscale, rstd)
+    if out is not None:
+        return _done(out)
     shape = T, D = tuple(_rows(X, torch.bfloat16, "X"))
     dev, _ = place = _place(X)
     pw = _fit(w, torch.bfloat16, "w", (D,), dev)
@@ -363,6 +381,9 @@ def rmsnorm_bwd(dY, H, w, rstd, dres=None, dH=None, dw=None):
     """(dH, dw): gradients of rmsnorm's Y with respect to h (X and res both
     take dH; dres, the gradient reaching h along the residual stream, is added)
     [T, D] bf16 and to w [D] fp32.  H is rmsnorm's (or X without a residual)."""
+    out = (_calls or _bind()).rmsnorm_bwd(dY, H, w, rstd, dres, dH, dw)
+    if out is not None:
+        return _done(out)
     shape = T, D = tuple(_rows(dY, torch.bfloat16, "dY"))
     dev, _ = place = _place(dY)
     ph = _fit(H, torch.bfloat16, "H", shape, dev)
@@ -380,6 +401,9 @@ def rmsnorm_bwd(dY, H, w, rstd, dres=None, dH=None, dw=None):
 def quant_rows(A, Q=None, scale=None):
     """(Q, scale): rows of A [rows, K] bf16 in int8 with one fp32 scale per row
     (the kept weights of prune24: one per output channel)."""
+    out = (_calls or _bind()).quant_rows(A, Q, scale)
+    if out is not None:
+        return _done(out)
     shape = rows, K = tuple(_rows(A, torch.bfloat16, "A"))
     place = _place(A)
     Q, pq = _out(Q, torch.int8, "Q", shape, A, place)
@@ -393,6 +417,9 @@ def fwd_q8(Xq, xscale, vals_q, wscale, meta, XL, R, out_features, Y=None):
     Xq [T, in] and xscale [T] from rmsnorm_q8 or quant_rows, and vals_q
     [out, in/2], wscale [out] the kept weights through quant_rows (XL, R None:
     no adapter)."""
+    out = (_calls or _bind()).fwd_q8(Xq, xscale, vals_q, wscale, meta, XL, R, out_features, Y)
+    if out is not None:
+        return _done(out)
     T, in_ = _rows(Xq, torch.int8, "Xq")
     dev, _ = place = _place(Xq)
     ps = _fit(xscale, torch.float32, "xscale", (T,), dev)

@@ -111,20 +111,18 @@ __device__ __forceinline__ void q8_store(const float (&v)[W], const Q8Params &p,
 // reads as zero).  Words past the row are zeros that no MMA reads.
 __device__ __forceinline__ void q8_copy_codes(uint8_t *e, const uint16_t *meta, int M, int K, int m0, int kt, int lane) {
     const int words = K >> 4;  // a multiple of 4
+    const int c = lane & 3;  // four lanes to a row, so that a copy touches 8 sectors and not 32
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = lane + 32 * i, x = (row >> 2) & 1;
-        const int64_t at = (int64_t)(m0 + row) * words + kt * 16;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint8_t *dst = e + row * 32 + 16 * ((c >> 1) ^ x) + 8 * (c & 1);
-            if (m0 + row >= M) {
-                *reinterpret_cast<uint2 *>(dst) = make_uint2(0x44444444u, 0x44444444u);
-                continue;
-            }
-            const bool in = kt * 16 + 4 * c < words && in_bounds(at + 4 * c, 4, (int64_t)M * words);
-            cp_async8(dst, in ? meta + at + 4 * c : meta, in ? 8u : 0u);
+    for (int i = 0; i < 16; ++i) {
+        const int row = 8 * i + (lane >> 2), x = (row >> 2) & 1;
+        const int64_t at = (int64_t)(m0 + row) * words + kt * 16 + 4 * c;
+        uint8_t *dst = e + row * 32 + 16 * ((c >> 1) ^ x) + 8 * (c & 1);
+        if (m0 + row >= M) {
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(0x44444444u, 0x44444444u);
+            continue;
         }
+        const bool in = kt * 16 + 4 * c < words && in_bounds(at, 4, (int64_t)M * words);
+        cp_async8(dst, in ? meta + at : meta, in ? 8u : 0u);
     }
 }
 

@@ -12,9 +12,9 @@
 // into an fp32 accumulator of its own, and the epilogue joins the two, which
 // neither scale could do inside one accumulator.
 //
-// Roles (224 threads): warp 0 operand producer, warp 1 TMEM owner and MMA
-// issuer, warps 2..5 epilogue, warp 6 loads the codes where TMA cannot
-// (q8_copy_codes).
+// Roles: warp 0 operand producer, warp 1 TMEM owner and MMA
+// issuer, warps 2..5 epilogue, the others load the codes where TMA
+// cannot (q8_load_codes).
 //
 // Persistent clusters of `splits` CTAs; the CTAs of a cluster share each
 // tile's sum over K, so that tiles can be handed out evenly whatever their
@@ -27,8 +27,8 @@
 // depend on the split.  The integer accumulator is double-buffered: the next
 // tile's MMAs run beside the epilogue.  Row tiles past the end start at
 // M - 128 instead, so that every code the MMA reads is a legal one (a layer of
-// 64 channels gets its codes from warp 6); K ends inside a k-tile after whole
-// MMAs.
+// 64 channels gets its codes from q8_load_codes); K ends inside a k-tile after
+// whole MMAs.
 //
 // Measured, with adapters: one token on 9216 -> 27648 31 us (80% of the copy
 // rate), sixteen on 36864 -> 9216 39.5; sixteen on 20480 -> 5120 19 us with
@@ -47,7 +47,7 @@ struct Q8Params {
     int M, T, K, r;        // output channels, tokens, dense K, adapter rank
     int m_tiles, num_work;
     int splits;            // CTAs per cluster
-    int meta_tma;          // 1: codes by TMA, 0: by warp 6
+    int meta_tma;          // 1: codes by TMA, 0: by the warps from 6 on
     const uint16_t *meta;  // [M x K/16]
     const float *xscale, *wscale;
     uint16_t *Y;           // [T x M]
@@ -79,6 +79,8 @@ struct Q8Cfg {
     static constexpr int BAR_BYTES = 256;
     static constexpr int NS_RAW = (232448 - 1024 - BAR_BYTES - XS_BYTES - RED_BYTES) / STAGE_BYTES;
     static constexpr int NS = NS_RAW > 8 ? 8 : NS_RAW;
+    static constexpr int CODE_WARPS = NS % 4 == 0 ? 4 : NS % 3 == 0 ? 3 : NS;  // a divisor of NS, see q8_load_codes
+    static constexpr int THREADS = 32 * (6 + CODE_WARPS);
     static constexpr int ADP_COL = 2 * BN;    // fp32 adapter accumulator, after the two integer ones
     static constexpr int E_COL = 3 * BN;      // 8 columns per stage
     static constexpr int TMEM_COLS = BN == 128 ? 512 : BN >= 32 ? 256 : 128;
@@ -104,30 +106,69 @@ __device__ __forceinline__ void q8_store(const float (&v)[W], const Q8Params &p,
     }
 }
 
-// A 128 x 32-byte code tile (rows from m0, k-tile kt) into `e` in the 32-byte
-// swizzle, as 8-byte copies of one warp: for code rows of K/8 bytes that are
-// not a multiple of 16, which TMA cannot address, and for layers of 64
-// channels, whose missing rows take positions 0 and 1 (of kept values that TMA
-// reads as zero).  Words past the row are zeros that no MMA reads.
-__device__ __forceinline__ void q8_copy_codes(uint8_t *e, const uint16_t *meta, int M, int K, int m0, int kt, int lane) {
-    const int words = K >> 4;  // a multiple of 4
-    const int c = lane & 3;  // four lanes to a row, so that a copy touches 8 sectors and not 32
+// The code tiles of a kernel's k-tiles (128 rows x 32 bytes, in the 32-byte
+// swizzle), by WARPS warps in turn: for code rows of K/8 bytes that are not a
+// multiple of 16, which TMA cannot address, and for layers of 64 channels,
+// whose missing rows take positions 0 and 1 (of kept values that TMA reads as
+// zero).  Words past the row are zeros that no MMA reads.
+//
+// A warp has the codes of its next k-tile on their way in registers (8 bytes at
+// a time, four lanes to a row) while it waits for the stage.  More than one
+// k-tile ahead does not work within a warp, as the fence between its stores and
+// the tensor core's reads waits for its loads too: 16 tokens, 9152 -> 27648
+// take 38.7 us with four warps, 77 with one that is four ahead, 41 with one
+// whose asynchronous copies go into the stage (codes by TMA, 9344: 33).
+//
+// Work items first, first + step, .. below num_work, each with the k-tiles
+// [k0, k1) and `extra` ones without codes; row0(w) is a work item's first row,
+// dst(s) the stage's code tile, wait(s, phase) the stage's being free,
+// publish(s) the warp's arrival.  False where a wait gave up.  WARPS divides NS,
+// so that a stage has one warp, which sees each of its phases: a wait tells only
+// a phase's parity.
+template <int WARPS, int NS, typename Row0, typename Dst, typename Wait, typename Publish>
+__device__ __forceinline__ bool q8_load_codes(const uint16_t *meta, int M, int K, int which, int lane, int first, int step,
+                                              int num_work, int k0, int k1, int extra, Row0 row0, Dst dst, Wait wait,
+                                              Publish publish) {
+    static_assert(NS % WARPS == 0, "one warp per stage");
+    const int words = K >> 4;  // of a row; a multiple of 4
+    const int c = lane & 3;
+    int w = first, kt = k0, s = 0;
+    uint32_t ph = 0;
+    auto advance = [&](int n) {
+        for (kt += n; kt >= k1 + extra && w < num_work; w += step) kt -= k1 + extra - k0;
+        for (s += n; s >= NS; ph ^= 1) s -= NS;
+    };
+    for (advance(which); w < num_work; advance(WARPS)) {
+        uint2 v[16];
+        if (kt < k1) {
+            const bool in = kt * 16 + 4 * c < words;
+            const int m0 = row0(w);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int row = 8 * i + (lane >> 2), x = (row >> 2) & 1;
-        const int64_t at = (int64_t)(m0 + row) * words + kt * 16 + 4 * c;
-        uint8_t *dst = e + row * 32 + 16 * ((c >> 1) ^ x) + 8 * (c & 1);
-        if (m0 + row >= M) {
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(0x44444444u, 0x44444444u);
-            continue;
+            for (int i = 0; i < 16; ++i) {
+                const int row = m0 + 8 * i + (lane >> 2);
+                const int64_t at = (int64_t)row * words + kt * 16 + 4 * c;
+                v[i] = row >= M ? make_uint2(0x44444444u, 0x44444444u) : make_uint2(0, 0);
+                if (in && row < M && in_bounds(at, 4, (int64_t)M * words)) v[i] = load_ahead8(meta + at);
+            }
         }
-        const bool in = kt * 16 + 4 * c < words && in_bounds(at, 4, (int64_t)M * words);
-        cp_async8(dst, in ? meta + at : meta, in ? 8u : 0u);
+        if (!wait(s, ph ^ 1)) return false;
+        if (kt < k1) {
+            uint8_t *e = dst(s);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int row = 8 * i + (lane >> 2), x = (row >> 2) & 1;
+                *reinterpret_cast<uint2 *>(e + row * 32 + 16 * ((c >> 1) ^ x) + 8 * (c & 1)) = v[i];
+            }
+            fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) publish(s);
     }
+    return true;
 }
 
 template <int BN>
-__global__ void __launch_bounds__(224, 1)
+__global__ void __launch_bounds__(Q8Cfg<BN>::THREADS, 1)
     q8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmR,
                    const __grid_constant__ CUtensorMap tmXL, const __grid_constant__ Q8Params p) {
@@ -363,36 +404,14 @@ __global__ void __launch_bounds__(224, 1)
             }
         }
     } else if (!p.meta_tma) {
-        // ------------------------------------------------------------ code loader
-        // LAG stages of copies stay in flight: a stage is published once the copies of the LAG after it are issued,
-        // which needs stages that the MMAs have already passed (LAG < NS)
-        constexpr int LAG = NS >= 4 ? NS - 2 : 1;
-        int s = 0, issued = 0, published = 0;
-        uint32_t ph = 0;
-        auto publish = [&]() {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[published % NS]);
-            ++published;
-        };
-        for (int w = cluster; w < p.num_work; w += num_clusters) {
-            const int m0 = max(0, min(w % p.m_tiles * 128, p.M - 128));
-            for (int kt = k0; kt < k1 + adp_kts; ++kt) {
-                if (!mbar_wait_warp(&empty[s], ph ^ 1, abort_flag)) {
-                    cp_async_wait<0>();
-                    goto done;
-                }
-                if (kt < k1) q8_copy_codes(smem + s * C::STAGE_BYTES + C::A_BYTES + 2 * C::B_PANEL, p.meta, p.M, p.K, m0, kt, lane);
-                cp_async_commit();
-                if (++issued > LAG) {
-                    cp_async_wait<LAG>();
-                    publish();
-                }
-                if (++s == NS) { s = 0; ph ^= 1; }
-            }
-        }
-        cp_async_wait<0>();
-        while (published < issued) publish();
+        // ------------------------------------------------------------ code loaders
+        if (!q8_load_codes<C::CODE_WARPS, NS>(
+                p.meta, p.M, p.K, warp - 6, lane, cluster, num_clusters, p.num_work, k0, k1, adp_kts,
+                [&](int w) { return max(0, min(w % p.m_tiles * 128, p.M - 128)); },
+                [&](int st) { return smem + st * C::STAGE_BYTES + C::A_BYTES + 2 * C::B_PANEL; },
+                [&](int st, uint32_t phase) { return mbar_wait_warp(&empty[st], phase, abort_flag); },
+                [&](int st) { mbar_arrive(&full[st]); }))
+            goto done;
     }
 done:
     __syncwarp();

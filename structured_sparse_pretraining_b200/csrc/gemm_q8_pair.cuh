@@ -20,9 +20,9 @@
 // gemm_q8_wide.cuh: the epilogue scales the integers to fp32 in place, the
 // rank-r MMAs accumulate onto that.
 //
-// Roles (352 threads): warp 0 operand producer, warp 1 TMEM owner and (pair
+// Roles (384 threads): warp 0 operand producer, warp 1 TMEM owner and (pair
 // leader) MMA issuer, warps 2..9 epilogue (a quarter of the rows, half of the
-// columns each), warp 10 the codes where TMA cannot address them.
+// columns each), warps 10 and 11 the codes where TMA cannot address them.
 #pragma once
 #include <cstdint>
 #include "gemm_q8.cuh"
@@ -55,7 +55,7 @@ struct Q8PairParams {
     uint16_t *Y;
 };
 
-__global__ void __launch_bounds__(352, 1)
+__global__ void __launch_bounds__(384, 1)
     q8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmR,
                    const __grid_constant__ CUtensorMap tmXL, const __grid_constant__ Q8PairParams p) {
@@ -290,37 +290,17 @@ __global__ void __launch_bounds__(352, 1)
             }
         }
     } else if (!p.meta_tma) {
-        // ------------------------------------------------------------ code loader, see q8_tile_kernel
-        constexpr int LAG = 1;
-        int s = 0, issued = 0, published = 0;
-        uint32_t ph = 0;
-        auto publish = [&]() {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                if (rank == 0) mbar_arrive(&full[published % NS]);
-                else mbar_arrive_cluster(cluster_addr(&full[published % NS], 0));
-            }
-            ++published;
-        };
-        for (int w = pair; w < p.num_work; w += num_pairs) {
-            const int m0 = min(w / p.n_tiles * 256 + 128 * (int)rank, p.M - 128);
-            for (int kt = 0; kt < kts + adp_kts; ++kt) {
-                if (!mbar_wait_warp(&empty[s], ph ^ 1, abort_flag)) {
-                    cp_async_wait<0>();
-                    goto done;
-                }
-                if (kt < kts) q8_copy_codes(smem + s * C::STAGE_BYTES + C::A_BYTES + 2 * C::B_PANEL, p.meta, p.M, p.K, m0, kt, lane);
-                cp_async_commit();
-                if (++issued > LAG) {
-                    cp_async_wait<LAG>();
-                    publish();
-                }
-                if (++s == NS) { s = 0; ph ^= 1; }
-            }
-        }
-        cp_async_wait<0>();
-        while (published < issued) publish();
+        // ------------------------------------------------------------ code loaders (both CTAs)
+        if (!q8_load_codes<2, NS>(
+                p.meta, p.M, p.K, warp - 10, lane, pair, num_pairs, p.num_work, 0, kts, adp_kts,
+                [&](int w) { return min(w / p.n_tiles * 256 + 128 * (int)rank, p.M - 128); },
+                [&](int st) { return smem + st * C::STAGE_BYTES + C::A_BYTES + 2 * C::B_PANEL; },
+                [&](int st, uint32_t phase) { return mbar_wait_warp(&empty[st], phase, abort_flag); },
+                [&](int st) {
+                    if (rank == 0) mbar_arrive(&full[st]);
+                    else mbar_arrive_cluster(cluster_addr(&full[st], 0));
+                }))
+            goto done;
     }
 done:
     __syncwarp();

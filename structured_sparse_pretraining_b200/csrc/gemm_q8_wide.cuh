@@ -61,6 +61,24 @@ struct Q8WideParams {
     uint16_t *Y;
 };
 
+// A code tile (rows m0 .. m0 + 127 of the layer, k-tile kt) into `e` where TMA
+// cannot address it (see q8_load_codes), as asynchronous copies of one warp.
+// Here two of them in flight beat loads ahead into registers, whose fence
+// leaves one (2458 tokens, 27200 -> 5824: 225 against 339 us; codes by TMA,
+// 27264: 186), and the accumulators' 168 registers leave no room for more warps.
+__device__ __forceinline__ void q8_copy_codes(uint8_t *e, const uint16_t *meta, int M, int K, int m0, int kt, int lane) {
+    const int words = K >> 4;  // a multiple of 4
+    const int c = lane & 3;  // four lanes to a row, so that a copy touches 8 sectors and not 32
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int row = 8 * i + (lane >> 2), x = (row >> 2) & 1;
+        const int64_t at = (int64_t)(m0 + row) * words + kt * 16 + 4 * c;
+        uint8_t *dst = e + row * 32 + 16 * ((c >> 1) ^ x) + 8 * (c & 1);
+        const bool in = kt * 16 + 4 * c < words && in_bounds(at, 4, (int64_t)M * words);
+        cp_async8(dst, in ? meta + at : meta, in ? 8u : 0u);
+    }
+}
+
 __global__ void __launch_bounds__(384, 1)
     q8_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmR,
@@ -334,7 +352,8 @@ __global__ void __launch_bounds__(384, 1)
             }
         }
     } else if (!p.meta_tma) {
-        // ------------------------------------------------------------ code loaders (both CTAs), see q8_tile_kernel
+        // ------------------------------------------------------------ code loaders (both CTAs)
+        // LAG stages of copies stay in flight: a stage is published once those of the next are issued
         const int blk = warp - 10;
         constexpr int LAG = 1;
         int s = 0, issued = 0, published = 0;

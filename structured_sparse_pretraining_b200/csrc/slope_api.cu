@@ -1923,7 +1923,7 @@ int launch_q8_tile(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap
     if (p.splits > 8 || (p.splits - 1) * shares.most() * 512 > slope::Q8Cfg<BN>::RED_BYTES)
         return fail(SLOPE_ERR_SHAPE, "int8 product: no room for the partials of a cluster of %d", p.splits);
     const int slot = Q8_TILE_SLOT + 8 * (BN == 16 ? 0 : BN == 32 ? 1 : BN == 64 ? 2 : 3) + p.splits - 1;
-    return launch_clusters(slope::q8_tile_kernel<BN>, slot, p.splits, 224, slope::Q8Cfg<BN>::SMEM_BYTES, p.num_work, sms, st, a,
+    return launch_clusters(slope::q8_tile_kernel<BN>, slot, p.splits, slope::Q8Cfg<BN>::THREADS, slope::Q8Cfg<BN>::SMEM_BYTES, p.num_work, sms, st, a,
                            b, e, r2, xl, p);
 }
 
@@ -1989,7 +1989,7 @@ int q8_product(const int8_t *X, const float *xscale, const int8_t *W, const floa
         pp.xscale = xscale;
         pp.wscale = wscale;
         pp.Y = Y;
-        return launch_pairs(slope::q8_pair_kernel, Q8_PAIR_SLOT, 352, C::SMEM_BYTES, pp.num_work, d.sms, st, a, b, e, r2, xl, pp);
+        return launch_pairs(slope::q8_pair_kernel, Q8_PAIR_SLOT, 384, C::SMEM_BYTES, pp.num_work, d.sms, st, a, b, e, r2, xl, pp);
     }
     switch (plan.bn) {
         case 16: return launch_q8_tile<16>(a, b, e, r2, xl, p, d.sms, st);

@@ -1693,7 +1693,16 @@ struct BwdPlan {
 BwdPlan pick_bwd_plan(int64_t T, int64_t D) {
     BwdPlan b{pick_row_plan(D), pick_stream_plan(D, 6 * D, true, true), 0};
     if (T <= BWD_ONCE_ROWS || b.stream.nv > 6 || b.stream.per_sm == 0) return b;
-    const int64_t blocks = (T + b.stream.rows - 1) / b.stream.rows, most = 148 * (int64_t)b.stream.per_sm;
+    const int64_t blocks = (T + b.stream.rows - 1) / b.stream.rows;
+    int64_t most = 148 * (int64_t)b.stream.per_sm;
+    if (b.stream.warp) {
+        // Short rows: the second launch takes as long as the first, so no more CTAs per SM than leave a warp four rows,
+        // and an equal number of rows to each (8192 x 320: 10.9 us with 256 CTAs, 12.8 with 444; 4096 x 512: 8.0 with
+        // 128, 10.2 with 444).
+        const int64_t per_sm = std::min<int64_t>(b.stream.per_sm, (blocks + 4 * 148 - 1) / (4 * 148));
+        const int64_t rows = (blocks + 148 * per_sm - 1) / (148 * per_sm);
+        most = (blocks + rows - 1) / rows;
+    }
     b.parts = blocks < most ? blocks : most;
     return b;
 }

@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(WARP ? 64 * ROW_WARPS : 1024) row_bwd_once_ker
 // pass reads the row again from shared memory, so registers hold only the sums
 // and the weight.  A warp refills a stage after its own second pass, a CTA
 // after the next row's barrier, when every thread is done with it.  8192 x 5120
-// with dres (8 bytes a value): 60 us, 85% of the copy rate.
+// with dres (8 bytes a value): 59 us, 86% of the copy rate.
 template <int NV, bool WARP>
 __global__ void __launch_bounds__(stream_threads(NV, true, WARP), stream_bwd_ctas(NV, WARP))
     row_bwd_stream_kernel(const __grid_constant__ RowBwdParams p) {
@@ -736,26 +736,28 @@ __global__ void __launch_bounds__(stream_threads(NV, true, WARP), stream_bwd_cta
 }
 
 // dw[d] = sum over the `parts` rows of part[.][d], in a fixed order: 32
-// columns per CTA, 8 warps over the rows, their sums added in warp order.  (32
-// warps with every load in flight were slower, 64 against 60 us at 8192 x 5120:
-// CTAs of that size do not fit beside the rings' and start after them.)
-__global__ void __launch_bounds__(256) dw_sum_kernel(const float *part, int parts, int D, float *dw) {
-    __shared__ float s[8][32];
+// columns per CTA, DW_WARPS warps over the rows, their sums added in warp
+// order.  The gradients of 8192 x 2048 take 31.8 us with 16 warps, 33.3 with 8,
+// 35.2 with 32 that have every load in flight: CTAs of that size do not fit
+// beside the rings' and start after them.
+constexpr int DW_WARPS = 16;
+__global__ void __launch_bounds__(32 * DW_WARPS) dw_sum_kernel(const float *part, int parts, int D, float *dw) {
+    __shared__ float s[DW_WARPS][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int d = blockIdx.x * 32 + lane;
     grid_dep_wait();
     grid_dep_launch();
     float a = 0.0f;
     if (d < D) {
-#pragma unroll 8
-        for (int r = warp; r < parts; r += 8)
+#pragma unroll 4
+        for (int r = warp; r < parts; r += DW_WARPS)
             if (in_bounds((int64_t)r * D + d, 1, (int64_t)parts * D)) a += __ldcg(part + (int64_t)r * D + d);
     }
     s[warp][lane] = a;
     __syncthreads();
     if (warp == 0 && d < D) {
 #pragma unroll
-        for (int k = 1; k < 8; ++k) a += s[k][lane];
+        for (int k = 1; k < DW_WARPS; ++k) a += s[k][lane];
         if (in_bounds(d, 1, D)) dw[d] = a;
     }
 }

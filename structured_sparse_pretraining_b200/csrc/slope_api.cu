@@ -1820,7 +1820,7 @@ int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, 
                    : sp.nv == 5 ? row_bwd_stream_launch<5, false>(p, sp, st, what)
                                 : row_bwd_stream_launch<6, false>(p, sp, st, what);
     if (rc) return rc;
-    return launch_pdl(slope::dw_sum_kernel, dim3((unsigned)((D + 31) / 32)), dim3(256), 0, st, "rmsnorm_bwd dw launch",
+    return launch_pdl(slope::dw_sum_kernel, dim3((unsigned)((D + 31) / 32)), dim3(32 * slope::DW_WARPS), 0, st, "rmsnorm_bwd dw launch",
                       (const float *)ws, (int)parts, (int)D, dw);
 }
 

@@ -167,6 +167,29 @@ __device__ __forceinline__ bool q8_load_codes(const uint16_t *meta, int M, int K
     return true;
 }
 
+// A pair's peer tells the leader of each stage whose codes its own warps have
+// written (`codes`, this CTA's) by an arrival on the leader's `full`, which
+// releases at cluster scope what its wait has acquired from them: the leader's
+// tcgen05.cp reads the codes of both CTAs.  The peer's MMA warp does it, which
+// has nothing else to do and nothing in flight: a cluster-scope release by the
+// loading warps waits for their loads ahead too (512 x 224 tiles: 2458 tokens,
+// 27200 -> 5824 294 us against 400; 256 x 256 tiles, whose loaders wait for
+// their loads anyway: 6000 tokens, 832 -> 5184 35 against 38, 300 tokens,
+// 4160 -> 9216 26 against 25).  False where a wait gave up.
+template <int NS>
+__device__ __forceinline__ bool q8_relay_codes(uint64_t *codes, uint64_t *full, int lane, int first, int step, int num_work,
+                                               int ktiles, volatile int *abort_flag) {
+    int s = 0;
+    uint32_t ph = 0;
+    for (int w = first; w < num_work; w += step)
+        for (int kt = 0; kt < ktiles; ++kt) {
+            if (!mbar_wait_warp(&codes[s], ph, abort_flag)) return false;
+            if (lane == 0) mbar_arrive_cluster_rel(cluster_addr(&full[s], 0));
+            if (++s == NS) { s = 0; ph ^= 1; }
+        }
+    return true;
+}
+
 template <int BN>
 __global__ void __launch_bounds__(Q8Cfg<BN>::THREADS, 1)
     q8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,

@@ -22,7 +22,8 @@
 //
 // Roles (384 threads): warp 0 operand producer, warp 1 TMEM owner and (pair
 // leader) MMA issuer, warps 2..9 epilogue (a quarter of the rows, half of the
-// columns each), warps 10 and 11 the codes where TMA cannot address them.
+// columns each), warps 10 and 11 the codes where TMA cannot address them (the
+// peer's warp 1 then tells the leader of them: q8_relay_codes).
 #pragma once
 #include <cstdint>
 #include "gemm_q8.cuh"
@@ -41,7 +42,7 @@ struct Q8PairCfg {
     static constexpr int TMEM_COLS = 512;
     static constexpr int SMEM_BYTES = NS * STAGE_BYTES + STAGING_BYTES + 256 + 1024;
     static_assert(E_COL + 8 * NS <= TMEM_COLS, "TMEM budget");
-    static_assert(256 >= 8 * (2 * NS + 4) + 8, "barrier area");
+    static_assert(256 >= 8 * (3 * NS + 4) + 8, "barrier area");
     static_assert(STAGE_BYTES % 1024 == 0 && B_PANEL % 1024 == 0, "swizzle-atom alignment");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -49,12 +50,13 @@ struct Q8PairCfg {
 struct Q8PairParams {
     int M, T, K, r;
     int n_tiles, num_work;
-    int meta_tma;
     const uint16_t *meta;
     const float *xscale, *wscale;
     uint16_t *Y;
 };
 
+// META_TMA: codes by TMA, else by warps 10 and 11.
+template <bool META_TMA>
 __global__ void __launch_bounds__(384, 1)
     q8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmR,
@@ -70,7 +72,8 @@ __global__ void __launch_bounds__(384, 1)
     uint64_t *conv = acc_full + 1;        // leader: both CTAs' sums are scaled fp32 (16 arrivals)
     uint64_t *adp_full = conv + 1;        // each CTA: the adapter is added
     uint64_t *acc_empty = adp_full + 1;   // leader: both CTAs drained the accumulator (16 arrivals)
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(acc_empty + 1);
+    uint64_t *codes = acc_empty + 1;      // peer: its codes of stage s are written (not by TMA)
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(codes + NS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -80,8 +83,9 @@ __global__ void __launch_bounds__(384, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&full[s], p.meta_tma ? 1 : 3);
+            mbar_init(&full[s], META_TMA ? 1 : 3);
             mbar_init(&empty[s], 1);
+            mbar_init(&codes[s], 1);
         }
         mbar_init(acc_full, 1);
         mbar_init(conv, 16);
@@ -93,7 +97,7 @@ __global__ void __launch_bounds__(384, 1)
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
-        if (p.meta_tma) tma_prefetch_desc(&tmE);
+        if (META_TMA) tma_prefetch_desc(&tmE);
         if (p.r > 0) {
             tma_prefetch_desc(&tmR);
             tma_prefetch_desc(&tmXL);
@@ -125,9 +129,9 @@ __global__ void __launch_bounds__(384, 1)
                     uint8_t *b = a + C::A_BYTES;
                     const uint32_t lead_full = cluster_addr(&full[s], 0);
                     if (kt < kts) {
-                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (C::STAGE_BYTES - (p.meta_tma ? 0 : C::E_BYTES)));
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (C::STAGE_BYTES - (META_TMA ? 0 : C::E_BYTES)));
                         tma_load_2d_pair(a, &tmA, lead_full, kt * 128, m0);
-                        if (p.meta_tma) tma_load_2d_pair(b + 2 * C::B_PANEL, &tmE, lead_full, kt * 16, m0);
+                        if (META_TMA) tma_load_2d_pair(b + 2 * C::B_PANEL, &tmE, lead_full, kt * 16, m0);
                         tma_load_2d_pair(b, &tmB, lead_full, kt * 256, n0 + 128 * (int)rank);
                         tma_load_2d_pair(b + C::B_PANEL, &tmB, lead_full, kt * 256 + 128, n0 + 128 * (int)rank);
                     } else {  // adapter: R^T (MN-major, two panels of 64 channels) and XL, 64 of the rank
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (!mbar_wait_warp(acc_empty, (it & 1) ^ 1, abort_flag)) goto done;
                 tc_fence_after();
                 for (int kt = 0; kt < kts; ++kt) {
-                    if (!mbar_wait_warp(&full[s], ph, abort_flag)) goto done;
+                    if (!(META_TMA ? mbar_wait_warp(&full[s], ph, abort_flag) : mbar_wait_codes(&full[s], ph, abort_flag))) goto done;
                     tc_fence_after();
                     const uint64_t off = (uint64_t)((s * C::STAGE_BYTES) >> 4);
                     const uint32_t ecol = tmem_base + C::E_COL + 8 * s;
@@ -191,6 +195,8 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 elect_commit<true>(adp_full);
             }
+        } else if (!META_TMA) {
+            if (!q8_relay_codes<NS>(codes, full, lane, pair, num_pairs, p.num_work, kts + adp_kts, abort_flag)) goto done;
         }
     } else if (warp < 10) {
         // ------------------------------------------------------------ epilogue
@@ -289,17 +295,14 @@ __global__ void __launch_bounds__(384, 1)
                 __syncwarp();  // every lane has read the tile before the next chunk overwrites it
             }
         }
-    } else if (!p.meta_tma) {
+    } else if (!META_TMA) {
         // ------------------------------------------------------------ code loaders (both CTAs)
         if (!q8_load_codes<2, NS>(
                 p.meta, p.M, p.K, warp - 10, lane, pair, num_pairs, p.num_work, 0, kts, adp_kts,
                 [&](int w) { return min(w / p.n_tiles * 256 + 128 * (int)rank, p.M - 128); },
                 [&](int st) { return smem + st * C::STAGE_BYTES + C::A_BYTES + 2 * C::B_PANEL; },
                 [&](int st, uint32_t phase) { return mbar_wait_warp(&empty[st], phase, abort_flag); },
-                [&](int st) {
-                    if (rank == 0) mbar_arrive(&full[st]);
-                    else mbar_arrive_cluster(cluster_addr(&full[st], 0));
-                }))
+                [&](int st) { mbar_arrive(rank == 0 ? &full[st] : &codes[st]); }))
             goto done;
     }
 done:

@@ -17,7 +17,8 @@
 //
 // Roles (384 threads): warp 0 operand producer, warp 1 TMEM owner and (pair
 // leader) MMA issuer, warps 2..5 epilogue of block 0, warps 6..9 of block 1,
-// warps 10 and 11 the codes of block 0 and 1 where TMA cannot address them.
+// warps 10 and 11 the codes of block 0 and 1 where TMA cannot address them
+// (the peer's warp 1 then tells the leader of them: q8_relay_codes).
 // An epilogue warp takes its 32 channels x 224 tokens into registers as bf16
 // pairs, releases the accumulator, and only then transposes and stores, beside
 // the next tile's MMAs.  Row blocks past the end start at M - 128 instead and
@@ -47,7 +48,7 @@ struct Q8WideCfg {
     static constexpr int TMEM_COLS = 512;
     static constexpr int SMEM_BYTES = NS * STAGE_BYTES + STAGING_BYTES + 256 + 1024;
     static_assert(E_COL + 8 * NBLK * NS <= TMEM_COLS, "TMEM budget");
-    static_assert(256 >= 8 * (2 * NS + 1 + 3 * NBLK) + 8, "barrier area");
+    static_assert(256 >= 8 * (3 * NS + 1 + 3 * NBLK) + 8, "barrier area");
     static_assert(STAGE_BYTES % 1024 == 0 && B_PANEL % 1024 == 0, "swizzle-atom alignment");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -55,7 +56,6 @@ struct Q8WideCfg {
 struct Q8WideParams {
     int M, T, K, r;
     int m_tiles, n_tiles, raster_g, num_work;
-    int meta_tma;          // 1: codes by TMA, 0: by warps 10 and 11
     const uint16_t *meta;  // [M x K/16]
     const float *xscale, *wscale;
     uint16_t *Y;
@@ -64,8 +64,8 @@ struct Q8WideParams {
 // A code tile (rows m0 .. m0 + 127 of the layer, k-tile kt) into `e` where TMA
 // cannot address it (see q8_load_codes), as asynchronous copies of one warp.
 // Here two of them in flight beat loads ahead into registers, whose fence
-// leaves one (2458 tokens, 27200 -> 5824: 225 against 339 us; codes by TMA,
-// 27264: 186), and the accumulators' 168 registers leave no room for more warps.
+// leaves one, and the accumulators' 168 registers leave no room for more warps
+// (2458 tokens, 27200 -> 5824: 263 us; codes by TMA, 27264: 181).
 __device__ __forceinline__ void q8_copy_codes(uint8_t *e, const uint16_t *meta, int M, int K, int m0, int kt, int lane) {
     const int words = K >> 4;  // a multiple of 4
     const int c = lane & 3;  // four lanes to a row, so that a copy touches 8 sectors and not 32
@@ -79,6 +79,8 @@ __device__ __forceinline__ void q8_copy_codes(uint8_t *e, const uint16_t *meta, 
     }
 }
 
+// META_TMA: codes by TMA, else by warps 10 and 11.
+template <bool META_TMA>
 __global__ void __launch_bounds__(384, 1)
     q8_wide_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmR,
@@ -94,7 +96,8 @@ __global__ void __launch_bounds__(384, 1)
     uint64_t *conv = acc_full + 1;          // per block: leader: both CTAs' sums are scaled fp32 (8 arrivals)
     uint64_t *adp_full = conv + NBLK;       // per block: each CTA: the adapter is added
     uint64_t *acc_empty = adp_full + NBLK;  // per block: leader: both CTAs drained it (8 arrivals)
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(acc_empty + NBLK);
+    uint64_t *codes = acc_empty + NBLK;     // peer: its codes of stage s are written (not by TMA; an arrival per block)
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(codes + NS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -104,8 +107,9 @@ __global__ void __launch_bounds__(384, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&full[s], p.meta_tma ? 1 : 1 + 2 * NBLK);
+            mbar_init(&full[s], META_TMA ? 1 : 1 + NBLK + 1);
             mbar_init(&empty[s], 1);
+            mbar_init(&codes[s], NBLK);
         }
         mbar_init(acc_full, 1);
         for (int b = 0; b < NBLK; ++b) {
@@ -119,7 +123,7 @@ __global__ void __launch_bounds__(384, 1)
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
-        if (p.meta_tma) tma_prefetch_desc(&tmE);
+        if (META_TMA) tma_prefetch_desc(&tmE);
         if (p.r > 0) {
             tma_prefetch_desc(&tmR);
             tma_prefetch_desc(&tmXL);
@@ -156,11 +160,11 @@ __global__ void __launch_bounds__(384, 1)
                     uint8_t *e = b + 2 * C::B_PANEL;
                     const uint32_t lead_full = cluster_addr(&full[s], 0);
                     if (kt < kts) {
-                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (C::STAGE_BYTES - (p.meta_tma ? 0 : NBLK * C::E_BYTES)));
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (C::STAGE_BYTES - (META_TMA ? 0 : NBLK * C::E_BYTES)));
 #pragma unroll
                         for (int blk = 0; blk < NBLK; ++blk) {
                             tma_load_2d_pair(a + blk * C::A_BYTES, &tmA, lead_full, kt * 128, m0[blk]);
-                            if (p.meta_tma) tma_load_2d_pair(e + blk * C::E_BYTES, &tmE, lead_full, kt * 16, m0[blk]);
+                            if (META_TMA) tma_load_2d_pair(e + blk * C::E_BYTES, &tmE, lead_full, kt * 16, m0[blk]);
                         }
                         tma_load_2d_pair(b, &tmB, lead_full, kt * 256, n0);
                         tma_load_2d_pair(b + C::B_PANEL, &tmB, lead_full, kt * 256 + 128, n0);
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(384, 1)
                     if (!mbar_wait_warp(&acc_empty[blk], (it & 1) ^ 1, abort_flag)) goto done;
                 tc_fence_after();
                 for (int kt = 0; kt < kts; ++kt) {
-                    if (!mbar_wait_warp(&full[s], ph, abort_flag)) goto done;
+                    if (!(META_TMA ? mbar_wait_warp(&full[s], ph, abort_flag) : mbar_wait_codes(&full[s], ph, abort_flag))) goto done;
                     tc_fence_after();
                     const uint64_t off = (uint64_t)((s * C::STAGE_BYTES) >> 4);
                     const uint32_t ecol = tmem_base + C::E_COL + 8 * NBLK * s;
@@ -254,6 +258,8 @@ __global__ void __launch_bounds__(384, 1)
                     }
                 }
             }
+        } else if (!META_TMA) {
+            if (!q8_relay_codes<NS>(codes, full, lane, pair, num_pairs, p.num_work, kts + adp_kts, abort_flag)) goto done;
         }
     } else if (warp < 10) {
         // ------------------------------------------------------------ epilogue (both CTAs)
@@ -351,9 +357,10 @@ __global__ void __launch_bounds__(384, 1)
                 __syncwarp();  // every lane has read the tile before the next chunk overwrites it
             }
         }
-    } else if (!p.meta_tma) {
+    } else if (!META_TMA) {
         // ------------------------------------------------------------ code loaders (both CTAs)
-        // LAG stages of copies stay in flight: a stage is published once those of the next are issued
+        // LAG stages of copies stay in flight: a stage is published once those of the next are issued, or sooner while
+        // the next stage is not free yet (2458 tokens, 27200 -> 5824: 263 us, 294 if it always waits for that)
         const int blk = warp - 10;
         constexpr int LAG = 1;
         int s = 0, issued = 0, published = 0;
@@ -361,10 +368,7 @@ __global__ void __launch_bounds__(384, 1)
         auto publish = [&]() {
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                if (rank == 0) mbar_arrive(&full[published % NS]);
-                else mbar_arrive_cluster(cluster_addr(&full[published % NS], 0));
-            }
+            if (lane == 0) mbar_arrive(rank == 0 ? &full[published % NS] : &codes[published % NS]);
             ++published;
         };
         for (int w = pair; w < p.num_work; w += num_pairs) {
@@ -372,6 +376,10 @@ __global__ void __launch_bounds__(384, 1)
             grouped_tile(w, p.m_tiles, p.n_tiles, p.raster_g, mt, nt);
             const int m0 = min(mt * C::TILE_M + 256 * blk + 128 * (int)rank, p.M - 128);
             for (int kt = 0; kt < kts + adp_kts; ++kt) {
+                if (published < issued && !__all_sync(0xffffffffu, mbar_test(&empty[s], ph ^ 1))) {
+                    cp_async_wait<0>();
+                    publish();
+                }
                 if (!mbar_wait_warp(&empty[s], ph ^ 1, abort_flag)) {
                     cp_async_wait<0>();
                     goto done;
@@ -380,7 +388,7 @@ __global__ void __launch_bounds__(384, 1)
                     q8_copy_codes(smem + s * C::STAGE_BYTES + NBLK * C::A_BYTES + 2 * C::B_PANEL + blk * C::E_BYTES, p.meta, p.M, p.K,
                                   m0, kt, lane);
                 cp_async_commit();
-                if (++issued > LAG) {
+                if (++issued - published > LAG) {
                     cp_async_wait<LAG>();
                     publish();
                 }

@@ -82,6 +82,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // About 2 s at the B200's clocks: far above any legitimate wait in these
 // kernels (a whole launch takes milliseconds), far below a hung GPU.
 constexpr long long kWaitLimitCycles = 4000000000LL;
@@ -384,15 +397,25 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_ptr, uint32_t v)
 }
 // Arrive on an mbarrier given by its shared::cluster address (possibly the
 // peer's), with the instruction's default (CTA-scope release) semantics.
-// What the arrive publishes here is TMEM or shared-memory state already
-// ordered by a tcgen05 fence or an async-proxy completion, so a cluster-scope
-// release, which costs about a TMA round trip, buys nothing.
+// For TMEM or shared-memory state already ordered by a tcgen05 fence or an
+// async-proxy completion, where a cluster-scope release, which costs about a
+// TMA round trip, buys nothing.  Plain writes to shared memory that the peer
+// will act on (codes that the leader's tcgen05.cp reads from both CTAs) take
+// mbar_arrive_cluster_rel and mbar_wait_codes.  The release waits for all that
+// its warp has in flight, so it is a warp's that loads nothing.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 // The same with cluster-scope release semantics.
 __device__ __forceinline__ void mbar_arrive_cluster_rel(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// The pair leader's wait, by its whole MMA warp, for codes that warps of both
+// CTAs wrote with plain stores: with cluster-scope acquire, as the leader's
+// tcgen05.cp reads the peer's shared memory too.  (The proxy fence that such
+// a read needs on the path from the stores is the writers'.)
+__device__ __forceinline__ bool mbar_wait_codes(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort_flag));
 }
 // TMA load into this CTA's shared memory whose completion is counted on the
 // barrier at `cluster_bar` (the pair leader's), for the paired MMA.  No multicast.

@@ -1828,7 +1828,7 @@ int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, 
 
 namespace {
 // ------------------------------------------------------------------ int8 sparse product
-constexpr int Q8_WIDE_SLOT = 42, Q8_PAIR_SLOT = 43, Q8_TILE_SLOT = 44;  // entries in launch_clusters' table (the tiles': 32)
+constexpr int Q8_WIDE_SLOT = 42, Q8_PAIR_SLOT = 43, Q8_TILE_SLOT = 46;  // entries in launch_clusters' table (codes not by TMA: 2 on; the tiles': 32)
 constexpr int64_t Q8_MAX_K = 131072;  // 128 * 128 * K / 2 stays below 2^31
 
 struct Q8Plan {
@@ -1981,24 +1981,24 @@ int q8_product(const int8_t *X, const float *xscale, const int8_t *W, const floa
         wp.n_tiles = (p.T + C::BN - 1) / C::BN;
         wp.raster_g = wide_raster_group(wp.m_tiles, d.sms);
         wp.num_work = wp.m_tiles * wp.n_tiles;
-        wp.meta_tma = p.meta_tma;
         wp.meta = meta;
         wp.xscale = xscale;
         wp.wscale = wscale;
         wp.Y = Y;
-        return launch_pairs(slope::q8_wide_kernel, Q8_WIDE_SLOT, 384, C::SMEM_BYTES, wp.num_work, d.sms, st, a, b, e, r2, xl, wp);
+        return p.meta_tma ? launch_pairs(slope::q8_wide_kernel<true>, Q8_WIDE_SLOT, 384, C::SMEM_BYTES, wp.num_work, d.sms, st, a, b, e, r2, xl, wp)
+                          : launch_pairs(slope::q8_wide_kernel<false>, Q8_WIDE_SLOT + 2, 384, C::SMEM_BYTES, wp.num_work, d.sms, st, a, b, e, r2, xl, wp);
     }
     if (plan.bn == 256) {
         using C = slope::Q8PairCfg;
         slope::Q8PairParams pp{p.M, p.T, p.K, p.r};
         pp.n_tiles = (p.T + C::BN - 1) / C::BN;
         pp.num_work = (p.M + 255) / 256 * pp.n_tiles;
-        pp.meta_tma = p.meta_tma;
         pp.meta = meta;
         pp.xscale = xscale;
         pp.wscale = wscale;
         pp.Y = Y;
-        return launch_pairs(slope::q8_pair_kernel, Q8_PAIR_SLOT, 384, C::SMEM_BYTES, pp.num_work, d.sms, st, a, b, e, r2, xl, pp);
+        return p.meta_tma ? launch_pairs(slope::q8_pair_kernel<true>, Q8_PAIR_SLOT, 384, C::SMEM_BYTES, pp.num_work, d.sms, st, a, b, e, r2, xl, pp)
+                          : launch_pairs(slope::q8_pair_kernel<false>, Q8_PAIR_SLOT + 2, 384, C::SMEM_BYTES, pp.num_work, d.sms, st, a, b, e, r2, xl, pp);
     }
     switch (plan.bn) {
         case 16: return launch_q8_tile<16>(a, b, e, r2, xl, p, d.sms, st);

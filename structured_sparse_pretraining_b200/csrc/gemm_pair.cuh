@@ -69,7 +69,7 @@ struct PairCfg {
     static constexpr int TMEM_COLS = 512;
     static constexpr int BAR_BYTES = 1024;
     static constexpr int SMEM_BYTES = NS * STAGE_BYTES + NE * E_BYTES + STAGING_BYTES + ADP_BYTES + BAR_BYTES + 1024;
-    static_assert(BAR_BYTES >= 8 * (2 * 8 + NE + 2 * (NE / CB) + 6) + 8, "barrier area");
+    static_assert(BAR_BYTES >= 8 * (2 * 8 + NE + 3 * (NE / CB) + 6) + 8, "barrier area");
     static_assert(BNH * 64 <= ADP_BYTES - ADP_A_BYTES, "adapter buffer");
     static_assert(NE % CB == 0, "code batches");
     static_assert(2 * BN + 4 * NE <= TMEM_COLS, "TMEM budget");
@@ -219,6 +219,25 @@ __device__ __forceinline__ void pair_unit(const GemmParams &p, int w, int &mt, i
     }
 }
 
+// The peer's lane images are plain stores of its code writers, and the leader's
+// tcgen05.cp reads them: its MMA warp, which has nothing else to do, passes
+// their arrivals (`mpeer`) on to the leader's `mfull` with cluster-scope
+// release, which the leader's wait acquires.  Each release takes a memory
+// round trip.  By the relay that shows little, since the code ring runs ahead;
+// by the writers themselves, who then stop, it shows (four OPT-66B-shaped
+// layers forward at one token: 288 against 349 us; batches of two slots 325, of
+// six 305).
+template <int NB>
+__device__ __forceinline__ bool relay_codes(uint64_t *mpeer, uint64_t *mfull, int batches, volatile int *abort_flag) {
+    uint32_t ph = 0;
+    for (int i = 0, b = 0; i < batches; ++i) {
+        if (!mbar_wait(&mpeer[b], ph, abort_flag)) return false;
+        mbar_arrive_cluster_rel(cluster_addr(&mfull[b], 0));
+        if (++b == NB) { b = 0; ph ^= 1; }
+    }
+    return true;
+}
+
 template <bool A2_MN, int BN, bool SPLIT>
 __global__ void __launch_bounds__(352, 1)
     sp_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -239,8 +258,9 @@ __global__ void __launch_bounds__(352, 1)
     uint64_t *empty = full + NS;        // each CTA: operand stage s may be refilled
     uint64_t *efull = empty + NS;       // each CTA: raw code tile of slot e is in shared memory
     uint64_t *eempty = efull + NE;      // each CTA: code batch b (shared memory + TMEM) may be refilled
-    uint64_t *mfull = eempty + NB;      // leader: both CTAs' lane images of batch b are ready (8 arrivals)
-    uint64_t *acc_full = mfull + NB;    // each CTA: accumulator ready
+    uint64_t *mfull = eempty + NB;      // leader: both CTAs' lane images of batch b are ready (4 arrivals and the relay's)
+    uint64_t *mpeer = mfull + NB;       // peer: its lane images of batch b are ready (4 arrivals)
+    uint64_t *acc_full = mpeer + NB;    // each CTA: accumulator ready
     uint64_t *acc_empty = acc_full + 2;  // leader: both CTAs drained the accumulator (8 arrivals)
     uint64_t *adp_full = acc_empty + 2;  // leader: both CTAs' adapter tiles are in shared memory
     uint64_t *adp_empty = adp_full + 1;  // each CTA: the adapter buffer may be refilled
@@ -259,7 +279,8 @@ __global__ void __launch_bounds__(352, 1)
         for (int e = 0; e < NE; ++e) mbar_init(&efull[e], 1);
         for (int bb = 0; bb < NB; ++bb) {
             mbar_init(&eempty[bb], 1);
-            mbar_init(&mfull[bb], 8);
+            mbar_init(&mfull[bb], 5);
+            mbar_init(&mpeer[bb], 4);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&acc_full[a], 1);
@@ -389,7 +410,7 @@ __global__ void __launch_bounds__(352, 1)
                 for (int kt = k0; kt < k1; ++kt, ++j) {
                     const int bb = e / CB;
                     if (e % CB == 0) {  // first slot of a batch: its lane images must be ready
-                        if (!mbar_wait(&mfull[bb], (bph >> bb) & 1u, abort_flag)) goto done;
+                        if (!mbar_wait_cluster(&mfull[bb], (bph >> bb) & 1u, abort_flag)) goto done;
                         bph ^= 1u << bb;
                     }
                     if (!mbar_wait(&full[s], ph, abort_flag)) goto done;
@@ -435,6 +456,8 @@ __global__ void __launch_bounds__(352, 1)
                 mma_commit_pair_both(&acc_full[acc]);
                 ++it;
             }
+        } else if (rank != 0 && lane == 0) {
+            if (!relay_codes<NB>(mpeer, mfull, (my_ktiles + CB - 1) / CB, abort_flag)) goto done;
         }
     } else if (warp < 6) {
         // ------------------------------------------------------------ epilogue (both CTAs)
@@ -558,10 +581,7 @@ __global__ void __launch_bounds__(352, 1)
                 fence_proxy_async_smem();  // visible to tcgen05.cp
                 if (e % CB == CB - 1 || j == my_ktiles - 1) {  // batch complete: publish it to the MMA issuer
                     __syncwarp();
-                    if (lane == 0) {
-                        if (rank == 0) mbar_arrive(&mfull[e / CB]);
-                        else mbar_arrive_cluster(cluster_addr(&mfull[e / CB], 0));
-                    }
+                    if (lane == 0) mbar_arrive(rank == 0 ? &mfull[e / CB] : &mpeer[e / CB]);
                 }
                 if (++e == NE) { e = 0; eph ^= 1; }
             }

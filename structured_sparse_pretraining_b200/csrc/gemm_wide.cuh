@@ -63,7 +63,9 @@ struct WideCfg {
     static constexpr int E_BYTES = 2048;         // one block's code tile: 128 rows x 16 bytes
     static constexpr int ESLOT_BYTES = NBLK * E_BYTES;
     static constexpr int NE = 8;                 // code slots (k-tiles), 4 TMEM columns per block each
-    static constexpr int CB = 4;                 // slots handed over per batch
+    // Slots handed over per batch: four, half the ring, leave less time for a batch's refill and hand-over than they
+    // take (2048 tokens, four OPT-66B-shaped layers: 2.26 ms with four, 2.08 to 2.16 with two, 2.45 with one).
+    static constexpr int CB = 2;
     static constexpr int STAGING_BYTES = 4 * 2048;
     static constexpr int META_COL = NBLK * BN;   // 448
     static constexpr int TMEM_COLS = 512;
@@ -71,7 +73,7 @@ struct WideCfg {
     static constexpr int SMEM_BYTES = NS * STAGE_BYTES + NE * ESLOT_BYTES + STAGING_BYTES + BAR_BYTES + 1024;
     static_assert(META_COL + 4 * NBLK * NE <= TMEM_COLS, "TMEM budget");
     static_assert(NE % CB == 0, "code batches");
-    static_assert(BAR_BYTES >= 8 * (2 * NS + NE + 2 * (NE / CB) + 1 + NBLK) + 8, "barrier area");
+    static_assert(BAR_BYTES >= 8 * (2 * NS + NE + 3 * (NE / CB) + 1 + NBLK) + 8, "barrier area");
     static_assert(STAGE_BYTES % 1024 == 0 && B_PANEL % 1024 == 0 && ESLOT_BYTES % 1024 == 0, "alignment");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
@@ -107,8 +109,9 @@ __global__ void __launch_bounds__(352, 1)
     uint64_t *empty = full + NS;          // each CTA: stage s may be refilled
     uint64_t *efull = empty + NS;         // each CTA: both raw code tiles of slot e are in shared memory
     uint64_t *eempty = efull + NE;        // each CTA: code batch b may be refilled
-    uint64_t *mfull = eempty + NBAT;      // leader: both CTAs' lane images of batch b are ready (8 arrivals)
-    uint64_t *acc_full = mfull + NBAT;    // each CTA: the tile's accumulators are complete
+    uint64_t *mfull = eempty + NBAT;      // leader: both CTAs' lane images of batch b are ready (4 arrivals and the relay's)
+    uint64_t *mpeer = mfull + NBAT;       // peer: its lane images of batch b are ready (4 arrivals)
+    uint64_t *acc_full = mpeer + NBAT;    // each CTA: the tile's accumulators are complete
     uint64_t *acc_empty = acc_full + 1;   // leader, per block: both CTAs drained it (8 arrivals)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(acc_empty + NBLK);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
@@ -125,7 +128,8 @@ __global__ void __launch_bounds__(352, 1)
         for (int e = 0; e < NE; ++e) mbar_init(&efull[e], 1);
         for (int b = 0; b < NBAT; ++b) {
             mbar_init(&eempty[b], 1);
-            mbar_init(&mfull[b], 8);
+            mbar_init(&mfull[b], 5);
+            mbar_init(&mpeer[b], 4);
         }
         mbar_init(acc_full, 1);
         for (int b = 0; b < NBLK; ++b) mbar_init(&acc_empty[b], 8);
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(352, 1)
                 for (int kt = 0; kt < lead; ++kt) {
                     const int bb = e / CB;
                     if (e % CB == 0) {  // first slot of a batch: its lane images must be ready
-                        if (!mbar_wait(&mfull[bb], (bph >> bb) & 1u, abort_flag)) goto done;
+                        if (!mbar_wait_cluster(&mfull[bb], (bph >> bb) & 1u, abort_flag)) goto done;
                         bph ^= 1u << bb;
                     }
                     if (!mbar_wait(&full[s], ph, abort_flag)) goto done;
@@ -342,7 +346,7 @@ __global__ void __launch_bounds__(352, 1)
                 for (int kt = lead; kt < p.k_tiles_total; ++kt, ++j) {
                     const int bb = e / CB;
                     if (e % CB == 0) {  // first slot of a batch: its lane images must be ready
-                        if (!mbar_wait(&mfull[bb], (bph >> bb) & 1u, abort_flag)) goto done;
+                        if (!mbar_wait_cluster(&mfull[bb], (bph >> bb) & 1u, abort_flag)) goto done;
                         bph ^= 1u << bb;
                     }
                     if (!mbar_wait(&full[s], ph, abort_flag)) goto done;
@@ -390,6 +394,8 @@ __global__ void __launch_bounds__(352, 1)
 #pragma unroll
                 for (int blk = 0; blk < NBLK; ++blk) ++fills[blk];
             }
+        } else if (rank != 0 && lane == 0) {
+            if (!relay_codes<NBAT>(mpeer, mfull, (my_ktiles + CB - 1) / CB, abort_flag)) goto done;
         }
     } else if (warp < 6) {
         // ------------------------------------------------------------ epilogue (both CTAs)
@@ -573,10 +579,7 @@ __global__ void __launch_bounds__(352, 1)
                 fence_proxy_async_smem();  // visible to tcgen05.cp
                 if (e % CB == CB - 1 || j == my_ktiles - 1) {  // batch complete: publish it to the MMA issuer
                     __syncwarp();
-                    if (lane == 0) {
-                        if (rank == 0) mbar_arrive(&mfull[e / CB]);
-                        else mbar_arrive_cluster(cluster_addr(&mfull[e / CB], 0));
-                    }
+                    if (lane == 0) mbar_arrive(rank == 0 ? &mfull[e / CB] : &mpeer[e / CB]);
                 }
                 if (++e == NE) { e = 0; eph ^= 1; }
             }

@@ -32,6 +32,18 @@ def test_codes_of_the_peer_are_released_and_acquired_at_cluster_scope(name):
     assert relay.index("mbar_wait_warp(&codes[s]") < relay.index("mbar_arrive_cluster_rel(cluster_addr(&full[s], 0))")
 
 
+@pytest.mark.parametrize("name", ["gemm_pair.cuh", "gemm_wide.cuh"])
+def test_lane_images_of_the_peer_are_released_and_acquired_at_cluster_scope(name):
+    """The bf16 products' code tiles, rearranged in place by warps of both CTAs."""
+    text = source(name)
+    assert not re.search(r"mbar_arrive_cluster\w*\(cluster_addr\(&mfull\[e", text)
+    assert re.search(r"relay_codes<\w+>\(mpeer, mfull", text)
+    waits = re.findall(r"(mbar_wait\w*)\(&mfull\[", text)
+    assert waits and set(waits) == {"mbar_wait_cluster"}, waits
+    relay = re.search(r"bool relay_codes\(.*?\n}", source("gemm_pair.cuh"), re.S).group(0)
+    assert relay.index("mbar_wait(&mpeer[b]") < relay.index("mbar_arrive_cluster_rel(cluster_addr(&mfull[b], 0))")
+
+
 def test_the_helpers_name_the_cluster():
     text = source("ptx.cuh")
     body = lambda name: re.search(name + r"\(.*?\n}", text, re.S).group(0)  # noqa: E731

@@ -191,13 +191,19 @@ __device__ __forceinline__ uint32_t row_max_bits(uint32_t mx) {
     return NORM ? mx & 0x7FFFFFFFu : max(mx << 16, mx & 0xFFFF0000u);
 }
 
-// Sum of squares of h 2^-80, eight values (rows whose squares overflow binary32).
-__device__ __forceinline__ float scaled_squares(uint4 h, float s2) {
+// Rows whose mean square plus eps, m, leaves binary32's normal range (an
+// overflow, or with an eps below it) take their squares again, of h f with f a
+// power of two; 1 for all others.  An infinity in the row stays one.
+__device__ __forceinline__ float square_factor(float m) {
+    return __float_as_uint(m) == kInfBits ? 0x1p-80f : m < 0x1p-120f ? 0x1p80f : 1.0f;
+}
+// Sum of the squares of h f, eight values.
+__device__ __forceinline__ float scaled_squares(uint4 h, float f, float s2) {
     const uint32_t a[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const float2 u = bf16x2_to_float2(a[k]);
-        s2 = fmaf(u.x * 0x1p-80f, u.x * 0x1p-80f, fmaf(u.y * 0x1p-80f, u.y * 0x1p-80f, s2));
+        s2 = fmaf(u.x * f, u.x * f, fmaf(u.y * f, u.y * f, s2));
     }
     return s2;
 }
@@ -217,8 +223,6 @@ __device__ __forceinline__ void row_outputs(const RowParams &p, int64_t at, floa
     }
     if (p.Q) *reinterpret_cast<uint2 *>(p.Q + at) = !finite ? make_uint2(0, 0) : NORM ? quant8(v, q) : quant8_rows(v, q);
 }
-
-__device__ __forceinline__ float row_rstd(float ss, float inv_d, float eps) { return rsqrtf(fmaf(ss, inv_d, eps)); }
 
 // NORM: the norm; otherwise the quantiser.  WARP: a warp per row, otherwise a
 // CTA per row, held in registers.  H may be the buffer of X or res, and Y that
@@ -282,12 +286,12 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
 
     float rstd = 1.0f;
     if (NORM) {
-        if (__float_as_uint(ss) == kInfBits) {
-            // the squares overflow binary32: once more on h 2^-80 (an infinity
-            // in the row stays one, and gives rstd = 0 and NaN beside it)
+        const float m = fmaf(ss, inv_d, p.eps), f = square_factor(m);
+        rstd = rsqrtf(m);
+        if (f != 1.0f) {  // (an infinity in the row gives rstd = 0, and NaN beside it)
             float s2 = 0.0f;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) s2 = scaled_squares(h[i], s2);
+            for (int i = 0; i < NV; ++i) s2 = scaled_squares(h[i], f, s2);
             s2 = warp_sum(s2);
             if (!WARP) {
                 __syncthreads();  // every thread has read the first sums
@@ -295,9 +299,7 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
                 __syncthreads();
                 s2 = warp_sum(lane < (int)(blockDim.x >> 5) ? s_sum[lane] : 0.0f);
             }
-            rstd = row_rstd(s2, inv_d, 0.0f) * 0x1p-80f;
-        } else {
-            rstd = row_rstd(ss, inv_d, p.eps);
+            rstd = rsqrtf(fmaf(s2, inv_d, p.eps * f * f)) * f;
         }
         if (p.rstd && gi == 0 && in_bounds(row, 1, p.T)) p.rstd[row] = rstd;
     }
@@ -428,17 +430,18 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM, false), stream_ctas(N
         }
         float rstd = 1.0f;
         if (NORM) {
-            rstd = row_rstd(ss, inv_d, p.eps);
-            if (__float_as_uint(ss) == kInfBits) {  // see row_kernel
+            const float m = fmaf(ss, inv_d, p.eps), f = square_factor(m);
+            rstd = rsqrtf(m);
+            if (f != 1.0f) {
                 float s2 = 0.0f;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) s2 = scaled_squares(held[i], s2);
+                for (int i = 0; i < NV; ++i) s2 = scaled_squares(held[i], f, s2);
                 s2 = warp_sum(s2);
                 __syncthreads();
                 if (lane == 0) s_sum[turn][warp] = s2;
                 __syncthreads();
                 s2 = warp_sum(lane < nw ? s_sum[turn][lane] : 0.0f);
-                rstd = row_rstd(s2, inv_d, 0.0f) * 0x1p-80f;
+                rstd = rsqrtf(fmaf(s2, inv_d, p.eps * f * f)) * f;
             }
         }
         if (gi == 0) {

@@ -304,13 +304,14 @@ int slope_bwd_dw_masked_noalloc(const uint16_t *dY, const uint16_t *X, const uin
  * layer's products in a decoder block).  For each token row, D values:
  *     h = bf16(X + res)  (or X where res is NULL),  rstd = (mean h^2 + eps)^(-1/2),
  *     Y = bf16(h rstd w),
- *     Q = round(127 p / max|p|), ties to even, with p = h w (exact in binary32),
+ *     Q = round(127 p / max|p|), ties to even, with p = h w exactly,
  *     qscale = rstd max|p| / 127,  so that Q qscale stands for h rstd w in int8.
  * X, res, H, Y [T x D] bf16; w [D] bf16; Q [T x D] int8 in [-127, 127];
  * qscale, rstd [T] fp32.  H (the residual stream for the next block; only
  * with res), Y, rstd (for slope_rmsnorm_bwd) and Q with qscale may each be
  * NULL; one of Y and Q is required.  Q is decided exactly: it depends on h
- * and w alone, not on the rounding of rstd.
+ * and w alone, not on the rounding of rstd, nor on binary32's range: rows of
+ * products too small for it take binary64.
  * A row of zeros gives Q = 0 with qscale = 0.  A row in which some |h w| is
  * not finite in binary32 gives Q = 0 with qscale = NaN, so that
  * slope_fwd_q8's outputs for that token are NaN; its Y follows IEEE

@@ -6,9 +6,10 @@
 // one):  h = bf16(x + e),  rstd = (mean h^2 + eps)^(-1/2),
 //        y = bf16((h w) rstd),  and in int8  y ~ q s  with
 //        p = h w,  q = round(127 p / max|p|),  s = rstd max|p| / 127.
-// The factor rstd cancels in q: p is the product of two bf16 numbers and so
-// exact in binary32, and q is decided exactly (quant_exact), so that q does
-// not depend on how the sum of squares was ordered or rounded.
+// The factor rstd cancels in q: p is the product of two bf16 numbers, exact in
+// binary32 but at the ends of its range (see FAR_MAX), and q is decided exactly
+// (quant_exact), so that q does not depend on how the sum of squares was
+// ordered or rounded.
 //
 // Quantiser.  q = round(127 a / max|a|), s = max|a| / 127 for rows a of bf16
 // values: the kept weights of an output channel, or tokens no norm produced.
@@ -208,6 +209,28 @@ __device__ __forceinline__ float scaled_squares(uint4 h, float f, float s2) {
     return s2;
 }
 
+// Products of two bf16 numbers have 16 significant bits, so binary32, whose
+// last place is 2^-149, holds them down to 2^-134.  In a row whose largest
+// product is FAR_MAX or more, what it loses below quantises to zero.  In others
+// (rows of zeros apart) p is taken in binary64 times 2^200, which is exact and
+// in range: products of bf16 numbers start at 2^-266.
+// Y takes the products' low bits only where rstd is large enough to bring them
+// back above bf16's own smallest values (last place 2^-133): above FAR_RSTD
+// y = h w rstd is taken in binary64 as well.
+constexpr float FAR_MAX = 0x1p-110f, FAR_RSTD = 0x1p14f;
+__device__ __forceinline__ float2 far_products(uint32_t h, uint32_t w) {
+    const float2 x = bf16x2_to_float2(h), y = bf16x2_to_float2(w);
+    return make_float2((float)((double)x.x * y.x * 0x1p200), (float)((double)x.y * y.y * 0x1p200));
+}
+// Whether any of the eight products is not zero.
+__device__ __forceinline__ bool any_product(uint4 h, uint4 w) {
+    const uint32_t a[4] = {h.x, h.y, h.z, h.w}, b[4] = {w.x, w.y, w.z, w.w};
+    uint32_t any = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) any |= __vminu2(a[k] & 0x7FFF7FFFu, b[k] & 0x7FFF7FFFu);
+    return any != 0;
+}
+
 // Eight outputs of a row from its p (h w, or the quantiser's values): y = p rstd and the codes of p.
 template <bool NORM>
 __device__ __forceinline__ void row_outputs(const RowParams &p, int64_t at, float2 (&v)[4], float rstd, const QuantRow &q,
@@ -222,6 +245,67 @@ __device__ __forceinline__ void row_outputs(const RowParams &p, int64_t at, floa
         *reinterpret_cast<uint4 *>(p.Y + at) = make_uint4(y[0], y[1], y[2], y[3]);
     }
     if (p.Q) *reinterpret_cast<uint2 *>(p.Q + at) = !finite ? make_uint2(0, 0) : NORM ? quant8(v, q) : quant8_rows(v, q);
+}
+
+// The outputs of a row that takes binary64, by its warp or CTA (`group` threads
+// of which this is number gi; s_max: 32 words that nobody reads any more).  A
+// call that reads the row again, two values at a time, so that the other rows'
+// registers do not pay for it.  `mx`: the row's largest |p| as a float's bits.
+template <bool WARP>
+__device__ __noinline__ void far_row(const RowParams &p, int64_t row, int gi, int group, float rstd, uint32_t mx, uint32_t *s_max) {
+    const int64_t base = row * p.D, total = p.T * p.D;
+    const bool tiny = mx < __float_as_uint(FAR_MAX);
+    // Values 2 j and 2 j + 1 of this thread's chunks.  H, which it has written, may be the buffer of X or res.
+    auto load = [&](int j, uint32_t &h, uint32_t &w) {
+        h = w = 0;
+        if (!in_bounds(base + 2 * j, 2, total) || !in_bounds(2 * j, 2, p.D)) return;
+        w = *reinterpret_cast<const uint32_t *>(p.w + 2 * j);
+        h = *reinterpret_cast<const uint32_t *>((p.H ? p.H : p.X) + base + 2 * j);
+        if (p.res && !p.H) {
+            const float2 x = bf16x2_to_float2(h), e = bf16x2_to_float2(*reinterpret_cast<const uint32_t *>(p.res + base + 2 * j));
+            h = pack_bf16x2(x.x + e.x, x.y + e.y);
+        }
+    };
+    if (tiny) {
+        float most = 0.0f;
+#pragma unroll 1
+        for (int c = gi; c < p.D >> 3; c += group)
+#pragma unroll 1
+            for (int j = 4 * c; j < 4 * c + 4; ++j) {
+                uint32_t h, w;
+                load(j, h, w);
+                const float2 v = far_products(h, w);
+                most = fmaxf(most, fmaxf(fabsf(v.x), fabsf(v.y)));
+            }
+        mx = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+        if (!WARP) {
+            if ((gi & 31) == 0) s_max[gi >> 5] = mx;
+            __syncthreads();
+            mx = __reduce_max_sync(0xffffffffu, (gi & 31) < (group >> 5) ? s_max[gi & 31] : 0u);
+        }
+    }
+    const float pmax = __uint_as_float(mx);
+    const QuantRow q = quant_row(pmax);
+    if (p.Q && gi == 0 && in_bounds(row, 1, p.T))
+        p.qscale[row] = tiny ? (float)((double)rstd * pmax / 127.0 * 0x1p-200) : rstd * pmax / 127.0f;
+#pragma unroll 1
+    for (int c = gi; c < p.D >> 3; c += group)
+#pragma unroll 1
+        for (int j = 4 * c; j < 4 * c + 4; ++j) {
+            uint32_t h, w;
+            load(j, h, w);
+            const float2 x = bf16x2_to_float2(h), u = bf16x2_to_float2(w);
+            if (!in_bounds(base + 2 * j, 2, total)) continue;
+            if (p.Y)
+                *reinterpret_cast<uint32_t *>(p.Y + base + 2 * j) =
+                    pack_bf16x2((float)((double)x.x * u.x * rstd), (float)((double)x.y * u.y * rstd));
+            if (p.Q) {
+                const float2 v = __fmul2_rn(tiny ? far_products(h, w) : __fmul2_rn(x, u), both(q.f));
+                const int a = static_cast<int>(quant_exact(v.x, rintf(v.x * q.inv), q.pm));
+                const int b = static_cast<int>(quant_exact(v.y, rintf(v.y * q.inv), q.pm));
+                *reinterpret_cast<uint16_t *>(p.Q + base + 2 * j) = static_cast<uint16_t>((a & 0xFF) | (b & 0xFF) << 8);
+            }
+        }
 }
 
 // NORM: the norm; otherwise the quantiser.  WARP: a warp per row, otherwise a
@@ -304,6 +388,19 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
         if (p.rstd && gi == 0 && in_bounds(row, 1, p.T)) p.rstd[row] = rstd;
     }
     const bool finite = mx < kInfBits;
+    if (NORM && finite) {
+        bool far = rstd > FAR_RSTD;
+        if (mx < __float_as_uint(FAR_MAX)) {  // not for a row of zeros; in a CTA every thread has read the maxima, then
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) any |= any_product(h[i], weight(gi + i * gsize));
+            far = WARP ? __any_sync(0xffffffffu, any) : __syncthreads_or(any) != 0;
+        }
+        if (far) {
+            far_row<WARP>(p, row, gi, gsize, rstd, mx, s_max);
+            return;
+        }
+    }
     const float pmax = __uint_as_float(mx);
     const QuantRow q = quant_row(finite ? pmax : 0.0f);
     if (p.Q && gi == 0 && in_bounds(row, 1, p.T))
@@ -379,12 +476,15 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM, false), stream_ctas(N
     if (gi == 0)
         for (int s = 0; s < STREAM_STAGES; ++s) fetch(row0 + s * step, s);
     uint4 w[NV];
+    auto load_w = [&]() {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = gi + i * gsize;
-        w[i] = NORM && c < nchunk && in_bounds(8 * c, 8, p.D) ? __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c))
-                                                              : make_uint4(0, 0, 0, 0);
-    }
+        for (int i = 0; i < NV; ++i) {
+            const int c = gi + i * gsize;
+            w[i] = NORM && c < nchunk && in_bounds(8 * c, 8, p.D) ? __ldg(reinterpret_cast<const uint4 *>(p.w + 8 * c))
+                                                                  : make_uint4(0, 0, 0, 0);
+        }
+    };
+    load_w();
     const float inv_d = 1.0f / (float)p.D;
     int s = 0, turn = 0;
     uint32_t ph = 0;
@@ -449,10 +549,22 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM, false), stream_ctas(N
             fetch(row + STREAM_STAGES * step, s);
             if (NORM && p.rstd && in_bounds(row, 1, p.T)) p.rstd[row] = rstd;
         }
+        const bool finite = mx < kInfBits;
+        bool far = NORM && finite && rstd > FAR_RSTD;
+        if (NORM && mx < __float_as_uint(FAR_MAX)) {  // see row_kernel
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) any |= any_product(held[i], w[i]);
+            far = __syncthreads_or(any) != 0;
+        }
         ph ^= s;
         s ^= 1;
         turn ^= 1;  // the next row's sums go beside this row's, which other warps may still read
-        const bool finite = mx < kInfBits;
+        if (far) {
+            far_row<false>(p, row, gi, gsize, rstd, mx, s_max[turn ^ 1]);
+            load_w();  // rather than hold it across the call
+            continue;
+        }
         const float pmax = __uint_as_float(mx);
         const QuantRow q = quant_row(finite ? pmax : 0.0f);
         if (p.Q && gi == 0 && in_bounds(row, 1, p.T))

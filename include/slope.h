@@ -314,8 +314,8 @@ int slope_bwd_dw_masked_noalloc(const uint16_t *dY, const uint16_t *X, const uin
  * products too small for it take binary64.
  * A row of zeros gives Q = 0 with qscale = 0.  A row in which some |h w| is
  * not finite in binary32 gives Q = 0 with qscale = NaN, so that
- * slope_fwd_q8's outputs for that token are NaN; its Y follows IEEE
- * arithmetic.  Squares whose mean leaves binary32's normal range are summed
+ * slope_fwd_q8's outputs for that token are NaN; its Y is bf16(h rstd w) all
+ * the same, by IEEE arithmetic.  Squares whose mean leaves binary32's normal range are summed
  * scaled (and eps with them).
  * D a multiple of 8 up to 32768 (SLOPE_ERR_SHAPE), T >= 1, eps > 0 and
  * finite (SLOPE_ERR_ARG).  H and Y may be the buffers of X or res (the call

@@ -216,8 +216,13 @@ __device__ __forceinline__ float scaled_squares(uint4 h, float f, float s2) {
 // in range: products of bf16 numbers start at 2^-266.
 // Y takes the products' low bits only where rstd is large enough to bring them
 // back above bf16's own smallest values (last place 2^-133): above FAR_RSTD
-// y = h w rstd is taken in binary64 as well.
+// y = h w rstd is taken in binary64 as well.  So it is in a row with a product
+// that is not finite in binary32: y may be.
 constexpr float FAR_MAX = 0x1p-110f, FAR_RSTD = 0x1p14f;
+__device__ __forceinline__ bool far_candidate(uint32_t mx, float rstd) {  // mx: the largest |p| as a float's bits
+    const uint32_t least = __float_as_uint(FAR_MAX);
+    return mx - least >= kInfBits - least || rstd > FAR_RSTD;
+}
 __device__ __forceinline__ float2 far_products(uint32_t h, uint32_t w) {
     const float2 x = bf16x2_to_float2(h), y = bf16x2_to_float2(w);
     return make_float2((float)((double)x.x * y.x * 0x1p200), (float)((double)x.y * y.y * 0x1p200));
@@ -286,24 +291,25 @@ __device__ __noinline__ void far_row(const RowParams &p, int64_t row, int gi, in
     }
     const float pmax = __uint_as_float(mx);
     const QuantRow q = quant_row(pmax);
+    const double unit = tiny ? (double)q.f * 0x1p200 : (double)q.f;
     if (p.Q && gi == 0 && in_bounds(row, 1, p.T))
-        p.qscale[row] = tiny ? (float)((double)rstd * pmax / 127.0 * 0x1p-200) : rstd * pmax / 127.0f;
+        p.qscale[row] = mx >= kInfBits ? __uint_as_float(0x7FC00000u)
+                        : tiny         ? (float)((double)rstd * pmax / 127.0 * 0x1p-200) : rstd * pmax / 127.0f;
 #pragma unroll 1
     for (int c = gi; c < p.D >> 3; c += group)
 #pragma unroll 1
         for (int j = 4 * c; j < 4 * c + 4; ++j) {
             uint32_t h, w;
             load(j, h, w);
-            const float2 x = bf16x2_to_float2(h), u = bf16x2_to_float2(w);
             if (!in_bounds(base + 2 * j, 2, total)) continue;
-            if (p.Y)
-                *reinterpret_cast<uint32_t *>(p.Y + base + 2 * j) =
-                    pack_bf16x2((float)((double)x.x * u.x * rstd), (float)((double)x.y * u.y * rstd));
+            const float2 x = bf16x2_to_float2(h), u = bf16x2_to_float2(w);
+            const double px = (double)x.x * u.x, py = (double)x.y * u.y;
+            if (p.Y) *reinterpret_cast<uint32_t *>(p.Y + base + 2 * j) = pack_bf16x2((float)(px * rstd), (float)(py * rstd));
             if (p.Q) {
-                const float2 v = __fmul2_rn(tiny ? far_products(h, w) : __fmul2_rn(x, u), both(q.f));
-                const int a = static_cast<int>(quant_exact(v.x, rintf(v.x * q.inv), q.pm));
-                const int b = static_cast<int>(quant_exact(v.y, rintf(v.y * q.inv), q.pm));
-                *reinterpret_cast<uint16_t *>(p.Q + base + 2 * j) = static_cast<uint16_t>((a & 0xFF) | (b & 0xFF) << 8);
+                const float vx = (float)(px * unit), vy = (float)(py * unit);
+                const int a = static_cast<int>(quant_exact(vx, rintf(vx * q.inv), q.pm));
+                const int b = static_cast<int>(quant_exact(vy, rintf(vy * q.inv), q.pm));
+                *reinterpret_cast<uint16_t *>(p.Q + base + 2 * j) = static_cast<uint16_t>(mx < kInfBits ? (a & 0xFF) | (b & 0xFF) << 8 : 0);
             }
         }
 }
@@ -387,9 +393,8 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
         }
         if (p.rstd && gi == 0 && in_bounds(row, 1, p.T)) p.rstd[row] = rstd;
     }
-    const bool finite = mx < kInfBits;
-    if (NORM && finite) {
-        bool far = rstd > FAR_RSTD;
+    if (NORM && far_candidate(mx, rstd)) {
+        bool far = true;
         if (mx < __float_as_uint(FAR_MAX)) {  // not for a row of zeros; in a CTA every thread has read the maxima, then
             bool any = false;
 #pragma unroll
@@ -401,8 +406,12 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
             return;
         }
     }
+    const bool finite = NORM || mx < kInfBits;
     const float pmax = __uint_as_float(mx);
     const QuantRow q = quant_row(finite ? pmax : 0.0f);
+    // without this the compiler keeps the row's p across the reductions: 50 registers for 43 with two chunks a thread
+#pragma unroll
+    for (int i = 0; i < NV; ++i) asm volatile("" : "+r"(h[i].x), "+r"(h[i].y), "+r"(h[i].z), "+r"(h[i].w));
     if (p.Q && gi == 0 && in_bounds(row, 1, p.T))
         p.qscale[row] = finite ? rstd * pmax / 127.0f : __uint_as_float(0x7FC00000u);
 #pragma unroll
@@ -549,9 +558,8 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM, false), stream_ctas(N
             fetch(row + STREAM_STAGES * step, s);
             if (NORM && p.rstd && in_bounds(row, 1, p.T)) p.rstd[row] = rstd;
         }
-        const bool finite = mx < kInfBits;
-        bool far = NORM && finite && rstd > FAR_RSTD;
-        if (NORM && mx < __float_as_uint(FAR_MAX)) {  // see row_kernel
+        bool far = NORM && far_candidate(mx, rstd);
+        if (far && mx < __float_as_uint(FAR_MAX)) {  // see row_kernel
             bool any = false;
 #pragma unroll
             for (int i = 0; i < NV; ++i) any |= any_product(held[i], w[i]);
@@ -565,6 +573,7 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM, false), stream_ctas(N
             load_w();  // rather than hold it across the call
             continue;
         }
+        const bool finite = NORM || mx < kInfBits;
         const float pmax = __uint_as_float(mx);
         const QuantRow q = quant_row(finite ? pmax : 0.0f);
         if (p.Q && gi == 0 && in_bounds(row, 1, p.T))

@@ -108,3 +108,29 @@ def test_in_place_where_rows_are_read_again():
         want = ops.rmsnorm_q8(X, w, 1e-30, with_y=True)
         got = ops.rmsnorm_q8(X, w, 1e-30, Y=X)
         assert all(torch.equal(a, b) for a, b in zip(got[:3], want[:3]))
+
+
+@pytest.mark.parametrize("T,D", SHAPES)
+@pytest.mark.parametrize("res", [False, True])
+def test_products_above_the_range(T, D, res):
+    """h w overflows binary32, h rstd w does not: Y is that; in int8 the row has no scale."""
+    X = (P.random_bf16((T, D), 1.0, 1).double() * 2.0 ** 100).to(torch.bfloat16)
+    e = (P.random_bf16((T, D), 1.0, 2).double() * 2.0 ** 100).to(torch.bfloat16) if res else None
+    w = (P.random_bf16((D,), 1.0, 3).double() * 2.0 ** 40).to(torch.bfloat16)
+    X[1], X[2, 5] = 1.0, float("inf")
+    if res:
+        e[1] = 0.5
+    h, y, rstd, _, _ = P.norm(X, w, 1e-5, e)
+    for y_only in (True, False):
+        if y_only:
+            Y, H, rs = ops.rmsnorm(X, w, 1e-5, res=e, with_rstd=True)
+        else:
+            Q, s, Y, H, rs = ops.rmsnorm_q8(X, w, 1e-5, res=e, with_y=True, with_rstd=True)
+            assert torch.isnan(s[[0, 2]]).all() and not Q[[0, 2]].any() and torch.isfinite(s[1]) and Q[1].any()
+        rows = [i for i in range(T) if i != 2]
+        close(rs[rows], rstd[rows], rel(D) * rstd[rows], "rstd")
+        close(Y[rows], y[rows], (P.BF16 * 1.01 + 2 * rel(D)) * y[rows].abs(), "Y")
+        assert torch.isfinite(Y[rows].float()).all()
+        assert rs[2] == 0 and torch.isnan(Y[2, 5]) and not Y[2, :5].any()
+        if res:
+            assert torch.equal(H, h)

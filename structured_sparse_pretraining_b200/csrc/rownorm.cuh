@@ -294,7 +294,7 @@ __device__ __noinline__ void far_row(const RowParams &p, int64_t row, int gi, in
     const double unit = tiny ? (double)q.f * 0x1p200 : (double)q.f;
     if (p.Q && gi == 0 && in_bounds(row, 1, p.T))
         p.qscale[row] = mx >= kInfBits ? __uint_as_float(0x7FC00000u)
-                        : tiny         ? (float)((double)rstd * pmax / 127.0 * 0x1p-200) : rstd * pmax / 127.0f;
+                        : tiny         ? (float)((double)rstd * pmax / 127.0 * 0x1p-200) : rstd * (pmax / 127.0f);
 #pragma unroll 1
     for (int c = gi; c < p.D >> 3; c += group)
 #pragma unroll 1
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
 #pragma unroll
     for (int i = 0; i < NV; ++i) asm volatile("" : "+r"(h[i].x), "+r"(h[i].y), "+r"(h[i].z), "+r"(h[i].w));
     if (p.Q && gi == 0 && in_bounds(row, 1, p.T))
-        p.qscale[row] = finite ? rstd * pmax / 127.0f : __uint_as_float(0x7FC00000u);
+        p.qscale[row] = finite ? rstd * (pmax / 127.0f) : __uint_as_float(0x7FC00000u);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = gi + i * gsize;
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM, false), stream_ctas(N
         const float pmax = __uint_as_float(mx);
         const QuantRow q = quant_row(finite ? pmax : 0.0f);
         if (p.Q && gi == 0 && in_bounds(row, 1, p.T))
-            p.qscale[row] = finite ? rstd * pmax / 127.0f : __uint_as_float(0x7FC00000u);
+            p.qscale[row] = finite ? rstd * (pmax / 127.0f) : __uint_as_float(0x7FC00000u);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = gi + i * gsize;

@@ -134,3 +134,16 @@ def test_products_above_the_range(T, D, res):
         assert rs[2] == 0 and torch.isnan(Y[2, 5]) and not Y[2, :5].any()
         if res:
             assert torch.equal(H, h)
+
+
+@pytest.mark.parametrize("T,D", SHAPES)
+def test_scale_of_outputs_above_the_range(T, D):
+    """One value carries each row, so rstd h is about sqrt(D); with w near the end of the range h rstd w overflows, its
+    127th part, the scale, does not."""
+    X = torch.zeros(T, D, dtype=torch.bfloat16, device="cuda")
+    X[:, 3] = 2.0
+    w = torch.full((D,), 2.0 ** 126, device="cuda").to(torch.bfloat16)
+    Q, s, _, _, _ = ops.rmsnorm_q8(X, w, 1e-5)
+    _, _, _, q, qs = P.norm(X, w, 1e-5)
+    assert torch.equal(Q, q) and torch.isfinite(s).all()
+    close(s, qs, (rel(D) + 3 * F32) * qs, "qscale")

@@ -385,9 +385,10 @@ __global__ void __launch_bounds__(Q8Cfg<BN>::THREADS, 1)
                     for (int j = 0; j < W; ++j) ai[j] += src[j * 128];
                 }
                 float v[W];
+                // the scales one by one, as their product may leave the range
 #pragma unroll
                 for (int j = 0; j < W; ++j)
-                    v[j] = fmaf((float)(int)ai[j], xs[c + j] * ws, p.r > 0 ? bits_to_f32(af[j]) : 0.0f);
+                    v[j] = fmaf((float)(int)ai[j] * ws, xs[c + j], p.r > 0 ? bits_to_f32(af[j]) : 0.0f);
                 q8_store(v, p, n0 + c, m0 + 32 * q, lane, row_ok);
             };
             using W8 = std::integral_constant<int, 8>;

@@ -221,15 +221,15 @@ __global__ void __launch_bounds__(384, 1)
                 xs[32 * cc + lane] = t < p.T && in_bounds(t, 1, p.T) ? __ldg(p.xscale + t) : 0.0f;
             }
             __syncwarp();
-            // 16 columns of integer sums to scaled fp32
+            // 16 columns of integer sums to scaled fp32 (the scales one by one, as their product may leave the range)
             auto scaled = [&](uint32_t (&v)[16], int h) {
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
                     const float4 x = *reinterpret_cast<const float4 *>(xs + 16 * h + j);
-                    v[j] = __float_as_uint((float)(int)v[j] * (x.x * ws));
-                    v[j + 1] = __float_as_uint((float)(int)v[j + 1] * (x.y * ws));
-                    v[j + 2] = __float_as_uint((float)(int)v[j + 2] * (x.z * ws));
-                    v[j + 3] = __float_as_uint((float)(int)v[j + 3] * (x.w * ws));
+                    v[j] = __float_as_uint((float)(int)v[j] * ws * x.x);
+                    v[j + 1] = __float_as_uint((float)(int)v[j + 1] * ws * x.y);
+                    v[j + 2] = __float_as_uint((float)(int)v[j + 2] * ws * x.z);
+                    v[j + 3] = __float_as_uint((float)(int)v[j + 3] * ws * x.w);
                 }
             };
             uint32_t out[NCH][16];  // bf16 pairs of neighbouring tokens, this lane's channel

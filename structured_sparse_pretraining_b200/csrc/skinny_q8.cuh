@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(32 * SQ8_WARPS) skinny_q8_kernel(const __grid_
             for (int t = 0; t < TB; ++t) {
                 if (t0 + t < p.T && in_bounds((int64_t)(t0 + t) * p.M + o0, SQ8_ROWS, (int64_t)p.T * p.M)) {
                     const float x = p.xscale[t0 + t];
-                    const uint32_t lo = pack_bf16x2(fmaf((float)acc[0][t], x * ws.x, ad[0][t]), fmaf((float)acc[1][t], x * ws.y, ad[1][t]));
-                    const uint32_t hi = pack_bf16x2(fmaf((float)acc[2][t], x * ws.z, ad[2][t]), fmaf((float)acc[3][t], x * ws.w, ad[3][t]));
+                    const uint32_t lo = pack_bf16x2(fmaf((float)acc[0][t] * ws.x, x, ad[0][t]), fmaf((float)acc[1][t] * ws.y, x, ad[1][t]));
+                    const uint32_t hi = pack_bf16x2(fmaf((float)acc[2][t] * ws.z, x, ad[2][t]), fmaf((float)acc[3][t] * ws.w, x, ad[3][t]));
                     *reinterpret_cast<uint2 *>(p.Y + (int64_t)(t0 + t) * p.M + o0) = make_uint2(lo, hi);
                 }
             }

@@ -371,7 +371,11 @@ int slope_quant_rows(const uint16_t *A, int64_t rows, int64_t K, int8_t *Q, floa
  * [out x in/16]; XL [T x r], R [r x out] bf16 as in slope_fwd (r = 0: no
  * adapter, both may be NULL); Y [T x out] bf16.  The int8 sums are exact in
  * 32-bit integers (so in is at most 131072, SLOPE_ERR_SHAPE), the adapter's
- * are fp32, and the two are joined and rounded once.  In binary32 a sum is
+ * are fp32, and their sum is rounded to bf16 once.  The forms of up to 128
+ * rows (slope_q8_plan) join the two in one addition; those of 256 and 512 rows
+ * accumulate the adapter onto the scaled sum, which then takes one more fp32
+ * rounding for each 16 of r (tensor cores may truncate: 2^-23 of the largest
+ * partial sum each).  In binary32 a sum is
  * multiplied by wscale first and by xscale then, so the scales' own product may
  * leave its range (a sum times wscale may not).  A NaN or infinite scale
  * reaches every output of its token or channel.  One launch (slope_q8_plan

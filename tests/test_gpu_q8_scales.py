@@ -46,3 +46,29 @@ def test_scales_whose_product_is_subnormal(T, K, M, r):
     want, tol = P.product(Xq, xs, Wq, ws, meta)
     # the last places of subnormals, bf16's 2^-133 and binary32's 2^-149
     assert ((Y.double() - want).abs() <= tol + 2.0 ** -134 + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("T,K,M,r", [(1, 512, 320, 256), (16, 256, 128, 256), (100, 832, 320, 256), (512, 4096, 5120, 256), (300, 4160, 9216, 128),
+                                     (3300, 832, 1984, 256), (2048, 2048, 4096, 256)])
+def test_adapter_that_cancels_the_sum(T, K, M, r):
+    """XL . R close to minus the int8 term, its parts spread over the whole rank: what is left shows every rounding.
+    The sum's part takes four roundings, and in the forms of 256 and 512 rows two units more for each 16 of the rank."""
+    Xq, Wq, meta, _, _ = operands(T, K, M, 0)
+    Xq = Xq[:r].repeat(-(-T // r), 1)[:T].contiguous()  # token t repeats token t % r
+    xs = torch.full((T,), 1.37 / 64, device="cuda")
+    ws = torch.rand(M, generator=torch.Generator().manual_seed(7)).cuda() * 0.01 + 0.001
+    main, _ = P.product(Xq, xs, Wq, ws, meta)
+    H = torch.ones(1, 1, dtype=torch.float64, device="cuda")
+    while H.shape[0] < r:  # Hadamard: rows of +-1, H H^T = r
+        H = torch.cat([torch.cat([H, H], 1), torch.cat([H, -H], 1)], 0)
+    base = torch.zeros(r, M, dtype=torch.float64, device="cuda")
+    base[:min(T, r)] = main[:r]
+    R = (-(H.t() @ base) / r).to(torch.bfloat16)
+    XL = H.to(torch.bfloat16).repeat(-(-T // r), 1)[:T].contiguous()
+    Y = ops.fwd_q8(Xq, xs, Wq, ws, meta, XL, R, M)
+    mags = XL.double().abs() @ R.double().abs()
+    want = main + XL.double() @ R.double()
+    assert want.abs().mean() < 0.02 * main.abs().mean(), "the terms cancel"
+    joined = ops.q8_plan(M, T, K, r)[0] <= 128
+    slack = (4 if joined else 4 + 2 * -(-r // 16)) * P.F32 * main.abs() + 2 * (r + 2) * P.F32 * mags
+    assert ((Y.double() - want).abs() <= P.BF16 * want.abs() + (1 + P.BF16) * slack).all()

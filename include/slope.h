@@ -319,7 +319,8 @@ int slope_bwd_dw_masked_noalloc(const uint16_t *dY, const uint16_t *X, const uin
  * scaled (and eps with them).
  * D a multiple of 8 up to 32768 (SLOPE_ERR_SHAPE), T >= 1, eps > 0 and
  * finite (SLOPE_ERR_ARG).  H and Y may be the buffers of X or res (the call
- * may run in place).  One launch, no workspace; bit-reproducible.
+ * may run in place); any other overlap of an output with an input or another
+ * output is SLOPE_ERR_ARG.  One launch, no workspace; bit-reproducible.
  */
 int slope_rmsnorm(const uint16_t *X, const uint16_t *res, const uint16_t *w, int64_t T, int64_t D, float eps, uint16_t *H,
                   uint16_t *Y, int8_t *Q, float *qscale, float *rstd, void *stream);
@@ -332,7 +333,8 @@ int slope_rmsnorm(const uint16_t *X, const uint16_t *res, const uint16_t *w, int
  * dY, H, dres, dH [T x D] bf16 (dres, the gradient that reaches h along the
  * residual stream, may be NULL); w [D] bf16; rstd [T], dw [D] fp32
  * (overwritten).  dH is the gradient of both X and res.  dH may be the buffer
- * of dres; it must not overlap dY or H (SLOPE_ERR_ARG).  ws: scratch of at
+ * of dres; any other overlap of dH, dw or ws with an input or each other is
+ * SLOPE_ERR_ARG.  ws: scratch of at
  * least slope_rmsnorm_bwd_ws(T, D) floats on the device, the caller's (so calls
  * with their own ws may overlap); less is SLOPE_ERR_SHAPE, and none is needed
  * (ws may be NULL) where that is 0.  Its contents do not matter before and
@@ -357,7 +359,8 @@ int slope_rmsnorm_bwd_ws(int64_t T, int64_t D, int64_t *floats);
  * they are.  Applied to tokens it gives its tokens where no slope_rmsnorm
  * made them.  A row of zeros gives Q = 0, scale = 0; a row with a NaN or an
  * infinity gives Q = 0, scale = NaN.  K a multiple of 8 up to 65536
- * (SLOPE_ERR_SHAPE), rows >= 1.  One launch, no workspace.
+ * (SLOPE_ERR_SHAPE), rows >= 1.  Outputs that overlap A or each other are
+ * SLOPE_ERR_ARG.  One launch, no workspace.
  */
 int slope_quant_rows(const uint16_t *A, int64_t rows, int64_t K, int8_t *Q, float *scale, void *stream);
 
@@ -378,7 +381,8 @@ int slope_quant_rows(const uint16_t *A, int64_t rows, int64_t K, int8_t *Q, floa
  * partial sum each).  In binary32 a sum is
  * multiplied by wscale first and by xscale then, so the scales' own product may
  * leave its range (a sum times wscale may not).  A NaN or infinite scale
- * reaches every output of its token or channel.  One launch (slope_q8_plan
+ * reaches every output of its token or channel.  Y may not overlap an input
+ * (SLOPE_ERR_ARG).  One launch (slope_q8_plan
  * says of which form) and no workspace: calls may overlap on any streams;
  * bit-reproducible.
  */

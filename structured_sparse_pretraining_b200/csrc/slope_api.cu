@@ -12,6 +12,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/slope.h"
@@ -1584,6 +1585,27 @@ int check_width(int64_t v, int64_t most, const char *name) {
     return SLOPE_OK;
 }
 
+// A call's buffers, for what its outputs may not overlap.  `same`: this output
+// may also be just that input, element for element.
+struct Buffer {
+    const char *name;
+    const void *p;
+    int64_t bytes;
+};
+bool overlap(const Buffer &a, const Buffer &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+int check_apart(const char *call, const Buffer &out, std::initializer_list<Buffer> others, std::initializer_list<const void *> same = {}) {
+    for (const Buffer &o : others) {
+        if (!overlap(out, o)) continue;
+        bool ok = false;
+        for (const void *s : same) ok |= s == out.p && o.p == s && o.bytes == out.bytes;
+        if (!ok) return fail(SLOPE_ERR_ARG, "%s: %s overlaps %s", call, out.name, o.name);
+    }
+    return SLOPE_OK;
+}
+
 // How a row of D values is laid over threads: one warp's up to 1024 values
 // (NV 16-byte chunks per lane), one CTA's above.
 struct RowPlan {
@@ -1743,6 +1765,16 @@ int slope_rmsnorm(const uint16_t *X, const uint16_t *res, const uint16_t *w, int
     if (int rc = check_tokens(T)) return rc;
     if (int rc = check_width(D, NORM_MAX_D, "D")) return rc;
     if (!(eps > 0.0f) || !std::isfinite(eps)) return fail(SLOPE_ERR_ARG, "rmsnorm: eps must be positive and finite");
+    const int64_t n = T * D;
+    const Buffer bx{"X", X, 2 * n}, be{"res", res, 2 * n}, bw{"w", w, 2 * D}, bh{"H", H, 2 * n}, by{"Y", Y, 2 * n}, bq{"Q", Q, n},
+        bs{"qscale", Q ? qscale : nullptr, 4 * T}, br{"rstd", rstd, 4 * T};
+    if (int rc = check_apart("rmsnorm", bh, {bx, be}, {X, res})) return rc;
+    if (int rc = check_apart("rmsnorm", by, {bx, be}, {X, res})) return rc;
+    if (int rc = check_apart("rmsnorm", bh, {bw, by})) return rc;
+    if (int rc = check_apart("rmsnorm", by, {bw})) return rc;
+    if (int rc = check_apart("rmsnorm", bq, {bx, be, bw, bh, by})) return rc;
+    if (int rc = check_apart("rmsnorm", bs, {bx, be, bw, bh, by, bq})) return rc;
+    if (int rc = check_apart("rmsnorm", br, {bx, be, bw, bh, by, bq, bs})) return rc;
     DevInfo d;
     if (int rc = device_info(d)) return rc;
     slope::RowParams p{X, res, w, H, Y, Q, Q ? qscale : nullptr, rstd, T, (int)D, eps};
@@ -1756,6 +1788,9 @@ int slope_quant_rows(const uint16_t *A, int64_t rows, int64_t K, int8_t *Q, floa
     if (rows <= 0) return fail(SLOPE_ERR_ARG, "rows = %lld must be positive", (long long)rows);
     if (rows > (int64_t(1) << 30)) return fail(SLOPE_ERR_SHAPE, "rows = %lld too large", (long long)rows);
     if (int rc = check_width(K, QUANT_MAX_K, "K")) return rc;
+    const Buffer ba{"A", A, 2 * rows * K}, bq{"Q", Q, rows * K}, bs{"scale", scale, 4 * rows};
+    if (int rc = check_apart("quant_rows", bq, {ba})) return rc;
+    if (int rc = check_apart("quant_rows", bs, {ba, bq})) return rc;
     DevInfo d;
     if (int rc = device_info(d)) return rc;
     slope::RowParams p{A, nullptr, nullptr, nullptr, nullptr, Q, scale, nullptr, rows, (int)K, 0.0f};
@@ -1796,6 +1831,11 @@ int slope_rmsnorm_bwd(const uint16_t *dY, const uint16_t *H, const uint16_t *w, 
             return fail(SLOPE_ERR_SHAPE, "rmsnorm_bwd: ws holds %lld floats, %lld are needed (slope_rmsnorm_bwd_ws)",
                         (long long)ws_floats, (long long)(parts * D));
     }
+    const Buffer bg{"dY", dY, 2 * T * D}, bh{"H", H, 2 * T * D}, bw{"w", w, 2 * D}, br{"rstd", rstd, 4 * T}, be{"dres", dres, 2 * T * D},
+        bo{"dH", dH, 2 * T * D}, bd{"dw", dw, 4 * D}, bp{"ws", parts > 0 ? ws : nullptr, 4 * parts * D};
+    if (int rc = check_apart("rmsnorm_bwd", bo, {bw, br})) return rc;
+    if (int rc = check_apart("rmsnorm_bwd", bd, {bg, bh, bw, br, be, bo})) return rc;
+    if (int rc = check_apart("rmsnorm_bwd", bp, {bg, bh, bw, br, be, bo, bd})) return rc;
     DevInfo d;
     if (int rc = device_info(d)) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -2029,6 +2069,10 @@ int slope_fwd_q8(const int8_t *Xq, const float *xscale, const int8_t *vals_q, co
         CHECK_PTR(XL);
         CHECK_PTR(R);
     }
+    if (int rc = check_apart("fwd_q8", {"Y", Y, 2 * T * out},
+                             {{"Xq", Xq, T * in}, {"xscale", xscale, 4 * T}, {"vals_q", vals_q, out * (in / 2)}, {"wscale", wscale, 4 * out},
+                              {"meta", meta, out * (in / 8)}, {"XL", r > 0 ? XL : nullptr, 2 * T * r}, {"R", r > 0 ? R : nullptr, 2 * r * out}}))
+        return rc;
     return q8_product(Xq, xscale, vals_q, wscale, meta, XL, R, T, in, out, r, Y, static_cast<cudaStream_t>(stream));
 }
 

@@ -396,8 +396,9 @@ int slope_fwd_q8(const int8_t *Xq, const float *xscale, const int8_t *vals_q, co
  * device with `sms` SMs: rows = 0 (CUDA cores, a few tokens; bn = tokens per
  * pass, splits = warps that share the sum over K), 128 (tensor-core tiles of
  * 128 channels x bn tokens on clusters of `splits` CTAs that share it), 256 or
- * 512 (256 x 256 or 512 x 224 tiles on SM pairs, no split).  Sizes as slope_fwd_q8; returns
- * SLOPE_ERR_ARG for NULL outputs or bad sizes.
+ * 512 (256 x 256 or 512 x 224 tiles on SM pairs, no split).  Sizes, and the
+ * errors of bad ones, as slope_fwd_q8; SLOPE_ERR_ARG for NULL outputs or a
+ * number of SMs that is not positive.
  */
 int slope_q8_plan(int64_t M, int64_t T, int64_t K, int64_t r, int sms, int *rows, int *bn, int *splits);
 

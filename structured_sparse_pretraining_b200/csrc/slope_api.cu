@@ -1871,6 +1871,14 @@ namespace {
 constexpr int Q8_WIDE_SLOT = 42, Q8_PAIR_SLOT = 43, Q8_TILE_SLOT = 46;  // entries in launch_clusters' table (codes not by TMA: 2 on; the tiles': 32)
 constexpr int64_t Q8_MAX_K = 131072;  // 128 * 128 * K / 2 stays below 2^31
 
+int check_q8_sizes(int64_t T, int64_t in, int64_t out, int64_t r) {
+    if (int rc = check_tokens(T)) return rc;
+    if (int rc = check_features(in, "in")) return rc;
+    if (in > Q8_MAX_K) return fail(SLOPE_ERR_SHAPE, "in = %lld: int8 sums are exact up to %lld", (long long)in, (long long)Q8_MAX_K);
+    if (int rc = check_features(out, "out")) return rc;
+    return check_rank(r);
+}
+
 struct Q8Plan {
     int bn;      // 0: CUDA cores, else the token width of the tensor-core tile
     int splits;  // CTAs that share a tile's sum over K (or warps a group of channels, on CUDA cores)
@@ -2060,11 +2068,7 @@ int slope_fwd_q8(const int8_t *Xq, const float *xscale, const int8_t *vals_q, co
     CHECK_PTR(wscale);
     CHECK_PTR(meta);
     CHECK_PTR(Y);
-    if (int rc = check_tokens(T)) return rc;
-    if (int rc = check_features(in, "in")) return rc;
-    if (in > Q8_MAX_K) return fail(SLOPE_ERR_SHAPE, "in = %lld: int8 sums are exact up to %lld", (long long)in, (long long)Q8_MAX_K);
-    if (int rc = check_features(out, "out")) return rc;
-    if (int rc = check_rank(r)) return rc;
+    if (int rc = check_q8_sizes(T, in, out, r)) return rc;
     if (r > 0) {
         CHECK_PTR(XL);
         CHECK_PTR(R);
@@ -2077,8 +2081,8 @@ int slope_fwd_q8(const int8_t *Xq, const float *xscale, const int8_t *vals_q, co
 }
 
 int slope_q8_plan(int64_t M, int64_t T, int64_t K, int64_t r, int sms, int *rows, int *bn, int *splits) {
-    if (!rows || !bn || !splits || M <= 0 || T <= 0 || K <= 0 || r < 0 || sms <= 0)
-        return fail(SLOPE_ERR_ARG, "slope_q8_plan: NULL output or a size that is not positive");
+    if (!rows || !bn || !splits || sms <= 0) return fail(SLOPE_ERR_ARG, "slope_q8_plan: NULL output or sms that is not positive");
+    if (int rc = check_q8_sizes(T, K, M, r)) return rc;
     const Q8Plan p = pick_q8_plan(M, T, K, r, sms);
     *rows = p.wide ? 512 : p.bn == 0 ? 0 : p.bn == 256 ? 256 : 128;
     *bn = p.bn == 0 ? p.tb : p.bn;

@@ -111,6 +111,17 @@ def kernel_work(op, T, inn, out, r):
     raise KeyError(op)
 
 
+def sweep_peak_s(op, T, inn, out, r, p_dense, int8):
+    """Seconds an inference call's tensor work takes at peak (p_dense: dense bf16 TFLOP/s): in the bf16 sweep at the
+    2:4-sparse rate, twice dense; in the int8 sweep the int8 product at its own 2:4-sparse rate, four times dense bf16,
+    and the adapter's dense bf16 products at p_dense."""
+    flops = kernel_work(op, T, inn, out, r)[0]
+    if not int8:
+        return flops / (2e12 * p_dense)
+    main = 2.0 * T * inn * out if op == "fwd_q8" else 0.0
+    return main / (4e12 * p_dense) + (flops - main) / (1e12 * p_dense)
+
+
 OPS = ["prune24_double", "fwd_fused", "bwd_dx_fused", "bwd_dw_fused"]
 
 # The device function each entry point's dominant launch runs (the sparse
@@ -663,10 +674,12 @@ def run_fwd_sweep(args):
             for key, dt in markers.deltas():
                 per.setdefault(key, []).append(dt)
         ops.status_sync()
-        tot_bytes = tot_flops = 0.0
+        tot_bytes = tot_flops = peak_s = 0.0
         kernels = {}
         for (name, inn, out), times in per.items():
             fl, by = kernel_work(name, T, inn, out, r)
+            at_peak = sweep_peak_s(name, T, inn, out, r, p_dense, args.int8)
+            peak_s += at_peak
             tot_bytes += by
             tot_flops += fl
             avg = sum(times) / len(times)
@@ -676,13 +689,14 @@ def run_fwd_sweep(args):
                 bn, sp = ops.sparse_plan(out, T, inn, sms)
                 fused_one = fusable(out, T, inn, r, sms)
                 ent.update(tflops=round(fl / (avg * 1e-3) / 1e12, 2),
-                           frac_of_sparse_peak=round(fl / (avg * 1e-3) / 1e12 / (2 * p_dense), 4),
+                           frac_of_sparse_peak=round(at_peak / (avg * 1e-3), 4),
                            kernel=kernel_of(name, T, inn, out, r, sms),
                            launches=1 if fused_one else 2,
                            token_tile=224 if fused_one else bn, k_splits=1 if fused_one else sp)
             if name == "fwd_q8":
                 rows, bn, sp = ops.q8_plan(out, T, inn, r, sms)
-                ent.update(tflops=round(fl / (avg * 1e-3) / 1e12, 2), tile_rows=rows, token_tile=bn, k_splits=sp)
+                ent.update(tflops=round(fl / (avg * 1e-3) / 1e12, 2), frac_of_sparse_peak=round(at_peak / (avg * 1e-3), 4),
+                           tile_rows=rows, token_tile=bn, k_splits=sp)
             kernels[f"{name}[{inn}x{out}]"] = ent
         gbs = tot_bytes / (ms * 1e-3) / 1e9
         tflops = tot_flops / (ms * 1e-3) / 1e12
@@ -696,7 +710,7 @@ def run_fwd_sweep(args):
                                                 "l2": "flushed between timed steps (256 MiB write, untimed)"},
                 "frac_of_hbm": round(gbs / hbm, 4), "hbm_peak_gbs": hbm, "peak_source": peak_kind,
                 "bytes_per_step": tot_bytes, "tflops": round(tflops, 2),
-                "frac_of_sparse_peak": round(tflops / (2 * p_dense), 4), "gpu_launches": launches * args.steps,
+                "frac_of_sparse_peak": round(peak_s / (ms * 1e-3), 4), "gpu_launches": launches * args.steps,
                 "kernels": kernels, "clocks": clk.summary()}
         print(json.dumps(line), flush=True)
         del graph, graph_m

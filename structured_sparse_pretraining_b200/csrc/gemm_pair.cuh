@@ -54,10 +54,12 @@ struct PairCfg {
     static constexpr int B_BYTES = 2 * B_PANEL;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int E_BYTES = 2048;        // code tile: 128 rows x 16 bytes
-    // Depth of the code ring: as deep as TMEM allows (4 columns per slot next
-    // to two BN-column accumulators).  A shallow ring starves the MMA: a code
-    // tile passes TMA, the writers and a hand-over before the MMA can use it.
-    static constexpr int NE = 2 * BN + 48 <= 512 ? 12 : 8;
+    // Depth of the code ring (4 TMEM columns per slot next to two BN-column
+    // accumulators; 2 KB of shared memory).  A shallow ring starves the MMA: a
+    // code tile passes TMA, the writers and a hand-over before the MMA can use
+    // it.  The narrow tiles' k-tiles are the shortest: 282 us with 16 slots at
+    // one token on four OPT-66B-shaped layers, 289 with 12, 281 with 20 or 24.
+    static constexpr int NE = BN <= 64 ? 16 : 2 * BN + 48 <= 512 ? 12 : 8;
     static constexpr int CB = 4;                // code slots handed over per batch
     static constexpr int STAGING_BYTES = 4 * 2048;  // epilogue: one 32 x 32 bf16 transpose tile per warp
     // adapter tile of rank <= 32 (padded to 16 or 32): A2 128 x 32 and B2 BNH x 32 bf16
@@ -225,8 +227,8 @@ __device__ __forceinline__ void pair_unit(const GemmParams &p, int w, int &mt, i
 // release, which the leader's wait acquires.  Each release takes a memory
 // round trip.  By the relay that shows little, since the code ring runs ahead;
 // by the writers themselves, who then stop, it shows (four OPT-66B-shaped
-// layers forward at one token: 288 against 349 us; batches of two slots 325, of
-// six 305).
+// layers forward at one token, twelve slots: 288 against 349 us; batches of two
+// slots 325, of six 305).
 template <int NB>
 __device__ __forceinline__ bool relay_codes(uint64_t *mpeer, uint64_t *mfull, int batches, volatile int *abort_flag) {
     uint32_t ph = 0;

@@ -12,6 +12,7 @@ ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "slope_api.cu")
 LIB = os.path.join(HERE, "libslope.so")
 LIB_DEBUG = os.path.join(HERE, "libslope_debug.so")
+CALLS = os.path.join(HERE, "_calls.so")
 DEPS = [os.path.join(HERE, "csrc", f) for f in os.listdir(os.path.join(HERE, "csrc"))] + [
     os.path.join(ROOT, "include", "slope.h")]
 
@@ -39,21 +40,39 @@ def _build_one(lib: str, extra, force: bool, verbose: bool) -> str:
     return lib
 
 
+def calls_key() -> str:
+    """What a built _calls.so belongs to: this Python and this torch."""
+    import torch
+    return f"{sysconfig.get_config_var('SOABI')} {sys.hexversion:#x} torch {torch.__version__} {int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+
+
+def calls_current() -> bool:
+    """Whether _calls.so is there and was built for this Python and this torch."""
+    try:
+        with open(CALLS, "rb") as f:  # calls.cpp keeps its key as a string
+            return b"slope calls for " + calls_key().encode() + b"\0" in f.read()
+    except OSError:
+        return False
+
+
 def build_calls(force: bool = False) -> str:
     """Build _calls.so: Python's and torch's headers, no device code."""
-    src, lib = os.path.join(HERE, "csrc", "calls.cpp"), os.path.join(HERE, "_calls.so")
+    src, lib = os.path.join(HERE, "csrc", "calls.cpp"), CALLS
     deps = [src, os.path.join(ROOT, "include", "slope.h")]
-    if not force and os.path.exists(lib) and os.path.getmtime(lib) >= max(map(os.path.getmtime, deps)):
+    if not force and calls_current() and os.path.getmtime(lib) >= max(map(os.path.getmtime, deps)):
         return lib
     import torch
     home = os.path.dirname(torch.__file__)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     include = [sysconfig.get_paths()["include"], os.path.join(home, "include"),
                os.path.join(home, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
-    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f'-DSLOPE_CALLS_KEY="{calls_key()}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
            + [f"-isystem{d}" for d in include] + ["-o", lib, src, "-L" + os.path.join(home, "lib"),
                                                   "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"g++ not started ({e})") from e
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError("g++ failed building _calls.so")
@@ -62,17 +81,18 @@ def build_calls(force: bool = False) -> str:
 
 def build(force: bool = False, verbose: bool = False, debug: bool = True) -> str:
     """Build libslope.so and _calls.so (and, with debug=True, libslope_debug.so
-    beside them, in parallel); returns the release library's path."""
+    beside them, in parallel); returns the release library's path.  Without
+    torch's C++ headers or g++ the library is built all the same."""
     from concurrent.futures import ThreadPoolExecutor
     with ThreadPoolExecutor(3) as ex:
         calls = ex.submit(build_calls, force)
-        if not debug:
-            calls.result()
-            return _build_one(LIB, [], force, verbose)
         rel = ex.submit(_build_one, LIB, [], force, verbose)
-        dbg = ex.submit(_build_one, LIB_DEBUG, ["-DSLOPE_DEBUG_BOUNDS"], force, False)
-        dbg.result()
-        calls.result()
+        if debug:
+            ex.submit(_build_one, LIB_DEBUG, ["-DSLOPE_DEBUG_BOUNDS"], force, False).result()
+        try:
+            calls.result()
+        except (RuntimeError, ImportError) as e:  # the library itself needs nvcc alone
+            sys.stderr.write(f"_calls.so not built ({e}); the int8 path's calls go through ctypes without it\n")
         return rel.result()
 
 

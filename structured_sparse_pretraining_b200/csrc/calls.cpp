@@ -19,6 +19,9 @@
 #include <initializer_list>
 #include "../../include/slope.h"
 
+// What this was built for, as build.py looks for it.
+extern "C" __attribute__((used, visibility("default"))) const char slope_calls_key[] = "slope calls for " SLOPE_CALLS_KEY;
+
 namespace {
 
 // The entry points of the library that ops.py loaded (release or debug build).
@@ -45,7 +48,7 @@ struct Call {
     bool fits = true;
 
     explicit Call(const at::Tensor *first) {
-        fits = first && first->get_device() == c10::cuda::current_device();
+        fits = lib.rmsnorm && first && first->get_device() == c10::cuda::current_device();  // bound, and here
         if (fits) dev = first->get_device();
     }
     template <typename T>

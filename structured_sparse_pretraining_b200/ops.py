@@ -8,6 +8,7 @@ bf16 tensors are torch.bfloat16; the 16-bit position-code words ("meta") are
 torch.int16 tensors holding the uint16 patterns.
 """
 import ctypes
+import warnings
 
 import torch
 
@@ -267,17 +268,29 @@ def bwd_dw_masked_noalloc(dY, X, meta, dW_vals):
 # the module _calls (csrc/calls.cpp) when everything fits: 4.5 us of host time
 # for fwd_q8 where the way from here takes 10.1.  What does not fit (another
 # device than the current one, a subclass, an error) goes the way from here,
-# with its messages.
+# with its messages; so does everything where the module was not built.
 _calls = None
+
+
+class _NoCalls:
+    """Stands for the module _calls where there is none for this Python and torch: leaves every call."""
+    rmsnorm = rmsnorm_bwd = quant_rows = fwd_q8 = staticmethod(lambda *a: None)
 
 
 def _bind():
     """The module _calls, on the entry points of the loaded library."""
     global _calls
+    from . import build
     try:
+        if not build.calls_current():
+            raise ImportError("not built for this Python and torch")
         from . import _calls as calls
     except ImportError as e:
-        raise RuntimeError(f"_calls.so not built or not loadable ({e}); run structured_sparse_pretraining_b200/build.py") from e
+        warnings.warn(f"_calls.so is not used ({e}); the int8 path's small calls take twice the host time: run "
+                      "structured_sparse_pretraining_b200/build.py", RuntimeWarning, stacklevel=3)
+        _lib.load()
+        _calls = _NoCalls
+        return _calls
     lib = _lib.load()
     names = ("rmsnorm", "rmsnorm_bwd", "rmsnorm_bwd_ws", "quant_rows", "fwd_q8")
     calls.bind(*(ctypes.cast(getattr(lib, "slope_" + n), ctypes.c_void_p).value for n in names))

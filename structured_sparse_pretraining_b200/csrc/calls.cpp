@@ -4,7 +4,7 @@
 //
 // Each function takes the Python function's arguments in order and returns its
 // result; or None where anything does not fit (a type, a shape, a device that
-// is not the current one, a tensor subclass), which ops.py then does or refuses
+// is not the current one, a tensor subclass, a vector not on 16 bytes), which ops.py then does or refuses
 // the long way, with its messages; or, as an integer, the status that the
 // entry point returned.  By ctypes and Python's tensor attributes fwd_q8 took
 // 10.1 us, of which the entry point with its launch is 3.0.
@@ -58,7 +58,10 @@ struct Call {
             fits = false;
             return nullptr;
         }
-        return static_cast<T *>(t->data_ptr());
+        T *p = static_cast<T *>(t->data_ptr());
+        // an fp32 vector may be a slice, which ops.py copies
+        if (type == at::kFloat && (reinterpret_cast<uintptr_t>(p) & 15u)) fits = false;
+        return p;
     }
     // whether an output that the caller gave fits (None: one will be allocated)
     void given(PyObject *o, at::ScalarType type, std::initializer_list<int64_t> shape) {

@@ -267,7 +267,8 @@ def bwd_dw_masked_noalloc(dY, X, meta, dW_vals):
 # The calls below may be a few microseconds of GPU work each, so they go through
 # the module _calls (csrc/calls.cpp) when everything fits: 4.5 us of host time
 # for fwd_q8 where the way from here takes 10.1.  What does not fit (another
-# device than the current one, a subclass, an error) goes the way from here,
+# device than the current one, a subclass, a vector that does not start on 16
+# bytes, an error) goes the way from here,
 # with its messages; so does everything where the module was not built.
 _calls = None
 
@@ -335,6 +336,34 @@ def _out(t, dtype, name, shape, like, place):
     return t, _fit(t, dtype, name, shape, place[0])
 
 
+# fp32 vectors (scales, rstd, dw) may be slices, s[3:], that do not start on the
+# 16 bytes that the entry points ask of every tensor: such a one goes through a
+# copy of its own, one more small launch.
+def _vector(t, name, shape, dev):
+    """(vector, pointer) of an fp32 input, copied where it does not start on 16 bytes."""
+    p = _fit(t, torch.float32, name, shape, dev)
+    if p % 16:
+        t = t.clone()
+        p = t.data_ptr()
+    return t, p
+
+
+def _vector_out(t, name, shape, like, place, back):
+    """(vector, pointer) of an fp32 output; where the given one does not start on 16 bytes the pointer is that of a new
+    one, and `back` takes the two for _write_back."""
+    t, p = _out(t, torch.float32, name, shape, like, place)
+    if p % 16:
+        new = torch.empty_like(t)
+        back.append((t, new))
+        p = new.data_ptr()
+    return t, p
+
+
+def _write_back(back):
+    for t, new in back:
+        t.copy_(new)
+
+
 def _call_on(place, name, *args):
     """Call an entry point on the device of `place` (current or not) and that device's current stream."""
     dev, current = place
@@ -374,6 +403,7 @@ def _rmsnorm(X, w, eps, res, with_y, with_q8, with_rstd, H, Y, Q, qscale, rstd):
     dev, _ = place = _place(X)
     pw = _fit(w, torch.bfloat16, "w", (D,), dev)
     pe = ph = py = pq = ps = pr = None
+    back = []
     if res is not None:
         pe = _fit(res, torch.bfloat16, "res", shape, dev)
         H, ph = _out(H, torch.bfloat16, "H", shape, X, place)
@@ -383,10 +413,11 @@ def _rmsnorm(X, w, eps, res, with_y, with_q8, with_rstd, H, Y, Q, qscale, rstd):
         Y, py = _out(Y, torch.bfloat16, "Y", shape, X, place)
     if with_q8:
         Q, pq = _out(Q, torch.int8, "Q", shape, X, place)
-        qscale, ps = _out(qscale, torch.float32, "qscale", (T,), X, place)
+        qscale, ps = _vector_out(qscale, "qscale", (T,), X, place, back)
     if with_rstd or rstd is not None:
-        rstd, pr = _out(rstd, torch.float32, "rstd", (T,), X, place)
+        rstd, pr = _vector_out(rstd, "rstd", (T,), X, place, back)
     _call_on(place, "slope_rmsnorm", X.data_ptr(), pe, pw, T, D, eps, ph, py, pq, ps, pr)
+    _write_back(back)
     return Q, qscale, Y, H, rstd
 
 
@@ -401,13 +432,15 @@ def rmsnorm_bwd(dY, H, w, rstd, dres=None, dH=None, dw=None):
     dev, _ = place = _place(dY)
     ph = _fit(H, torch.bfloat16, "H", shape, dev)
     pw = _fit(w, torch.bfloat16, "w", (D,), dev)
-    pr = _fit(rstd, torch.float32, "rstd", (T,), dev)
+    rstd, pr = _vector(rstd, "rstd", (T,), dev)
     pe = None if dres is None else _fit(dres, torch.bfloat16, "dres", shape, dev)
     dH, pdh = _out(dH, torch.bfloat16, "dH", shape, dY, place)
-    dw, pdw = _out(dw, torch.float32, "dw", (D,), dY, place)
+    back = []
+    dw, pdw = _vector_out(dw, "dw", (D,), dY, place, back)
     floats = _norm_bwd_floats(T, D)
     ws, pws = _out(None, torch.float32, "ws", (floats,), dY, place) if floats else (None, None)
     _call_on(place, "slope_rmsnorm_bwd", dY.data_ptr(), ph, pw, pr, pe, T, D, pdh, pdw, pws, floats)
+    _write_back(back)
     return dH, dw
 
 
@@ -420,8 +453,10 @@ def quant_rows(A, Q=None, scale=None):
     shape = rows, K = tuple(_rows(A, torch.bfloat16, "A"))
     place = _place(A)
     Q, pq = _out(Q, torch.int8, "Q", shape, A, place)
-    scale, ps = _out(scale, torch.float32, "scale", (rows,), A, place)
+    back = []
+    scale, ps = _vector_out(scale, "scale", (rows,), A, place, back)
     _call_on(place, "slope_quant_rows", A.data_ptr(), rows, K, pq, ps)
+    _write_back(back)
     return Q, scale
 
 
@@ -435,9 +470,9 @@ def fwd_q8(Xq, xscale, vals_q, wscale, meta, XL, R, out_features, Y=None):
         return _done(out)
     T, in_ = _rows(Xq, torch.int8, "Xq")
     dev, _ = place = _place(Xq)
-    ps = _fit(xscale, torch.float32, "xscale", (T,), dev)
+    xscale, ps = _vector(xscale, "xscale", (T,), dev)
     pv = _fit(vals_q, torch.int8, "vals_q", (out_features, in_ // 2), dev)
-    pws = _fit(wscale, torch.float32, "wscale", (out_features,), dev)
+    wscale, pws = _vector(wscale, "wscale", (out_features,), dev)
     pm = _fit(meta, torch.int16, "meta", (out_features, in_ // 16), dev)
     r, px, pr = 0, None, None
     if R is not None:

@@ -26,7 +26,8 @@ workload instead.  `--fwd-sweep` times inference
 per token count, against HBM bandwidth; with `--int8` the int8 path instead:
 the norm with the residual's addition and its int8 and bf16 outputs (or the
 quantiser, where no norm precedes), the adapter's down-projection, and the
-int8 product, per layer.
+int8 product, per layer.  (The root-mean-square norm stands in for these
+models' layer norm, which the library does not have.)
 """
 import argparse
 import json

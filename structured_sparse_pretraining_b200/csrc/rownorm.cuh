@@ -18,9 +18,12 @@
 //   dh = rstd (g - n mean(g n)) (+ the gradient arriving along the residual),
 //   dw = sum over tokens of dY n.
 //
-// All of it is bound by HBM: each row is read once, held in registers as
-// bf16 while its statistics are reduced, and written once.  A row is one
-// warp's up to 1024 values and one CTA's above, NV 16-byte chunks to a thread.
+// A row is read once, held in registers as bf16 while its statistics are
+// reduced, and written once (but for the gradients of few rows, which read dY
+// and H twice, and far_row): HBM bounds it at many rows, except the int8 output
+// without a residual, which the instructions per value bound, and a launch's
+// latency at few.  A row is one warp's up to 1024 values and one CTA's above,
+// NV 16-byte chunks to a thread.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>

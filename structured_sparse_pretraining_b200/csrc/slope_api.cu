@@ -1705,7 +1705,8 @@ int row_launch(const slope::RowParams &p, int sms, cudaStream_t st, const char *
 // The gradients' form: one launch up to BWD_ONCE_ROWS rows (and for rows too
 // long for a ring), else rings and a second launch for dw, with `parts` rows of
 // partial sums (the rings' CTAs; the scratch query has no device, so 148 SMs
-// are taken).
+// are taken).  The border was measured at rows of about 1000 values; the rows
+// without a ring are those above 18432.
 constexpr int64_t BWD_ONCE_ROWS = 1024;
 struct BwdPlan {
     RowPlan row;

@@ -219,12 +219,12 @@ __device__ __forceinline__ float scaled_squares(uint4 h, float f, float s2) {
 // in range: products of bf16 numbers start at 2^-266.
 // Y takes the products' low bits only where rstd is large enough to bring them
 // back above bf16's own smallest values (last place 2^-133): above FAR_RSTD
-// y = h w rstd is taken in binary64 as well.  So it is in a row with a product
-// that is not finite in binary32: y may be.
+// y = h w rstd, where it is asked for, is taken in binary64 as well.  So it is in
+// a row with a product that is not finite in binary32: y may be.
 constexpr float FAR_MAX = 0x1p-110f, FAR_RSTD = 0x1p14f;
-__device__ __forceinline__ bool far_candidate(uint32_t mx, float rstd) {  // mx: the largest |p| as a float's bits
+__device__ __forceinline__ bool far_candidate(const RowParams &p, uint32_t mx, float rstd) {  // mx: the largest |p| as a float's bits
     const uint32_t least = __float_as_uint(FAR_MAX);
-    return mx - least >= kInfBits - least || rstd > FAR_RSTD;
+    return mx - least >= kInfBits - least || (rstd > FAR_RSTD && p.Y);
 }
 __device__ __forceinline__ float2 far_products(uint32_t h, uint32_t w) {
     const float2 x = bf16x2_to_float2(h), y = bf16x2_to_float2(w);
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(WARP ? 32 * ROW_WARPS : 1024) row_kernel(const
         }
         if (p.rstd && gi == 0 && in_bounds(row, 1, p.T)) p.rstd[row] = rstd;
     }
-    if (NORM && far_candidate(mx, rstd)) {
+    if (NORM && far_candidate(p, mx, rstd)) {
         bool far = true;
         if (mx < __float_as_uint(FAR_MAX)) {  // not for a row of zeros; in a CTA every thread has read the maxima, then
             bool any = false;
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(stream_threads(NV, NORM, false), stream_ctas(N
             fetch(row + STREAM_STAGES * step, s);
             if (NORM && p.rstd && in_bounds(row, 1, p.T)) p.rstd[row] = rstd;
         }
-        bool far = NORM && far_candidate(mx, rstd);
+        bool far = NORM && far_candidate(p, mx, rstd);
         if (far && mx < __float_as_uint(FAR_MAX)) {  // see row_kernel
             bool any = false;
 #pragma unroll

@@ -13,8 +13,13 @@ SRC = os.path.join(HERE, "csrc", "slope_api.cu")
 LIB = os.path.join(HERE, "libslope.so")
 LIB_DEBUG = os.path.join(HERE, "libslope_debug.so")
 CALLS = os.path.join(HERE, "_calls.so")
-DEPS = [os.path.join(HERE, "csrc", f) for f in os.listdir(os.path.join(HERE, "csrc"))] + [
-    os.path.join(ROOT, "include", "slope.h")]
+
+
+def deps():
+    """What the library is built from."""
+    csrc = os.path.join(HERE, "csrc")
+    return [os.path.join(csrc, f) for f in os.listdir(csrc)] + [os.path.join(ROOT, "include", "slope.h")]
+
 
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-v"]
@@ -27,7 +32,7 @@ def nvcc():
 
 def _build_one(lib: str, extra, force: bool, verbose: bool) -> str:
     if not force and os.path.exists(lib):
-        newest = max(os.path.getmtime(d) for d in DEPS)
+        newest = max(os.path.getmtime(d) for d in deps())
         if os.path.getmtime(lib) >= newest:
             return lib
     cmd = [nvcc()] + NVCC_FLAGS + list(extra) + ["-o", lib, SRC]

@@ -350,17 +350,33 @@ def _vector(t, name, shape, dev):
 
 def _vector_out(t, name, shape, like, place, back):
     """(vector, pointer) of an fp32 output; where the given one does not start on 16 bytes the pointer is that of a new
-    one, and `back` takes the two for _write_back."""
+    one, and `back` takes the name and the two for _write_back."""
     t, p = _out(t, torch.float32, name, shape, like, place)
     if p % 16:
         new = torch.empty_like(t)
-        back.append((t, new))
+        back.append((name, t, new))
         p = new.data_ptr()
     return t, p
 
 
+def _span(t):
+    return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+
+
+def _check_back(back, call, **tensors):
+    """Refuse what the entry point cannot see behind the copies: a vector of `back` that overlaps another buffer."""
+    for name, t, _ in back:
+        a, b = _span(t)
+        for other, o in tensors.items():
+            if o is None or other == name:
+                continue
+            c, d = _span(o)
+            if a < d and c < b:
+                raise ValueError(f"{call}: {name} overlaps {other}")
+
+
 def _write_back(back):
-    for t, new in back:
+    for _, t, new in back:
         t.copy_(new)
 
 
@@ -416,6 +432,8 @@ def _rmsnorm(X, w, eps, res, with_y, with_q8, with_rstd, H, Y, Q, qscale, rstd):
         qscale, ps = _vector_out(qscale, "qscale", (T,), X, place, back)
     if with_rstd or rstd is not None:
         rstd, pr = _vector_out(rstd, "rstd", (T,), X, place, back)
+    _check_back(back, "rmsnorm", X=X, res=res, w=w, H=H if res is not None else None, Y=Y if with_y else None,
+                Q=Q if with_q8 else None, qscale=qscale if with_q8 else None, rstd=rstd)
     _call_on(place, "slope_rmsnorm", X.data_ptr(), pe, pw, T, D, eps, ph, py, pq, ps, pr)
     _write_back(back)
     return Q, qscale, Y, H, rstd
@@ -432,11 +450,12 @@ def rmsnorm_bwd(dY, H, w, rstd, dres=None, dH=None, dw=None):
     dev, _ = place = _place(dY)
     ph = _fit(H, torch.bfloat16, "H", shape, dev)
     pw = _fit(w, torch.bfloat16, "w", (D,), dev)
-    rstd, pr = _vector(rstd, "rstd", (T,), dev)
+    aligned, pr = _vector(rstd, "rstd", (T,), dev)  # (held until the call)
     pe = None if dres is None else _fit(dres, torch.bfloat16, "dres", shape, dev)
     dH, pdh = _out(dH, torch.bfloat16, "dH", shape, dY, place)
     back = []
     dw, pdw = _vector_out(dw, "dw", (D,), dY, place, back)
+    _check_back(back, "rmsnorm_bwd", dY=dY, H=H, w=w, rstd=rstd, dres=dres, dH=dH, dw=dw)
     floats = _norm_bwd_floats(T, D)
     ws, pws = _out(None, torch.float32, "ws", (floats,), dY, place) if floats else (None, None)
     _call_on(place, "slope_rmsnorm_bwd", dY.data_ptr(), ph, pw, pr, pe, T, D, pdh, pdw, pws, floats)
@@ -455,6 +474,7 @@ def quant_rows(A, Q=None, scale=None):
     Q, pq = _out(Q, torch.int8, "Q", shape, A, place)
     back = []
     scale, ps = _vector_out(scale, "scale", (rows,), A, place, back)
+    _check_back(back, "quant_rows", A=A, Q=Q, scale=scale)
     _call_on(place, "slope_quant_rows", A.data_ptr(), rows, K, pq, ps)
     _write_back(back)
     return Q, scale

@@ -61,3 +61,21 @@ def test_captured():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(Q, want[0]) and torch.equal(s[3:], want[1])
+
+
+def test_overlaps_are_refused_there_too():
+    X, e, w = P.random_bf16((9, 256), 1.0, 1), P.random_bf16((9, 256), 2.0, 2), P.random_bf16((256,), 1.0, 3)
+    s = torch.zeros(40, device="cuda")
+    with pytest.raises(ValueError, match="qscale overlaps rstd"):
+        ops.rmsnorm_q8(X, w, EPS, qscale=s[1:10], rstd=s[5:14])
+    with pytest.raises(ValueError, match="qscale overlaps rstd"):
+        v = s[1:10]
+        ops.rmsnorm_q8(X, w, EPS, qscale=v, rstd=v)
+    with pytest.raises(ValueError, match="scale overlaps A"):
+        ops.quant_rows(X, scale=X.view(torch.float32).view(-1)[1:10])
+    rstd = torch.ones(400, device="cuda")
+    with pytest.raises(ValueError, match="dw overlaps rstd"):
+        ops.rmsnorm_bwd(e, X, w, rstd[1:10], dw=rstd[7:263])
+    assert not s.any() and (rstd == 1).all()
+    ops.rmsnorm_q8(X, w, EPS, qscale=s[1:10], rstd=s[10:19])
+    assert s[1:19].all() and not s[0] and not s[19:].any()

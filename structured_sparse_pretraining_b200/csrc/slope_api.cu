@@ -1903,12 +1903,17 @@ struct Q8Plan {
 //  * 512 x 224 tiles: 0.82 us a k-tile of a round, about 3.7 us for its drain,
 //    and 7 us (9216 -> 9216 at 8192 tokens: 296 us against 363 with 256 x 256
 //    tiles; at 2048 tokens, where they fill 2.4 rounds, 102 against 85).
+//  * Both with codes that TMA cannot address (K an odd multiple of 64): a k-tile
+//    takes 1.2 to 1.3 us once the ring has filled, while the 128 x bn tiles lose
+//    little (300 tokens: 27200 -> 5824 64 us with 128 x 128, 142 and 139; 9152
+//    -> 27648 118, 147 and 107; 4160 -> 9216 22, 26 and 29).
 //  * CUDA cores, up to 4 tokens: 3 us, and 0.3 us for each megabyte of weights,
 //    a third as much again for each further token (1024 -> 4096 at one token
 //    4.3 us against the tiles' 5.3, 4096 -> 4096 5.7 against 8.3; 9216 -> 27648
 //    37 against 32).
 Q8Plan pick_q8_plan(int64_t M, int64_t T, int64_t K, int64_t r, int sms) {
     const int64_t kts = (K + 255) / 256, adp = (r + 63) / 64;
+    const bool codes_tma = K % 128 == 0;
     Q8Plan best{0, 1, 0, false};
     double best_us = 1e300;
     const int bns[4] = {16, 32, 64, 128};
@@ -1935,13 +1940,15 @@ Q8Plan pick_q8_plan(int64_t M, int64_t T, int64_t K, int64_t r, int sms) {
     const int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
     if (T > 64 && M >= 128) {
         const int64_t tiles = (M + 255) / 256 * ((T + 255) / 256);
-        const double t = 6.0 + (double)((tiles + pairs - 1) / pairs) * ((double)(kts + adp) + 3.5) * 0.55;
+        const double by_tma = ((double)(kts + adp) + 3.5) * 0.55, by_warps = 1.3 * (double)kts - 3.0 + 0.55 * (double)adp;
+        const double t = 6.0 + (double)((tiles + pairs - 1) / pairs) * (codes_tma || by_tma > by_warps ? by_tma : by_warps);
         if (t < best_us) {
             best_us = t;
             best = Q8Plan{256, 1, 0, false};
         }
         const int64_t wide_tiles = (M + 511) / 512 * ((T + 223) / 224);
-        const double t_wide = 7.0 + (double)((wide_tiles + pairs - 1) / pairs) * ((double)kts + 4.5) * 0.82;
+        const double wide_tma = ((double)kts + 4.5) * 0.82, wide_warps = 1.2 * (double)kts + 0.8;
+        const double t_wide = 7.0 + (double)((wide_tiles + pairs - 1) / pairs) * (codes_tma || wide_tma > wide_warps ? wide_tma : wide_warps);
         if (t_wide < best_us) {
             best_us = t_wide;
             best = Q8Plan{224, 1, 0, true};

@@ -53,7 +53,7 @@ def test_the_helpers_name_the_cluster():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T,K,M,form", [(300, 4160, 9216, 256), (512, 4160, 5120, 256), (3300, 832, 1984, 512), (2222, 5824, 2880, 512)])
+@pytest.mark.parametrize("T,K,M,form", [(1024, 1984, 4160, 256), (4000, 1472, 2752, 256), (3300, 832, 1984, 512), (2222, 5824, 2880, 512)])
 def test_codes_without_tma_change_from_call_to_call(T, K, M, form):
     """K an odd multiple of 64 in the pair forms: stages that held other codes a moment before."""
     import q8_plain as P
